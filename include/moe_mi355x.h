@@ -77,7 +77,9 @@ typedef enum {
 typedef enum {
   MOE_F32 = 0,             /* IEEE binary32                                     */
   MOE_BF16 = 1,            /* bfloat16                                          */
-  MOE_FP8_E4M3FN = 2       /* OCP E4M3FN codes (uint8) with fp32 block scales   */
+  MOE_FP8_E4M3FN = 2,      /* OCP E4M3FN codes (uint8) with fp32 block scales   */
+  MOE_MXFP4 = 3            /* OCP MXFP4: E2M1 codes, two a byte, with one E8M0
+                              scale byte per 32 values along K                  */
 } moe_dtype;
 
 /* Problem description.  Supported combinations:
@@ -87,6 +89,8 @@ typedef enum {
  *       shared expert and shared gate stay bf16 -- "Qwen3.8, weights in hand",
  *       section "What FP8 actually quantizes"); scale_block must be 128 and
  *       H, I multiples of 128.
+ *   act_dtype BF16 with w_dtype MXFP4 (routed experts only, as fp8);
+ *       scale_block must be 32 and H, I multiples of 32.
  * Limits: 1 <= E <= 1024, 1 <= k <= min(E, 64), H and I multiples of 8 (bf16)
  * or of 4 (f32), I_shared 0 or a multiple of 8; T*k < 2^31; the tensors the
  * kernels address with 32-bit element offsets below 2^31 elements (T*H,
@@ -102,7 +106,7 @@ typedef struct {
   int64_t I_shared;   /* shared expert intermediate width; 0 = no shared expert */
   int32_t act_dtype;  /* moe_dtype of x, router, shared expert, y, out         */
   int32_t w_dtype;    /* moe_dtype of routed expert matrices                   */
-  int32_t scale_block;/* fp8 scale block edge (128), else ignored              */
+  int32_t scale_block;/* fp8 scale block edge (128), MXFP4 group (32), else ignored */
   uint32_t flags;     /* MOE_FLAG_* (0 = default)                              */
 } moe_problem;
 
@@ -136,7 +140,12 @@ typedef struct {
  *             stride 0 means dense (I*H).  A fused [E, 2I, H] gate_up tensor
  *             is passed as w_gate = base, w_up = base + I*H, strides 2*I*H.
  *   s_gate/s_up [E, I/128, H/128] fp32, s_down [E, H/128, I/128] fp32:
- *             fp8 block scales (value = code * scale); NULL unless fp8.
+ *             fp8 block scales (value = code * scale); NULL unless fp8 or MXFP4.
+ *   MXFP4: the matrices hold E2M1 codes, the even k of a pair in the low four
+ *             bits: [E][I, H/2] bytes ([E][H, I/2] for w_down), strides still
+ *             counted in values (multiples of 32); s_gate/s_up [E, I, H/32]
+ *             and s_down [E, H, I/32] are E8M0 bytes: value = code * 2^(s - 127),
+ *             s = 255 is NaN.  moe_mx_quantize writes both.
  *   sh_gate, sh_up [I_shared, H], sh_down [H, I_shared], sh_gate_w [1, H]:
  *             shared expert and its gate projection, act dtype; NULL iff
  *             I_shared == 0.                                                 */
@@ -148,9 +157,9 @@ typedef struct {
   int64_t stride_gate;
   int64_t stride_up;
   int64_t stride_down;
-  const float* s_gate;
-  const float* s_up;
-  const float* s_down;
+  const void* s_gate; /* fp32 (fp8 weights) or E8M0 bytes (MXFP4) */
+  const void* s_up;
+  const void* s_down;
   const void* sh_gate;
   const void* sh_up;
   const void* sh_down;
@@ -341,6 +350,36 @@ size_t moe_audit_workspace_bytes(int64_t slices);
  * statistics).  Errors are reported before any launch. */
 moe_status moe_weight_audit(const void* w, int32_t dtype, int64_t slices, int64_t n, int64_t slice_stride,
                             moe_audit_stats* stats, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * MXFP4 weights (the 4-bit OCP microscaling format) of the routed experts:
+ * groups of 32 consecutive values of a row share one E8M0 scale 2^(s - 127),
+ * each value is an E2M1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign).
+ *   s     = max(floor(log2(amax)) - 2, -127) + 127   (amax: the group's largest |w|)
+ *   code  = w / 2^(s - 127) rounded to the nearest code, ties to the even one,
+ *           larger values to 6; the sign is kept (also of zeros)
+ * A group with an infinity or a NaN gets s = 255, so it reads back as NaN; an
+ * all-zero group gets s = 0.
+ * --------------------------------------------------------------------------- */
+
+/* w: rows of K values at w + r * row_stride (elements), dtype MOE_BF16 or
+ * MOE_F32 (MOE_ERR_DTYPE otherwise) -> codes [rows, K/2] bytes and scales
+ * [rows, K/32] bytes, both dense, in the layout that moe_weights takes (an
+ * [E, I, H] tensor is rows = E*I, K = H).  K a multiple of 32
+ * (MOE_ERR_UNSUPPORTED otherwise), row_stride >= K; rows 0 is a no-op;
+ * rows * K < 2^42 and row_stride < 2^31 (MOE_ERR_SHAPE).  w and codes 16-byte
+ * aligned and row_stride a multiple of 16 bytes (MOE_ERR_ALIGN).  The outputs
+ * must not overlap w.  Errors are reported before any launch. */
+moe_status moe_mx_quantize(const void* w, int32_t dtype, int64_t rows, int64_t K, int64_t row_stride, void* codes,
+                           void* scales, void* stream);
+
+/* The values as bf16: w [r * row_stride + k] = code * 2^(s - 127).  Exact for
+ * every code and scale (a value below bf16's smallest normal number, possible
+ * for s < 2 only, may become zero; 4 and 6 times 2^126 and 2 to 6 times 2^127
+ * become infinite).  Sizes, alignment and errors as moe_mx_quantize; values
+ * between the rows (row_stride > K) are left as they were. */
+moe_status moe_mx_dequantize(const void* codes, const void* scales, int64_t rows, int64_t K, void* w,
+                             int64_t row_stride, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Measurement helper (not a step of the layer): reads `bytes` of device

@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import moe
+from . import moe, mx
 
 
 def _dec(problem, t, dt):
@@ -37,6 +37,10 @@ def expert_weights_fn(problem):
         if c.wdt == "fp8":
             b = c.scale_block
             return tuple(moe.dequant_blocks(problem.host_raw(w[e]), problem.host_raw(s[e]), b)
+                         for w, s in ((problem.w_gate, problem.s_gate), (problem.w_up, problem.s_up),
+                                      (problem.w_down, problem.s_down)))
+        if c.wdt == "mxfp4":
+            return tuple(mx.dequant(problem.host_raw(w[e]), problem.host_raw(s[e]))
                          for w, s in ((problem.w_gate, problem.s_gate), (problem.w_up, problem.s_up),
                                       (problem.w_down, problem.s_down)))
         return tuple(moe.decode(problem.host_raw(w[e]), c.wdt)

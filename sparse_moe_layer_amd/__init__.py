@@ -14,10 +14,10 @@ import torch
 
 from ._lib import (LIB, MOE_BF16, MOE_F32, MOE_FLAG_FORCE_GEMM, MOE_FLAG_FORCE_STREAM,  # noqa: F401
                    MOE_FLAG_GEMM_TILE_128, MOE_FLAG_GEMM_TILE_256, MOE_FLAG_PAGE_ROUTING, MOE_FP8_E4M3FN,
-                   MOE_NOALLOC_SCRATCH_BYTES, MOE_OK, EXPORTS, moe_audit_stats, moe_gr_weights, moe_problem,
+                   MOE_MXFP4, MOE_NOALLOC_SCRATCH_BYTES, MOE_OK, EXPORTS, moe_audit_stats, moe_gr_weights, moe_problem,
                    moe_weights)
 
-_DT = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8": MOE_FP8_E4M3FN}
+_DT = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8": MOE_FP8_E4M3FN, "mxfp4": MOE_MXFP4}
 
 
 class MoEError(RuntimeError):
@@ -198,6 +198,53 @@ def audit_records(stats: torch.Tensor) -> list:
             for i in range(host.shape[0])]
 
 
+def _mx_shape(values, codes, scales, where: str):
+    """(rows, K, row stride) of a matrix of values [.., K] (the last dimension contiguous, the ones before it one
+    run of rows) with packed codes [.., K/2] and scales [.., K/32]."""
+    K = values.shape[-1]
+    lead = tuple(values.shape[:-1])
+    if tuple(codes.shape) != (*lead, K // 2) or tuple(scales.shape) != (*lead, K // 32) or K % 32 or K < 32:
+        raise ValueError(f"{where}: codes must be [.., K/2] and scales [.., K/32] for values [.., K], K a multiple of 32")
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise ValueError(f"{where}: codes and scales are uint8 tensors")
+    if not (values.device == codes.device == scales.device):
+        raise ValueError(f"{where}: tensors on different devices")
+    rows = codes.numel() // (K // 2)
+    if values.is_contiguous():
+        return rows, K, K
+    if values.dim() != 2 or values.stride(1) != 1 or values.stride(0) < K:
+        raise ValueError(f"{where}: values must be contiguous, or 2-D with contiguous rows")
+    return rows, K, values.stride(0)
+
+
+def moe_mx_quantize(w, codes, scales, stream=None):
+    """w [.., K] (bf16 or fp32) -> MXFP4 codes [.., K/2] and E8M0 scales [.., K/32] (uint8)."""
+    if w.dtype not in (torch.bfloat16, torch.float32):
+        raise MoEError(3, "moe_mx_quantize")  # 3: MOE_ERR_DTYPE
+    rows, K, stride = _mx_shape(w, codes, scales, "moe_mx_quantize")
+    _check(LIB.moe_mx_quantize(w.data_ptr(), MOE_F32 if w.dtype == torch.float32 else MOE_BF16, rows, K, stride,
+                               _ptr(codes), _ptr(scales), _stream(stream)), "moe_mx_quantize")
+
+
+def moe_mx_dequantize(codes, scales, w, stream=None):
+    """MXFP4 codes [.., K/2] and scales [.., K/32] -> their values, w [.., K] bf16."""
+    if w.dtype != torch.bfloat16:
+        raise MoEError(3, "moe_mx_dequantize")  # 3: MOE_ERR_DTYPE
+    rows, K, stride = _mx_shape(w, codes, scales, "moe_mx_dequantize")
+    _check(LIB.moe_mx_dequantize(_ptr(codes), _ptr(scales), rows, K, w.data_ptr(), stride, _stream(stream)),
+           "moe_mx_dequantize")
+
+
+def mx_quantize(w, stream=None):
+    """MXFP4 form of a weight tensor [.., K]: (codes [.., K/2], scales [.., K/32]), uint8, on w's device."""
+    if w.shape[-1] % 32 or w.shape[-1] < 32:
+        raise MoEError(6, "moe_mx_quantize")  # 6: MOE_ERR_UNSUPPORTED
+    codes = torch.empty((*w.shape[:-1], w.shape[-1] // 2), dtype=torch.uint8, device=w.device)
+    scales = torch.empty((*w.shape[:-1], w.shape[-1] // 32), dtype=torch.uint8, device=w.device)
+    moe_mx_quantize(w, codes, scales, stream)
+    return codes, scales
+
+
 _DT_OF_TORCH = {torch.float32: "f32", torch.bfloat16: "bf16", torch.uint8: "fp8"}
 
 
@@ -206,15 +253,15 @@ def layer_forward(x, k: int, w_router, w_gate, w_up, w_down, s_gate=None, s_up=N
     """The whole layer in one call: returns (out [T, H], ids [T, k] int32, w [T, k] fp32).
 
     Shapes come from the tensors: x [T, H] (bf16 or fp32), w_router [E, H], w_gate / w_up [E, I, H],
-    w_down [E, H, I] (bf16, fp32, or uint8 e4m3fn codes with fp32 128 x 128 block scales s_*), and
-    the optional shared expert sh_gate / sh_up [I_s, H], sh_down [H, I_s], sh_gate_w [1, H].
+    w_down [E, H, I] (bf16, fp32, or uint8 e4m3fn codes with fp32 128 x 128 block scales s_*; or
+    MXFP4: uint8 codes [E, I, H/2], [E, H, I/2] with uint8 scales s_*, as mx_quantize makes them), and the optional shared expert sh_gate / sh_up [I_s, H], sh_down [H, I_s], sh_gate_w [1, H].
     Outputs and the workspace are allocated on x's device; every computation runs in the library.
     """
     T, H = x.shape
     E, I = w_gate.shape[0], w_gate.shape[1]
     Is = sh_gate.shape[0] if sh_gate is not None else 0
-    wdt = _DT_OF_TORCH[w_gate.dtype]
-    P = problem(T, H, E, k, I, Is, _DT_OF_TORCH[x.dtype], wdt, 128, flags)
+    wdt = "mxfp4" if s_gate is not None and s_gate.dtype == torch.uint8 else _DT_OF_TORCH[w_gate.dtype]
+    P = problem(T, H, E, k, I, Is, _DT_OF_TORCH[x.dtype], wdt, 32 if wdt == "mxfp4" else 128, flags)
     W = weights(w_router, w_gate, w_up, w_down, s_gate, s_up, s_down, sh_gate, sh_up, sh_down, sh_gate_w)
     ws = workspace(P, device=x.device)
     out = torch.empty((T, H), dtype=x.dtype, device=x.device)

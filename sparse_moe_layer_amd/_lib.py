@@ -16,7 +16,7 @@ LIB_PATH = os.environ.get("MOE_MI355X_LIB") or os.path.join(_HERE, "libmoe_mi355
 
 MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, \
     MOE_ERR_UNSUPPORTED, MOE_ERR_HIP = range(8)
-MOE_F32, MOE_BF16, MOE_FP8_E4M3FN = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_FP8_E4M3FN, MOE_MXFP4 = 0, 1, 2, 3
 MOE_FLAG_FORCE_GEMM = 1
 MOE_FLAG_FORCE_STREAM = 2
 MOE_FLAG_GEMM_TILE_128 = 4
@@ -28,7 +28,7 @@ EXPORTS = ["moe_abi_version", "moe_status_str", "moe_validate", "moe_workspace_b
            "moe_dispatch", "moe_expert_ffn", "moe_expert_gate_up", "moe_expert_down", "moe_combine",
            "moe_layer_forward", "moe_gr_workspace_bytes", "moe_gr_read", "moe_gr_write", "moe_combine_gr_write",
            "moe_audit_workspace_bytes", "moe_weight_audit", "moe_layer_forward_noalloc",
-           "moe_hbm_read_probe", "moe_mfma_pipe_probe"]
+           "moe_hbm_read_probe", "moe_mfma_pipe_probe", "moe_mx_quantize", "moe_mx_dequantize"]
 
 
 class moe_problem(ctypes.Structure):
@@ -78,6 +78,8 @@ def _load():
         "moe_layer_forward_noalloc": (i32, [P, W, vp, vp, vp, vp, vp]),
         "moe_hbm_read_probe": (i32, [vp, sz, vp, vp]),
         "moe_mfma_pipe_probe": (i32, [ctypes.c_int32, ctypes.c_int32, vp, sz, vp, vp]),
+        "moe_mx_quantize": (i32, [vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, vp, vp, vp]),
+        "moe_mx_dequantize": (i32, [vp, vp, ctypes.c_int64, ctypes.c_int64, vp, ctypes.c_int64, vp]),
         "moe_gr_workspace_bytes": (sz, [P, ctypes.c_int64]),
         "moe_gr_read": (i32, [P, G, vp, vp, vp, vp, sz, vp]),
         "moe_gr_write": (i32, [P, vp, vp, vp, vp, vp]),

@@ -23,6 +23,10 @@ size_t act_bytes(const moe_problem* p) { return p->act_dtype == MOE_F32 ? 4 : 2;
 size_t w_bytes(const moe_problem* p) {
   return p->w_dtype == MOE_F32 ? 4 : (p->w_dtype == MOE_BF16 ? 2 : 1);
 }
+// bytes of n stored weights (MXFP4: two codes a byte; strides are multiples of 32 there)
+int64_t stored_bytes(const moe_problem* p, int64_t n) {
+  return p->w_dtype == MOE_MXFP4 ? n / 2 : n * (int64_t)w_bytes(p);
+}
 
 // ---------------------------------------------------------------------------
 // router form: fp32 SIMT (fp32 layers), split-K weight streaming (T <= 16, the
@@ -120,10 +124,12 @@ moe_status check_problem(const moe_problem* p) {
   const bool f32 = p->act_dtype == MOE_F32 && p->w_dtype == MOE_F32;
   const bool bf = p->act_dtype == MOE_BF16 && p->w_dtype == MOE_BF16;
   const bool fp8 = p->act_dtype == MOE_BF16 && p->w_dtype == MOE_FP8_E4M3FN;
-  if (!f32 && !bf && !fp8) return MOE_ERR_DTYPE;
+  const bool mx = p->act_dtype == MOE_BF16 && p->w_dtype == MOE_MXFP4;
+  if (!f32 && !bf && !fp8 && !mx) return MOE_ERR_DTYPE;
   const int64_t q = f32 ? 4 : 8;  // 16-byte vectors along every K-contiguous row
   if (p->H % q || p->I % q || p->I_shared % q) return MOE_ERR_UNSUPPORTED;
   if (fp8 && (p->scale_block != 128 || p->H % 128 || p->I % 128)) return MOE_ERR_UNSUPPORTED;
+  if (mx && (p->scale_block != 32 || p->H % 32 || p->I % 32)) return MOE_ERR_UNSUPPORTED;
   const uint32_t known = MOE_FLAG_FORCE_GEMM | MOE_FLAG_FORCE_STREAM | MOE_FLAG_GEMM_TILE_128 | MOE_FLAG_GEMM_TILE_256 |
                          MOE_FLAG_PAGE_ROUTING;
   if (p->flags & ~known) return MOE_ERR_UNSUPPORTED;
@@ -147,9 +153,12 @@ moe_status check_weights(const moe_problem* p, const moe_weights* w, bool need_r
     if (!w->w_gate || !w->w_up || !w->w_down) return MOE_ERR_NULL;
     if (!al16(w->w_gate) || !al16(w->w_up) || !al16(w->w_down)) return MOE_ERR_ALIGN;
     if (w->stride_gate < 0 || w->stride_up < 0 || w->stride_down < 0) return MOE_ERR_SHAPE;
-    const int64_t wb = (int64_t)w_bytes(p);
-    if ((w->stride_gate * wb) % 16 || (w->stride_up * wb) % 16 || (w->stride_down * wb) % 16) return MOE_ERR_ALIGN;
-    if (p->w_dtype == MOE_FP8_E4M3FN) {
+    if (p->w_dtype == MOE_MXFP4 && (w->stride_gate % 32 || w->stride_up % 32 || w->stride_down % 32))
+      return MOE_ERR_ALIGN;
+    if (stored_bytes(p, w->stride_gate) % 16 || stored_bytes(p, w->stride_up) % 16 ||
+        stored_bytes(p, w->stride_down) % 16)
+      return MOE_ERR_ALIGN;
+    if (p->w_dtype == MOE_FP8_E4M3FN || p->w_dtype == MOE_MXFP4) {
       if (!w->s_gate || !w->s_up || !w->s_down) return MOE_ERR_NULL;
       if (!al16(w->s_gate) || !al16(w->s_up) || !al16(w->s_down)) return MOE_ERR_ALIGN;
     }
@@ -219,7 +228,7 @@ FfnArgs ffn_args(const moe_problem* p, const moe_weights* w, const void* x, cons
   a.k = (int)p->k;
   a.I = (int)p->I;
   a.Is = (p->I_shared > 0 && shared) ? (int)p->I_shared : 0;
-  a.fp8 = p->w_dtype == MOE_FP8_E4M3FN;
+  a.wt = p->w_dtype == MOE_FP8_E4M3FN ? moe::kWtFp8 : p->w_dtype == MOE_MXFP4 ? moe::kWtMx : moe::kWtPlain;
   a.x = x;
   a.offsets = offsets;
   a.sorted = sorted;
@@ -251,7 +260,7 @@ bool use_big_tiles(const moe_problem* p, const FfnArgs& a) {
   // (the 128-row fp8 tiles decode every weight once per m-tile; on the
   // skewed 2.4T layer at 40 rows per expert the 256-row tiles of its large
   // groups measured faster).
-  return p->T * p->k >= (a.fp8 ? 32 : 128) * p->E;
+  return p->T * p->k >= (a.wt == moe::kWtFp8 ? 32 : 128) * p->E;
 }
 
 // A second stream per device (default priority) and two events, so that
@@ -593,6 +602,35 @@ moe_status moe_combine_gr_write(const moe_problem* p, const void* y, const int32
     return MOE_ERR_ALIGN;
   return hip_status(moe::launch_combine_gr_write(y, assign_pos, topk_w, y_shared, shared_logit, out, resid, s,
                                                  resid_out, (int)p->T, (int)p->H, (int)p->k, (hipStream_t)stream));
+}
+
+static moe_status check_mx(int64_t rows, int64_t K, int64_t row_stride, int64_t elem_bytes) {
+  if (rows < 0 || K < 1 || row_stride < K || row_stride >= ((int64_t)1 << 31) ||
+      rows >= ((int64_t)1 << 42) || (rows > 0 && K > ((int64_t)1 << 42) / rows))
+    return MOE_ERR_SHAPE;
+  if (K % 32) return MOE_ERR_UNSUPPORTED;
+  if ((row_stride * elem_bytes) % 16) return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+
+moe_status moe_mx_quantize(const void* w, int32_t dtype, int64_t rows, int64_t K, int64_t row_stride, void* codes,
+                           void* scales, void* stream) {
+  if (dtype != MOE_BF16 && dtype != MOE_F32) return MOE_ERR_DTYPE;
+  const moe_status st = check_mx(rows, K, row_stride, dtype == MOE_F32 ? 4 : 2);
+  if (st != MOE_OK || rows == 0) return st;
+  if (!w || !codes || !scales) return MOE_ERR_NULL;
+  if (!al16(w) || !al16(codes)) return MOE_ERR_ALIGN;
+  return hip_status(moe::launch_mx_quantize(w, dtype == MOE_F32, rows, K, row_stride, codes, scales,
+                                            (hipStream_t)stream));
+}
+
+moe_status moe_mx_dequantize(const void* codes, const void* scales, int64_t rows, int64_t K, void* w,
+                             int64_t row_stride, void* stream) {
+  const moe_status st = check_mx(rows, K, row_stride, 2);
+  if (st != MOE_OK || rows == 0) return st;
+  if (!w || !codes || !scales) return MOE_ERR_NULL;
+  if (!al16(w) || !al16(codes)) return MOE_ERR_ALIGN;
+  return hip_status(moe::launch_mx_dequantize(codes, scales, rows, K, w, row_stride, (hipStream_t)stream));
 }
 
 size_t moe_audit_workspace_bytes(int64_t slices) {

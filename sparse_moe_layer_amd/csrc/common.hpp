@@ -69,6 +69,21 @@ __device__ __forceinline__ u32x4 fp8x8_to_bf16x8_exact(u32x2 codes) {
   return out;
 }
 
+// The fp32 whose exponent field is an E8M0 byte: the scale 2^(s - 127) of an
+// MXFP4 group (s = 0 gives the field 0, which the scaled conversion below
+// takes as 2^-127; s = 255 gives an infinity, which it takes as NaN).
+__device__ __forceinline__ float e8m0(uint32_t s) { return __uint_as_float(s << 23); }
+
+// Eight E2M1 codes (a dword, the even value of each pair in the low four bits)
+// times a power-of-two scale -> eight bf16, exactly (two significant bits and
+// bf16's own exponent range): one scaled conversion per two codes.
+__device__ __forceinline__ u32x4 mx8_to_bf16x8(uint32_t codes, float scale) {
+  return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3))};
+}
+
 // Wave-wide reductions (64 lanes).
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll

@@ -35,17 +35,24 @@ enum PlanPos : int {
 // An expert with at most this many rows streams its weights (small-M path).
 constexpr int kStreamMaxRows = 16;
 
+// How the routed experts' weights are stored.
+enum WeightKind : int {
+  kWtPlain = 0,  // the activation dtype
+  kWtFp8 = 1,    // e4m3fn codes, fp32 scales of 128 x 128 blocks
+  kWtMx = 2,     // MXFP4: e2m1 codes two a byte, an E8M0 byte per 32 values of a row
+};
+
 // Everything the grouped expert kernels need to resolve a group (routed
 // expert g < E, or the shared expert g == E) and its operands.
 struct FfnArgs {
   int T, H, E, k, I, Is;
-  int fp8;                    // routed weights are e4m3fn codes + fp32 block scales
+  int wt;                     // how the routed weights are stored (WeightKind)
   const void* x;              // [T, H] bf16
   const int32_t* offsets;     // [E+1]
   const int32_t* sorted;      // [R]
-  const void* wg; const void* wu; const void* wd;  // routed, elements: bf16 or u8 codes
+  const void* wg; const void* wu; const void* wd;  // routed, elements: bf16, u8 codes or packed 4-bit codes
   int64_t sg, su, sd;         // expert strides (elements)
-  const float* scg; const float* scu; const float* scd;  // fp8 block scales
+  const void* scg; const void* scu; const void* scd;  // fp8: fp32 block scales; MXFP4: E8M0 bytes
   const void* shg; const void* shu; const void* shd;     // shared expert (bf16) or null
   void* h;                    // [R, I]  bf16 hidden of routed rows
   void* h_sh;                 // [T, Is] bf16 hidden of the shared expert
@@ -148,6 +155,13 @@ hipError_t launch_combine_gr_write(const void* y, const int32_t* pos, const floa
 moe_status layer_forward_checks(const moe_problem* p, const moe_weights* w, const void* x, const void* out);
 moe_status layer_forward_run(const moe_problem* p, const moe_weights* w, const void* x, void* out,
                              int32_t* topk_ids, float* topk_w, void* ws, hipStream_t s, bool fork_ok = true);
+
+// MXFP4 weights: rows of K values (bf16, or fp32 with f32) to codes and E8M0
+// scales, and back to bf16.
+hipError_t launch_mx_quantize(const void* w, bool f32, int64_t rows, int64_t K, int64_t row_stride, void* codes,
+                              void* scales, hipStream_t s);
+hipError_t launch_mx_dequantize(const void* codes, const void* scales, int64_t rows, int64_t K, void* w,
+                                int64_t row_stride, hipStream_t s);
 
 // Gated residual read / write (bf16).
 // Expert-weight audit (bf16): histograms of the bit patterns per slice and

@@ -83,15 +83,15 @@ __device__ __forceinline__ void stream_dot(const bf16* a_row, const bf16* const*
 // number of rows of the experts listed before it: the stable order of the
 // dispatch kernels, in which an expert's rows are its tokens ascending.
 // Wave 0 of workgroup 0 also writes offsets, sorted and pos from the masks.
-template <int PHASE, bool FP8, bool SPLIT = false>
+template <int PHASE, int WT, bool SPLIT = false>
 __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(FfnArgs f, int list_begin_idx, int list_end_idx,
                                                                int self_plan, SmallRoute route) {
-  static_assert(!SPLIT || (PHASE == 1 && !FP8), "split items are bf16 gate/up");
-  constexpr int STAGE_BYTES = item_lds_bytes<FP8, SPLIT>();  // per wave
-  constexpr bool ROUTES = PHASE == 1 && !FP8 && SPLIT;       // may take the dispatch (self_plan == 2)
+  static_assert(!SPLIT || (PHASE == 1 && WT != kWtFp8), "split items are bf16 or MXFP4 gate/up");
+  constexpr int STAGE_BYTES = item_lds_bytes<WT, SPLIT>();         // per wave
+  constexpr bool ROUTES = PHASE == 1 && WT == kWtPlain && SPLIT;  // may take the dispatch (self_plan == 2)
   // the masks and (workgroup 0) the experts' first rows fit wave 0's own stage buffer
   static_assert(!ROUTES || 2 * kMaxExperts * 4 <= STAGE_BYTES, "route scratch in the stage");
-  __shared__ __attribute__((aligned(16))) char stage[WAVES * STAGE_BYTES];
+  __shared__ __attribute__((aligned(16))) char stage[STAGE_BYTES ? WAVES * STAGE_BYTES : 16];
   __shared__ int glist[kMaxExperts + 1];  // SELF_PLAN: touched groups
   __shared__ int wtot[WAVES];
   const int lane = threadIdx.x & 63;
@@ -221,7 +221,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(FfnArgs f, int li
       base = f.sb_base[sb];
       nrows = f.sb_nrows[sb];
     }
-    stream_item<PHASE, FP8, SPLIT>(f, g, r0, base, nrows, self_plan ? nullptr : f.sb_tok + sb * kStreamBM, slab,
+    stream_item<PHASE, WT, SPLIT>(f, g, r0, base, nrows, self_plan ? nullptr : f.sb_tok + sb * kStreamBM, slab,
                                    lane, stage + wave * STAGE_BYTES, mk);
   }
 }
@@ -315,25 +315,31 @@ hipError_t launch_ffn_stream(const FfnArgs& a, int phase, hipStream_t s, bool se
   SmallRoute r{nullptr, nullptr, nullptr, nullptr};
   if (route) {
     // the dispatch from the ids: bf16 gate/up of a small batch listing its own groups
-    if (phase != 1 || a.fp8 || !self_plan || a.T > kSmallBatch || a.E > kMaxExperts || !route->ids ||
+    if (phase != 1 || a.wt != kWtPlain || !self_plan || a.T > kSmallBatch || a.E > kMaxExperts || !route->ids ||
         !route->offsets || !route->sorted || !route->pos)
       return hipErrorInvalidValue;
     r = *route;
     sp = 2;
   }
-  if (a.fp8) {
-    if (phase == 1) stream_kernel<1, true><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
-    else stream_kernel<2, true><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
+  if (a.wt != kWtPlain) {
+    if (a.wt == kWtFp8) {
+      if (phase == 1) stream_kernel<1, kWtFp8><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
+      else stream_kernel<2, kWtFp8><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
+    } else {
+      if (phase == 1 && split) stream_kernel<1, kWtMx, true><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
+      else if (phase == 1) stream_kernel<1, kWtMx><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
+      else stream_kernel<2, kWtMx><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
+    }
     if (a.Is > 0) {
       if (phase == 1 && split)
-        stream_kernel<1, false, true><<<grid, blk, 0, s>>>(a, kPlanRoutedBlocks, kPlanBlocks, sp, r);
-      else if (phase == 1) stream_kernel<1, false><<<grid, blk, 0, s>>>(a, kPlanRoutedBlocks, kPlanBlocks, sp, r);
-      else stream_kernel<2, false><<<grid, blk, 0, s>>>(a, kPlanRoutedBlocks, kPlanBlocks, sp, r);
+        stream_kernel<1, kWtPlain, true><<<grid, blk, 0, s>>>(a, kPlanRoutedBlocks, kPlanBlocks, sp, r);
+      else if (phase == 1) stream_kernel<1, kWtPlain><<<grid, blk, 0, s>>>(a, kPlanRoutedBlocks, kPlanBlocks, sp, r);
+      else stream_kernel<2, kWtPlain><<<grid, blk, 0, s>>>(a, kPlanRoutedBlocks, kPlanBlocks, sp, r);
     }
   } else {
-    if (phase == 1 && split) stream_kernel<1, false, true><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanBlocks, sp, r);
-    else if (phase == 1) stream_kernel<1, false><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanBlocks, sp, r);
-    else stream_kernel<2, false><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanBlocks, sp, r);
+    if (phase == 1 && split) stream_kernel<1, kWtPlain, true><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanBlocks, sp, r);
+    else if (phase == 1) stream_kernel<1, kWtPlain><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanBlocks, sp, r);
+    else stream_kernel<2, kWtPlain><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanBlocks, sp, r);
   }
   return hipGetLastError();
 }

@@ -277,10 +277,67 @@ __device__ __forceinline__ void stream_dot_lds8(const bf16* a_row, const bf16* a
   }
 }
 
+// ---- MXFP4 streaming -------------------------------------------------------
+// A 16-byte load of E2M1 codes is 32 values of one row: one scale group, and
+// this lane's share of four MFMA steps.  The K order inside an MFMA is free as
+// long as both operands use it, so step s of a 128-wide K run takes values
+// kb + 32 q + 8 s .. + 8 from lane group q of weights and activations alike,
+// and codes go from global memory straight into fragments: no LDS.
+// w_row[j] / s_row[j]: this lane's row (lane % 16) of weight block j, as codes
+// and as scale bytes.
+constexpr int KB4 = 128;  // K values per load of the wave
+constexpr int U4 = 2;     // loads per row and batch; two batches in flight
+
+template <int NB>
+__device__ __forceinline__ void stream_dot_mx(const bf16* a_row, const bf16* a_any, const uint8_t* const* w_row,
+                                              const uint8_t* const* s_row, int K, int lane, f32x4* acc) {
+  const int q = lane >> 4;
+  const int nb = (K + KB4 - 1) / KB4;
+  const bf16* arow = a_row ? a_row : a_any;
+  u32x4 wv[2][U4][NB], av[2][U4][4];
+  uint32_t sv[2][U4][NB];
+  // past the end every load reads the row's last group, whose activations are zeroed
+  auto load = [&](int x, int b0) {
+#pragma unroll
+    for (int u = 0; u < U4; ++u) {
+      int k = (b0 + u) * KB4 + q * 32;
+      k = k < K ? k : K - 32;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        wv[x][u][j] = ld16_nt(w_row[j] + (k >> 1));
+        sv[x][u][j] = s_row[j][k >> 5];
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) av[x][u][s] = ld16(arow + k + 8 * s);
+    }
+  };
+  auto compute = [&](int x, int b0) {
+#pragma unroll
+    for (int u = 0; u < U4; ++u) {
+      const bool in = a_row && (b0 + u) * KB4 + q * 32 < K;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const u32x4 am = in ? av[x][u][s] : u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              as_bf16x8(am), as_bf16x8(mx8_to_bf16x8(wv[x][u][j][s], e8m0(sv[x][u][j]))), acc[j], 0, 0, 0);
+      }
+    }
+  };
+  load(0, 0);
+  for (int b = 0; b < nb; b += 2 * U4) {
+    load(1, b + U4);
+    compute(0, b);
+    load(0, b + 2 * U4);
+    compute(1, b + U4);
+  }
+}
+
 // Bytes of wave-private LDS one item needs.
-template <bool FP8, bool SPLIT>
+template <int WT, bool SPLIT>
 constexpr int item_lds_bytes() {
-  return (SPLIT ? 1 : 2) * 8 * (FP8 ? PAIR8 : PAIR);
+  return WT == kWtMx ? 0 : (SPLIT ? 1 : 2) * 8 * (WT == kWtFp8 ? PAIR8 : PAIR);
 }
 
 // One item: slab `slab` of group g (routed expert g < E, or the shared
@@ -289,13 +346,14 @@ constexpr int item_lds_bytes() {
 // (the plan's list); else, when tok_mask is nonzero, the group's tokens as a
 // bit mask (row m is the token of its m-th set bit: a batch of at most 32
 // tokens whose dispatch is not in memory yet); else f.sorted.  lds: this
-// wave's item_lds_bytes<FP8, SPLIT>() bytes.  Returns at once if the slab
+// wave's item_lds_bytes<WT, SPLIT>() bytes.  Returns at once if the slab
 // lies past the group's columns.
-template <int PHASE, bool FP8, bool SPLIT>
+template <int PHASE, int WT, bool SPLIT>
 __device__ __forceinline__ void stream_item(const FfnArgs& f, int g, int r0, int base, int nrows,
                                             const int32_t* tok_row, int slab, int lane, char* lds,
                                             uint32_t tok_mask = 0u) {
-  static_assert(!SPLIT || (PHASE == 1 && !FP8), "split items are bf16 gate/up");
+  constexpr bool FP8 = WT == kWtFp8;
+  static_assert(!SPLIT || (PHASE == 1 && !FP8), "split items are bf16 or MXFP4 gate/up");
   constexpr int NB = SPLIT ? 1 : 2;
   const int cols_per_item = PHASE == 1 ? (SPLIT ? 8 : 16) : 32;
   const int m = lane & 15;  // A row / B column within a 16-block
@@ -337,10 +395,10 @@ __device__ __forceinline__ void stream_item(const FfnArgs& f, int g, int r0, int
       col = col < Ncols ? col : Ncols - 1;
       if (PHASE == 1) {
         const int kb = f.H / 128;
-        s_row[j] = (j ? f.scu : f.scg) + (int64_t)g * (f.I / 128) * kb + (col / 128) * kb;
+        s_row[j] = reinterpret_cast<const float*>(j ? f.scu : f.scg) + (int64_t)g * (f.I / 128) * kb + (col / 128) * kb;
       } else {
         const int kb = f.I / 128;
-        s_row[j] = f.scd + (int64_t)g * (f.H / 128) * kb + (col / 128) * kb;
+        s_row[j] = reinterpret_cast<const float*>(f.scd) + (int64_t)g * (f.H / 128) * kb + (col / 128) * kb;
       }
     }
   }
@@ -348,7 +406,24 @@ __device__ __forceinline__ void stream_item(const FfnArgs& f, int g, int r0, int
   f32x4 acc[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if constexpr (FP8) {
+  if constexpr (WT == kWtMx) {
+    // this lane's row of each block (split: gate rows 0-7, up rows 8-15);
+    // rows past the matrix read its last one and are never stored
+    const uint8_t* w_row[NB];
+    const uint8_t* s_row4[NB];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const bool up = PHASE == 1 && (SPLIT ? m >= 8 : j == 1);
+      int row = PHASE == 1 ? c0 + (SPLIT ? m & 7 : m) : c0 + j * 16 + m;
+      row = row < Ncols ? row : Ncols - 1;
+      const void* mat = PHASE == 1 ? (up ? f.wu : f.wg) : f.wd;
+      const void* sc = PHASE == 1 ? (up ? f.scu : f.scg) : f.scd;
+      const int64_t stride = PHASE == 1 ? (up ? f.su : f.sg) : f.sd;
+      w_row[j] = reinterpret_cast<const uint8_t*>(mat) + ((int64_t)g * stride + (int64_t)row * K) / 2;
+      s_row4[j] = reinterpret_cast<const uint8_t*>(sc) + ((int64_t)g * Ncols + row) * (K / 32);
+    }
+    stream_dot_mx<NB>(a_row, reinterpret_cast<const bf16*>(PHASE == 1 ? f.x : f.h), w_row, s_row4, K, lane, acc);
+  } else if constexpr (FP8) {
     // (an fp8 launch covers the routed groups only; the shared expert's
     // bf16 weights go through the bf16 launch)
     // first row and valid-row count of each 16-row weight block, and this

@@ -60,13 +60,13 @@ class MoEConfig:
     I: int
     I_shared: int = 0          # 0: no shared expert
     act: str = "bf16"          # "f32" | "bf16"
-    wdt: str = "bf16"          # "f32" | "bf16" | "fp8"
+    wdt: str = "bf16"          # "f32" | "bf16" | "fp8" | "mxfp4"
     x_std: float = 1.0
     w_std: float = 0.02
     router_std: Optional[float] = None  # None: 1/sqrt(H) (logit std ~1)
     zipf_s: float = 0.0        # >0: per-expert router bias -s*ln(rank)
     zero_frac: float = 0.0     # fraction of gate/up entries forced to 0 (fp8)
-    scale_block: int = 128     # fp8 block edge
+    scale_block: int = 128     # fp8 block edge; MXFP4: 32, the group along K
 
     @property
     def R(self) -> int:
@@ -201,6 +201,22 @@ def quantize_e4m3fn_blocks(w32: torch.Tensor, block: int):
     return codes.contiguous(), s.to(torch.float32).contiguous()
 
 
+def quantize_mxfp4_rows(w32: torch.Tensor):
+    """Quantise the rows of one [N, K] fp32 matrix to MXFP4: E2M1 codes, two a byte (the even value in the low
+    bits), and one E8M0 byte s per 32 values, scale 2^(s-127) = 2^(floor(log2 amax) - 2) (a group of zeros gets s = 0).
+    Round to nearest, ties to the even code, saturating at 6.  Returns (codes uint8 [N, K/2], scales uint8 [N, K/32])."""
+    N, K = w32.shape
+    assert K % 32 == 0
+    g = w32.reshape(N, K // 32, 32)
+    s = ((g.abs().amax(dim=2).contiguous().view(torch.int32) >> 23) - 2).clamp(min=0)
+    v = (g * ((254 - s) << 23).view(torch.float32)[:, :, None]).reshape(N, K)
+    a = v.abs()
+    code = ((a > 0.25).int() + (a >= 0.75).int() + (a > 1.25).int() + (a >= 1.75).int() + (a > 2.5).int()
+            + (a >= 3.5).int() + (a > 5.0).int())
+    code = code | (torch.signbit(v).int() << 3)
+    return (code[:, 0::2] | (code[:, 1::2] << 4)).to(torch.uint8).contiguous(), s.to(torch.uint8).contiguous()
+
+
 # ----------------------------------------------------------------------------
 # Problem tensors
 # ----------------------------------------------------------------------------
@@ -213,6 +229,7 @@ class Problem:
     sh_gate/up  [I_s, H]    act   or None;  sh_down [H, I_s]
     w_gate/up   [E, I, H]   act or uint8 e4m3fn codes;  w_down [E, H, I]
     s_gate/up   [E, I/b, H/b] fp32 (fp8 only);  s_down [E, H/b, I/b]
+    MXFP4: w_gate/up [E, I, H/2], w_down [E, H, I/2] and s_gate/up [E, I, H/32], s_down [E, H, I/32], all uint8
     """
 
     def __init__(self, cfg: MoEConfig, seed: int, device="cpu", x_attempts=None,
@@ -304,18 +321,25 @@ class Problem:
         w32 = self.expert_fp32(e, which)
         if self.cfg.wdt == "fp8":
             return quantize_e4m3fn_blocks(w32, self.cfg.scale_block)
+        if self.cfg.wdt == "mxfp4":
+            return quantize_mxfp4_rows(w32)
         return to_storage(w32, self.cfg.wdt), None
 
     def _draw_experts(self):
         c = self.cfg
         dev = self.device
-        if c.wdt == "fp8":
+        if c.wdt in ("fp8", "mxfp4"):
             wdtype = torch.uint8
         else:
             wdtype = torch.bfloat16 if c.wdt == "bf16" else torch.float32
-        self.w_gate = torch.empty((c.E, c.I, c.H), dtype=wdtype, device=dev)
-        self.w_up = torch.empty((c.E, c.I, c.H), dtype=wdtype, device=dev)
-        self.w_down = torch.empty((c.E, c.H, c.I), dtype=wdtype, device=dev)
+        per = 2 if c.wdt == "mxfp4" else 1  # values per stored element
+        self.w_gate = torch.empty((c.E, c.I, c.H // per), dtype=wdtype, device=dev)
+        self.w_up = torch.empty((c.E, c.I, c.H // per), dtype=wdtype, device=dev)
+        self.w_down = torch.empty((c.E, c.H, c.I // per), dtype=wdtype, device=dev)
+        if c.wdt == "mxfp4":
+            self.s_gate = torch.empty((c.E, c.I, c.H // 32), dtype=torch.uint8, device=dev)
+            self.s_up = torch.empty((c.E, c.I, c.H // 32), dtype=torch.uint8, device=dev)
+            self.s_down = torch.empty((c.E, c.H, c.I // 32), dtype=torch.uint8, device=dev)
         if c.wdt == "fp8":
             b = c.scale_block
             self.s_gate = torch.empty((c.E, c.I // b, c.H // b), dtype=torch.float32, device=dev)
