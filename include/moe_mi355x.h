@@ -265,6 +265,25 @@ moe_status moe_layer_forward(const moe_problem* p, const moe_weights* w, const v
 moe_status moe_layer_forward_noalloc(const moe_problem* p, const moe_weights* w, const void* x,
                                      void* out, int32_t* topk_ids, float* topk_w, void* stream);
 
+/* The whole layer for a batch of at most 16 tokens (a decode or speculative
+ * step), in two kernels instead of moe_layer_forward's five to seven: the
+ * router, then top-k, expert products, shared expert and combine in one grid.
+ * bf16 activations with any routed weight type; T > MOE_FEW_MAX_TOKENS or
+ * fp32 layers return MOE_ERR_UNSUPPORTED.
+ *   Routing as moe_route (MOE_FLAG_PAGE_ROUTING included; the other flags name
+ *   kernels that this call does not use and change nothing).  The hidden h is
+ *   rounded to bf16 as everywhere; the experts' outputs y are not: each token's
+ *   sum over its experts and the shared one stays fp32 until out is rounded,
+ *   so out may differ from moe_layer_forward's in its last bits.  Results are
+ *   deterministic run to run.
+ * ws: moe_few_workspace_bytes(p) bytes, 256-byte aligned (0 if p is invalid or
+ * unsupported); concurrent calls need distinct workspaces.  topk_ids and
+ * topk_w may be NULL.  Other arguments and errors as moe_layer_forward.    */
+#define MOE_FEW_MAX_TOKENS 16
+size_t moe_few_workspace_bytes(const moe_problem* p);
+moe_status moe_layer_forward_few(const moe_problem* p, const moe_weights* w, const void* x, void* out,
+                                 int32_t* topk_ids, float* topk_w, void* ws, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------------------
  * Gated residual around the layer (Qwen3.8-Flash-Next study, "Gated residual:
  * four streams, one sublayer input"): the persistent residual is four

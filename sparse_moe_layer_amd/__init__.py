@@ -14,7 +14,7 @@ import torch
 
 from ._lib import (LIB, MOE_BF16, MOE_F32, MOE_FLAG_FORCE_GEMM, MOE_FLAG_FORCE_STREAM,  # noqa: F401
                    MOE_FLAG_GEMM_TILE_128, MOE_FLAG_GEMM_TILE_256, MOE_FLAG_PAGE_ROUTING, MOE_FP8_E4M3FN,
-                   MOE_MXFP4, MOE_NOALLOC_SCRATCH_BYTES, MOE_OK, EXPORTS, moe_audit_stats, moe_gr_weights, moe_problem,
+                   MOE_FEW_MAX_TOKENS, MOE_MXFP4, MOE_NOALLOC_SCRATCH_BYTES, MOE_OK, EXPORTS, moe_audit_stats, moe_gr_weights, moe_problem,
                    moe_weights)
 
 _DT = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8": MOE_FP8_E4M3FN, "mxfp4": MOE_MXFP4}
@@ -126,6 +126,25 @@ def moe_mfma_pipe_probe(variant: int, steps: int, src, sink, stream=None):
 def moe_layer_forward_noalloc(p, w: moe_weights, x, out, topk_ids, topk_w, stream=None):
     _check(LIB.moe_layer_forward_noalloc(ctypes.byref(p), ctypes.byref(w), _ptr(x), _ptr(out), _ptr(topk_ids),
                                          _ptr(topk_w), _stream(stream)), "moe_layer_forward_noalloc")
+
+
+def moe_few_workspace_bytes(p: moe_problem) -> int:
+    return LIB.moe_few_workspace_bytes(ctypes.byref(p))
+
+
+def few_workspace(p: moe_problem, device="cuda") -> torch.Tensor:
+    """A device buffer of moe_few_workspace_bytes(p) bytes."""
+    n = moe_few_workspace_bytes(p)
+    if n == 0:
+        st = moe_validate(p)
+        raise MoEError(st if st != MOE_OK else 6, "moe_few_workspace_bytes")  # 6: MOE_ERR_UNSUPPORTED
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_layer_forward_few(p, w: moe_weights, x, out, topk_ids, topk_w, ws, stream=None):
+    """The whole layer for at most MOE_FEW_MAX_TOKENS tokens; ws: few_workspace(p)."""
+    _check(LIB.moe_layer_forward_few(ctypes.byref(p), ctypes.byref(w), _ptr(x), _ptr(out), _ptr(topk_ids),
+                                     _ptr(topk_w), _ptr(ws), ws.numel(), _stream(stream)), "moe_layer_forward_few")
 
 
 def gr_weights(norm_w, w_read, w_up, rank: int, eps: float = 1e-6) -> moe_gr_weights:

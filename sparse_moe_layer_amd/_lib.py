@@ -23,12 +23,14 @@ MOE_FLAG_GEMM_TILE_128 = 4
 MOE_FLAG_GEMM_TILE_256 = 8
 MOE_FLAG_PAGE_ROUTING = 16
 MOE_NOALLOC_SCRATCH_BYTES = 32 << 20
+MOE_FEW_MAX_TOKENS = 16
 
 EXPORTS = ["moe_abi_version", "moe_status_str", "moe_validate", "moe_workspace_bytes", "moe_route",
            "moe_dispatch", "moe_expert_ffn", "moe_expert_gate_up", "moe_expert_down", "moe_combine",
            "moe_layer_forward", "moe_gr_workspace_bytes", "moe_gr_read", "moe_gr_write", "moe_combine_gr_write",
            "moe_audit_workspace_bytes", "moe_weight_audit", "moe_layer_forward_noalloc",
-           "moe_hbm_read_probe", "moe_mfma_pipe_probe", "moe_mx_quantize", "moe_mx_dequantize"]
+           "moe_hbm_read_probe", "moe_mfma_pipe_probe", "moe_mx_quantize", "moe_mx_dequantize",
+           "moe_few_workspace_bytes", "moe_layer_forward_few"]
 
 
 class moe_problem(ctypes.Structure):
@@ -78,6 +80,8 @@ def _load():
         "moe_layer_forward_noalloc": (i32, [P, W, vp, vp, vp, vp, vp]),
         "moe_hbm_read_probe": (i32, [vp, sz, vp, vp]),
         "moe_mfma_pipe_probe": (i32, [ctypes.c_int32, ctypes.c_int32, vp, sz, vp, vp]),
+        "moe_few_workspace_bytes": (sz, [P]),
+        "moe_layer_forward_few": (i32, [P, W, vp, vp, vp, vp, vp, sz, vp]),
         "moe_mx_quantize": (i32, [vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, vp, vp, vp]),
         "moe_mx_dequantize": (i32, [vp, vp, ctypes.c_int64, ctypes.c_int64, vp, ctypes.c_int64, vp]),
         "moe_gr_workspace_bytes": (sz, [P, ctypes.c_int64]),

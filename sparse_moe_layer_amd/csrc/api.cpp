@@ -382,6 +382,40 @@ moe_status do_ffn(const moe_problem* p, const moe_weights* w, const void* x, con
   return run_ffn(p, a, 3, b, s, fork_ok, route);
 }
 
+// Workspace of the few-token call: logits | counters | h | h_shared.
+struct FewWs {
+  float* logits;
+  int32_t* counters;
+  void* h;
+  void* h_sh;
+  size_t total;
+};
+
+FewWs few_layout(const moe_problem* p, void* base) {
+  char* b = static_cast<char*>(base);
+  size_t o = 0;
+  FewWs L{};
+  auto take = [&](size_t bytes) {
+    char* r = b ? b + o : nullptr;
+    o += up(bytes);
+    return r;
+  };
+  L.logits = reinterpret_cast<float*>(take((size_t)p->T * (p->E + 1) * 4));
+  L.counters = reinterpret_cast<int32_t*>(take(2 * moe::kFewCounterStride * 4));
+  L.h = take((size_t)p->T * p->k * p->I * 2);
+  L.h_sh = take((size_t)p->T * p->I_shared * 2);
+  L.total = o;
+  return L;
+}
+
+moe_status check_few(const moe_problem* p) {
+  const moe_status st = check_problem(p);
+  if (st != MOE_OK) return st;
+  if (p->act_dtype != MOE_BF16 || p->T > MOE_FEW_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+static_assert(MOE_FEW_MAX_TOKENS == moe::kSmallBatch, "tokens of the few-token call");
+
 }  // namespace
 
 namespace moe {
@@ -543,6 +577,35 @@ moe_status moe_layer_forward(const moe_problem* p, const moe_weights* w, const v
   return moe::layer_forward_run(p, w, x, out, topk_ids, topk_w, ws, (hipStream_t)stream);
 }
 
+
+size_t moe_few_workspace_bytes(const moe_problem* p) {
+  if (check_few(p) != MOE_OK) return 0;
+  return few_layout(p, nullptr).total;
+}
+
+moe_status moe_layer_forward_few(const moe_problem* p, const moe_weights* w, const void* x, void* out,
+                                 int32_t* topk_ids, float* topk_w, void* ws, size_t ws_bytes, void* stream) {
+  moe_status st = check_few(p);
+  if (st != MOE_OK || p->T == 0) return st;
+  if ((st = moe::layer_forward_checks(p, w, x, out)) != MOE_OK) return st;
+  if (!ws) return MOE_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(ws) % kAlign) return MOE_ERR_ALIGN;
+  const FewWs L = few_layout(p, ws);
+  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  const bool sh = p->I_shared > 0;
+  FfnArgs f = ffn_args(p, w, x, nullptr, nullptr, sh);
+  f.h = L.h;
+  f.h_sh = L.h_sh;
+  moe::FewArgs a{};
+  a.logits = L.logits;
+  a.has_shared = sh;
+  a.page = (p->flags & MOE_FLAG_PAGE_ROUTING) != 0;
+  a.ids = topk_ids;
+  a.w = topk_w;
+  a.out = out;
+  a.counters = L.counters;
+  return hip_status(moe::launch_layer_few(f, w->w_router, sh ? w->sh_gate_w : nullptr, a, (hipStream_t)stream));
+}
 
 // ---------------------------------------------------------------------------
 // gated residual

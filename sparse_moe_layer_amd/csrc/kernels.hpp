@@ -156,6 +156,21 @@ moe_status layer_forward_checks(const moe_problem* p, const moe_weights* w, cons
 moe_status layer_forward_run(const moe_problem* p, const moe_weights* w, const void* x, void* out,
                              int32_t* topk_ids, float* topk_w, void* ws, hipStream_t s, bool fork_ok = true);
 
+// The layer for a few tokens (T <= kSmallBatch, bf16 activations) in two
+// kernels: arguments of the second one.
+struct FewArgs {
+  float* logits;         // [T, E + 1 if shared], written by the first kernel
+  int has_shared;
+  int page;              // the page's routing numerics
+  int32_t* ids;          // [T, k] or null
+  float* w;              // [T, k] or null
+  void* out;             // [T, H] bf16
+  int32_t* counters;     // two words kFewCounterStride ints apart: items claimed, items done
+};
+constexpr int kFewCounterStride = 64;
+// f.h [T*k, I] and f.h_sh [T, Is] are scratch; f.offsets and f.sorted are not used.
+hipError_t launch_layer_few(const FfnArgs& f, const void* w_router, const void* w_sg, const FewArgs& a, hipStream_t s);
+
 // MXFP4 weights: rows of K values (bf16, or fp32 with f32) to codes and E8M0
 // scales, and back to bf16.
 hipError_t launch_mx_quantize(const void* w, bool f32, int64_t rows, int64_t K, int64_t row_stride, void* codes,

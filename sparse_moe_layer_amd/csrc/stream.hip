@@ -21,48 +21,6 @@ namespace {
 using namespace streamk;
 constexpr int WAVES = 4;
 
-// acc[j] += A[16 rows, kbeg..kend) x B_j[16 rows, kbeg..kend)^T for NB bf16
-// weight blocks, operands loaded straight into MFMA fragments (the small-batch
-// router).  a_row: this lane's A row (row lane%16) or null (zero row);
-// b_row[j]: this lane's row of weight block j.  kq = 8*(lane/16) is the
-// lane's K offset inside a 32-wide K step.  U K steps per batch, two batches
-// in flight.
-template <int NB>
-__device__ __forceinline__ void stream_dot(const bf16* a_row, const bf16* const* b_row, int kbeg, int kend, int kq,
-                                           f32x4* acc) {
-  u32x4 av[2][U];
-  u32x4 bv[2][U][NB];
-  const int nsteps = (kend - kbeg + KSTEP - 1) / KSTEP;
-  auto load = [&](int buf, int s0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int kk = kbeg + (s0 + u) * KSTEP + kq;
-      const bool in = kk < kend;
-      av[buf][u] = (in && a_row) ? ld16(a_row + kk) : u32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int j = 0; j < NB; ++j) bv[buf][u][j] = in ? ld16(b_row[j] + kk) : u32x4{0, 0, 0, 0};
-    }
-  };
-  auto mma = [&](int buf) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int j = 0; j < NB; ++j)
-        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(av[buf][u]), as_bf16x8(bv[buf][u][j]), acc[j],
-                                                         0, 0, 0);
-  };
-  load(0, 0);
-  for (int s0 = 0; s0 < nsteps; s0 += 2 * U) {
-    const bool more = s0 + U < nsteps;
-    if (more) load(1, s0 + U);
-    mma(0);
-    if (more) {
-      if (s0 + 2 * U < nsteps) load(0, s0 + 2 * U);
-      mma(1);
-    }
-  }
-}
-
 // SPLIT (bf16 gate/up only): items of 8 hidden columns, one 16-row block of
 // 8 gate rows and the 8 up rows of the same columns.  Half-size items end a
 // launch with less idle time; they pay off when the whole batch streams

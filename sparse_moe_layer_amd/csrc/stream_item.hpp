@@ -25,6 +25,48 @@ constexpr int KSTEP = 32;
 
 __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
+// acc[j] += A[16 rows, kbeg..kend) x B_j[16 rows, kbeg..kend)^T for NB bf16
+// weight blocks, operands loaded straight into MFMA fragments (the
+// small-batch routers).  a_row: this lane's A row (row lane%16) or null (zero row);
+// b_row[j]: this lane's row of weight block j.  kq = 8*(lane/16) is the
+// lane's K offset inside a 32-wide K step.  U K steps per batch, two batches
+// in flight.
+template <int NB>
+__device__ __forceinline__ void stream_dot(const bf16* a_row, const bf16* const* b_row, int kbeg, int kend, int kq,
+                                           f32x4* acc) {
+  u32x4 av[2][U];
+  u32x4 bv[2][U][NB];
+  const int nsteps = (kend - kbeg + KSTEP - 1) / KSTEP;
+  auto load = [&](int buf, int s0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kk = kbeg + (s0 + u) * KSTEP + kq;
+      const bool in = kk < kend;
+      av[buf][u] = (in && a_row) ? ld16(a_row + kk) : u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < NB; ++j) bv[buf][u][j] = in ? ld16(b_row[j] + kk) : u32x4{0, 0, 0, 0};
+    }
+  };
+  auto mma = [&](int buf) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(av[buf][u]), as_bf16x8(bv[buf][u][j]), acc[j],
+                                                         0, 0, 0);
+  };
+  load(0, 0);
+  for (int s0 = 0; s0 < nsteps; s0 += 2 * U) {
+    const bool more = s0 + U < nsteps;
+    if (more) load(1, s0 + U);
+    mma(0);
+    if (more) {
+      if (s0 + 2 * U < nsteps) load(0, s0 + 2 * U);
+      mma(1);
+    }
+  }
+}
+
 // ---- LDS-staged bf16 streaming -------------------------------------------
 // A batch holds SB = 256 K values (512 B) of NB*16 weight rows.  Rows 2i and
 // 2i+1 of the batch sit in 1 KB at i * 1040 B (1 KB + 16 B pad); odd rows
@@ -172,10 +214,13 @@ __device__ __forceinline__ void stream_dot_lds(const bf16* a_row, const bf16* a_
 constexpr int SB8 = 256;
 constexpr int PAIR8 = 528;
 
-template <int NB>
+// SPLIT (NB == 1): rows 0-7 from wrow0[0] and rows 8-15 from wrow0[1], with
+// nvalid[0] and nvalid[1] valid rows (s_row[0] is the lane's own row's either way).
+template <int NB, bool SPLIT = false>
 __device__ __forceinline__ void stream_dot_lds8(const bf16* a_row, const bf16* a_any, const uint8_t* const* wrow0,
                                                 const int* nvalid, int ldw, const float* const* s_row, int kbeg,
                                                 int kend, int lane, char* lds, f32x4* acc) {
+  static_assert(!SPLIT || NB == 1, "a split block is the only block");
   constexpr int NL = NB * 4;       // weight loads per batch (4 rows each)
   constexpr int NA = SB8 / KSTEP;  // activation loads per batch
   const int kq = (lane >> 4) * 8;
@@ -193,8 +238,14 @@ __device__ __forceinline__ void stream_dot_lds8(const bf16* a_row, const bf16* a
     for (int j = 0; j < NB; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = 4 * i + q4 < nvalid[j] ? 4 * i + q4 : nvalid[j] - 1;
-        wb[j * 4 + i] = ld16_nt(wrow0[j] + (uint32_t)(r * ldw + k));
+        if constexpr (SPLIT) {
+          const int half = i >> 1, rh = (4 * i + q4) & 7;
+          const int r = rh < nvalid[half] ? rh : nvalid[half] - 1;
+          wb[i] = ld16_nt(wrow0[half] + (uint32_t)(r * ldw + k));
+        } else {
+          const int r = 4 * i + q4 < nvalid[j] ? 4 * i + q4 : nvalid[j] - 1;
+          wb[j * 4 + i] = ld16_nt(wrow0[j] + (uint32_t)(r * ldw + k));
+        }
       }
   };
   auto load_a = [&](int x, int b) {
@@ -290,9 +341,10 @@ constexpr int U4 = 2;     // loads per row and batch; two batches in flight
 
 template <int NB>
 __device__ __forceinline__ void stream_dot_mx(const bf16* a_row, const bf16* a_any, const uint8_t* const* w_row,
-                                              const uint8_t* const* s_row, int K, int lane, f32x4* acc) {
+                                              const uint8_t* const* s_row, int kbeg, int kend, int lane,
+                                              f32x4* acc) {
   const int q = lane >> 4;
-  const int nb = (K + KB4 - 1) / KB4;
+  const int nb = (kend - kbeg + KB4 - 1) / KB4;
   const bf16* arow = a_row ? a_row : a_any;
   u32x4 wv[2][U4][NB], av[2][U4][4];
   uint32_t sv[2][U4][NB];
@@ -300,8 +352,8 @@ __device__ __forceinline__ void stream_dot_mx(const bf16* a_row, const bf16* a_a
   auto load = [&](int x, int b0) {
 #pragma unroll
     for (int u = 0; u < U4; ++u) {
-      int k = (b0 + u) * KB4 + q * 32;
-      k = k < K ? k : K - 32;
+      int k = kbeg + (b0 + u) * KB4 + q * 32;
+      k = k < kend ? k : kend - 32;
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         wv[x][u][j] = ld16_nt(w_row[j] + (k >> 1));
@@ -314,7 +366,7 @@ __device__ __forceinline__ void stream_dot_mx(const bf16* a_row, const bf16* a_a
   auto compute = [&](int x, int b0) {
 #pragma unroll
     for (int u = 0; u < U4; ++u) {
-      const bool in = a_row && (b0 + u) * KB4 + q * 32 < K;
+      const bool in = a_row && kbeg + (b0 + u) * KB4 + q * 32 < kend;
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         const u32x4 am = in ? av[x][u][s] : u32x4{0, 0, 0, 0};
@@ -353,7 +405,7 @@ __device__ __forceinline__ void stream_item(const FfnArgs& f, int g, int r0, int
                                             const int32_t* tok_row, int slab, int lane, char* lds,
                                             uint32_t tok_mask = 0u) {
   constexpr bool FP8 = WT == kWtFp8;
-  static_assert(!SPLIT || (PHASE == 1 && !FP8), "split items are bf16 or MXFP4 gate/up");
+  static_assert(!SPLIT || PHASE == 1, "split items are gate/up");
   constexpr int NB = SPLIT ? 1 : 2;
   const int cols_per_item = PHASE == 1 ? (SPLIT ? 8 : 16) : 32;
   const int m = lane & 15;  // A row / B column within a 16-block
@@ -395,7 +447,12 @@ __device__ __forceinline__ void stream_item(const FfnArgs& f, int g, int r0, int
       col = col < Ncols ? col : Ncols - 1;
       if (PHASE == 1) {
         const int kb = f.H / 128;
-        s_row[j] = reinterpret_cast<const float*>(j ? f.scu : f.scg) + (int64_t)g * (f.I / 128) * kb + (col / 128) * kb;
+        const bool up = SPLIT ? m >= 8 : j == 1;
+        if (SPLIT) {
+          col = c0 + (m & 7);
+          col = col < Ncols ? col : Ncols - 1;
+        }
+        s_row[j] = reinterpret_cast<const float*>(up ? f.scu : f.scg) + (int64_t)g * (f.I / 128) * kb + (col / 128) * kb;
       } else {
         const int kb = f.I / 128;
         s_row[j] = reinterpret_cast<const float*>(f.scd) + (int64_t)g * (f.H / 128) * kb + (col / 128) * kb;
@@ -422,16 +479,17 @@ __device__ __forceinline__ void stream_item(const FfnArgs& f, int g, int r0, int
       w_row[j] = reinterpret_cast<const uint8_t*>(mat) + ((int64_t)g * stride + (int64_t)row * K) / 2;
       s_row4[j] = reinterpret_cast<const uint8_t*>(sc) + ((int64_t)g * Ncols + row) * (K / 32);
     }
-    stream_dot_mx<NB>(a_row, reinterpret_cast<const bf16*>(PHASE == 1 ? f.x : f.h), w_row, s_row4, K, lane, acc);
+    stream_dot_mx<NB>(a_row, reinterpret_cast<const bf16*>(PHASE == 1 ? f.x : f.h), w_row, s_row4, 0, K, lane, acc);
   } else if constexpr (FP8) {
     // (an fp8 launch covers the routed groups only; the shared expert's
     // bf16 weights go through the bf16 launch)
     // first row and valid-row count of each 16-row weight block, and this
     // lane's fragment row's scale row
-    const uint8_t* w0[NB];
-    int nv[NB];
+    constexpr int NW0 = SPLIT ? 2 : NB;
+    const uint8_t* w0[NW0];
+    int nv[NW0];
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
+    for (int j = 0; j < NW0; ++j) {
       int first = PHASE == 1 ? c0 : c0 + j * 16;
       first = first < Ncols ? first : Ncols - 1;
       nv[j] = Ncols - first;
@@ -441,7 +499,7 @@ __device__ __forceinline__ void stream_item(const FfnArgs& f, int g, int r0, int
       w0[j] = mat + (int64_t)first * K;
     }
     const bf16* a_any = reinterpret_cast<const bf16*>(PHASE == 1 ? f.x : f.h);
-    stream_dot_lds8<NB>(a_row, a_any, w0, nv, K, s_row, 0, K, lane, lds, acc);
+    stream_dot_lds8<NB, SPLIT>(a_row, a_any, w0, nv, K, s_row, 0, K, lane, lds, acc);
   } else {
     // first row and valid-row count of each weight block (gate/up: of the
     // gate half and the up half of the one split block)
