@@ -1,308 +1,618 @@
 // The whole layer for a few tokens (T <= 16) in two kernels (Qwen3.8-Flash-Next
 // study, MoE section: eq. expert(x) and eq. MoE(x) over its pipeline figure):
-//   few_router_kernel  : logits[t, e] = x_t . W_r[e] and x_t . w_sg, complete in fp32
+//   few_router_kernel  : logits[t, e] = x_t . W_r[e] and x_t . w_sg, complete in fp32, and the
+//                        shared expert's hidden h_sh = SiLU(S_gate x) * (S_up x), which needs no routing
 //   few_experts_kernel : top-k and weights, then h = SiLU(W_gate x) * (W_up x) of every
-//                        (token, expert) pair and of the shared expert, then
+//                        (token, expert) pair, then
 //     out[t] = sum_j w[t,j] W_down[e_j] h[t,j] + sigmoid(s_t) S_down h_sh[t]
 // A batch this small is bound by reading the touched experts' weights once,
 // and below a few hundred MB by the latency of the steps between them, so the
 // launches between the stages go: every workgroup does the top-k itself (a few
 // KB of logits), and the one dependency between workgroups, h before the down
-// products, is a counter in memory.
+// products, is counters in memory.
 //
-// Work order and why every wait ends: the gate/up items are claimed from a
-// counter, and a workgroup goes on to its down columns only when the counter
-// has run out.  Then every gate/up item is held by a workgroup that runs and
-// waits for nothing, so the number of finished items reaches their total
-// whatever else the GPU runs, however few workgroups of this grid are resident.
+// Work order and why every wait ends: the gate/up chunks have owners, but an
+// owner takes its chunk by a flag first.  A workgroup waits for h only when its
+// own chunks are done, and while it waits it looks for chunks whose flag is
+// free and does them.  So a chunk is held by a wave that runs and waits for
+// nothing, or free for any waiting workgroup, and the number of finished slabs
+// reaches its total whatever else the GPU runs, even with one workgroup of the
+// grid resident.
 //
-// Down products: a workgroup owns 16 output columns and goes over all groups,
-// its waves taking (group, K range) units in turn; a fragment row is a token
-// (zero where the token does not use the expert), so each unit's fp32 block is
-// scaled by the routing weights and added in registers, the waves' sums are
+// Gate/up: a slab is 16 hidden columns, a block of their gate rows and one of
+// their up rows; when the slabs are fewer than the waves their K range is split over 2
+// to 8 waves of a workgroup, added in LDS in K order.  Down: a workgroup owns
+// up to 16 output columns and goes over all groups, each wave over an equal
+// share of their K ranges; a fragment row is a token, so each group's fp32 block
+// is scaled by the routing weights and added in registers, the waves' sums are
 // added in LDS in wave order, and out is rounded once.  No per-assignment
-// output is stored or rounded, and no sum depends on timing.
+// output is stored or rounded, and no sum depends on timing.  A wave asks for
+// its first down weights before it waits for h, so the memory stays busy
+// across the dependency.
 #include "common.hpp"
+#include "frag_dot.hpp"
 #include "kernels.hpp"
-#include "stream_item.hpp"
 #include "topk.hpp"
 
 namespace moe {
 namespace {
 
-using namespace streamk;
+using fragdot::Job;
+using fragdot::NoGate;
 
-constexpr int FW = 8;                      // waves per workgroup of the experts kernel
+constexpr int RW = 16;                       // waves per workgroup of the router kernel
+constexpr int kLogFW = 3, FW = 1 << kLogFW;  // of the experts kernel, one workgroup per compute unit
+constexpr int kSlab = 16;                    // hidden columns per slab: a block of gate rows and one of up rows
 constexpr int kFewRows = kSmallBatch * 64;  // (token, expert) pairs at most
 static_assert(kSmallBatch == 16 && kMaxExperts < 2048, "a fragment row per token; packed list entries");
 
-// Workgroup b: router rows 16 b .. 16 b + 15 (row E: the shared gate), K split
-// over 16 waves whose blocks are added in wave order.  The first workgroup
-// zeroes the counters of the kernel that follows.
-constexpr int RWF = 16;
-__global__ __launch_bounds__(RWF * 64) void few_router_kernel(const bf16* __restrict__ x, const bf16* __restrict__ wr,
-                                                              const bf16* __restrict__ wsg,
-                                                              float* __restrict__ logits, int T, int H, int E, int N,
-                                                              int kchunk, int32_t* counters) {
-  if (blockIdx.x == 0 && threadIdx.x < 2) counters[threadIdx.x * kFewCounterStride] = 0;
-  __shared__ f32x4 part[RWF][64];
+// Workgroups [0, nr): 16 router rows each; workgroup nr (shared expert only):
+// its gate's logit; the rest: 8 of its hidden columns each (8 gate, 8 up rows).
+// K is split over the waves, whose blocks are added in wave order.  The grid also
+// zeroes the counters and claim flags of the kernel that follows.
+__global__ __launch_bounds__(RW * 64) void few_router_kernel(const bf16* __restrict__ x, const bf16* __restrict__ wr,
+                                                             const bf16* __restrict__ wsg, float* __restrict__ logits,
+                                                             int T, int H, int E, int N, int nr,
+                                                             const bf16* __restrict__ shg,
+                                                             const bf16* __restrict__ shu, int Is,
+                                                             bf16* __restrict__ h_sh, int kchunk, int32_t* counters,
+                                                             int ncounters) {
+  for (int i = blockIdx.x * (RW * 64) + threadIdx.x; i < ncounters; i += gridDim.x * (RW * 64)) counters[i] = 0;
+  __shared__ f32x4 part[RW][64];
+  __shared__ __attribute__((aligned(16))) char act[RW][fragdot::kLds];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int m = lane & 15, kq = (lane >> 4) * 8;
+  const int m = lane & 15;
   const int kbeg = w * kchunk;
   const int kend = kbeg + kchunk < H ? kbeg + kchunk : H;
-  f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
-  if (kbeg < kend) {
-    const bf16* a_row = m < T ? x + (int64_t)m * H : nullptr;
-    int n = blockIdx.x * 16 + m;
-    n = n < N ? n : N - 1;
-    const bf16* b_row[1] = {n < E ? wr + (int64_t)n * H : wsg};
-    stream_dot<1>(a_row, b_row, kbeg, kend, kq, acc);
+  const bool route = (int)blockIdx.x <= nr;
+  const int c0 = (int)blockIdx.x <= nr ? blockIdx.x * 16 : (blockIdx.x - nr - 1) * 8;
+  Job<1> b{};
+  int cols;
+  if ((int)blockIdx.x < nr) {
+    cols = E - c0 < 16 ? E - c0 : 16;
+    b.w[0] = reinterpret_cast<const char*>(wr + (int64_t)c0 * H);
+    b.w[1] = reinterpret_cast<const char*>(wr + (int64_t)(c0 + 8) * H);
+    b.wrows[0] = cols < 8 ? cols : 8;
+    b.wrows[1] = cols < 8 ? 0 : cols - 8;
+  } else if (route) {
+    cols = 1;
+    b.w[0] = b.w[1] = reinterpret_cast<const char*>(wsg);
+    b.wrows[0] = 1;
+  } else {
+    cols = Is - c0 < 8 ? Is - c0 : 8;
+    b.w[0] = reinterpret_cast<const char*>(shg + (int64_t)c0 * H);
+    b.w[1] = reinterpret_cast<const char*>(shu + (int64_t)c0 * H);
+    b.wrows[0] = b.wrows[1] = cols;
   }
-  part[w][lane] = acc[0];
+  b.rows = T;
+  b.ar = m < T ? m : 0;
+  b.k0 = kbeg;
+  b.kend = kend;
+  bool todo = kbeg < kend;
+  part[w][lane] = f32x4{0.f, 0.f, 0.f, 0.f};
+  fragdot::run<kWtPlain, 1, 0>(
+      x, (uint32_t)T * (uint32_t)H * 2u, H, lane, act[w],
+      [&](Job<1>& j) {
+        if (todo) j = b;
+        const bool was = todo;
+        todo = false;
+        return was;
+      },
+      [&](int, const f32x4 (&acc)[1]) { part[w][lane] = acc[0]; }, NoGate{});
   __syncthreads();
   if (w == 0) {
     f32x4 t = part[0][lane];
 #pragma unroll
-    for (int i = 1; i < RWF; ++i) t += part[i][lane];
-    const int col = blockIdx.x * 16 + m;
+    for (int i = 1; i < RW; ++i) t += part[i][lane];
+    const int col = (int)blockIdx.x == nr ? E : c0 + m;  // logits column
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int tok = 4 * (lane >> 4) + i;
-      if (tok < T && col < N) logits[(int64_t)tok * N + col] = t[i];
+      if (route) {
+        if (tok < T && m < cols) logits[(int64_t)tok * N + col] = t[i];
+      } else {
+        const float up = __shfl_xor(t[i], 8, 64);  // the up row of lane m is lane m + 8's
+        if (tok < T && m < cols) h_sh[(int64_t)tok * Is + c0 + m] = f2bf(silu(t[i]) * up);
+      }
     }
   }
 }
 
-// Top-k of one token by one wave: lane j < k returns the j-th pick and its
-// renormalised weight.
-template <int PER_LANE>
-__device__ __forceinline__ void pick(const float* row, int E, int k, int page, int lane, int* id, float* wj) {
-  uint64_t key[PER_LANE];
-#pragma unroll
-  for (int i = 0; i < PER_LANE; ++i) {
-    const int e = lane + 64 * i;
-    float a = row[e < E ? e : E - 1];
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, ROWS, 0xf, false));
+}
+// Sum over the 64 lanes (wave-uniform), in a fixed order.
+__device__ __forceinline__ float row_sum(float v) {
+  v = dpp_add<0x111, 0xf>(v);  // row_shr:1, 2, 4, 8: lane 15 of each row has the row's
+  v = dpp_add<0x112, 0xf>(v);
+  v = dpp_add<0x114, 0xf>(v);
+  v = dpp_add<0x118, 0xf>(v);
+  v = dpp_add<0x142, 0xa>(v);  // row_bcast:15 into rows 1 and 3
+  v = dpp_add<0x143, 0xc>(v);  // row_bcast:31 into rows 2 and 3
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+
+// Top-k of one token by one wave, into ids[0..k) and wts[0..k) (LDS).  The
+// k-th largest of the 64 lanes' own maxima bounds the answer from below, so
+// only logits at least that large (about k of them) are ranked, each by
+// counting the larger ones.  More than 64 candidates (many equal logits): k
+// rounds of a wave-wide maximum.  keys: kMaxExperts of LDS.  The loops are
+// rolled where that costs little: the code runs once, and its instructions
+// arrive from memory.
+__device__ __forceinline__ void pick(const float* row, int E, int k, int page, int lane, uint32_t* keys,
+                                     uint64_t* cand, int* ids, float* wts) {
+  uint32_t top = 0;
+#pragma unroll 4
+  for (int e = lane; e < E; e += 64) {
+    float a = row[e];
     if (page) a = bf2f(f2bf(a));
-    key[i] = make_key(e < E ? ord(a) : 0u, e);
+    const uint32_t v = ord(a);
+    keys[e] = v;
+    top = v > top ? v : top;
   }
-  const uint64_t sel = select_topk<PER_LANE>(key, k, lane);
-  const uint32_t hi = (uint32_t)(sel >> 32);
-  const float top = unord(__builtin_amdgcn_readlane(hi, 0));
-  const float ex = lane < k ? expf(unord(hi) - top) : 0.f;
-  const float v = ex / wave_sum(ex);
-  *wj = page ? bf2f(f2bf(v)) : v;
-  int e = (int)~(uint32_t)sel;
-  *id = (unsigned)e < (unsigned)E ? e : E - 1;  // (out of range only for NaN logits)
+  // how many lanes' maxima rank before this lane's: all 64 read back from LDS
+  uint32_t* const tops = reinterpret_cast<uint32_t*>(cand);
+  tops[lane] = top;
+  __builtin_amdgcn_wave_barrier();
+  int above = 0;
+#pragma unroll 4
+  for (int j = 0; j < 64; j += 4) {
+    const u32x4 o = *reinterpret_cast<const u32x4*>(tops + j);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) above += o[i] > top || (o[i] == top && j + i < lane);
+  }
+  const uint32_t bound =
+      (uint32_t)__builtin_amdgcn_readlane((int)top, __builtin_ctzll(__ballot(above == k - 1) | 1ull << 63));
+  int n = 0;
+#pragma unroll 4
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int e = e0 + lane;
+    const uint32_t v = e < E ? keys[e] : 0u;
+    const bool in = e < E && v >= bound;
+    const uint64_t bal = __ballot(in);
+    const int at = n + __popcll(bal & ((1ull << lane) - 1ull));
+    if (in && at < 64) cand[at] = make_key(v, e);
+    n += __popcll(bal);
+  }
+  n = (int)uniform((uint32_t)n);
+  __builtin_amdgcn_wave_barrier();
+  uint64_t mine = 0;
+  int rank = 64;
+  if (n <= 64) {
+    mine = lane < n ? cand[lane] : 0ull;
+    cand[lane] = mine;  // (zeros behind the candidates)
+    __builtin_amdgcn_wave_barrier();
+    rank = lane < n ? 0 : 64;
+#pragma unroll 1
+    for (int j = 0; j < n; j += 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) rank += cand[j + i] > mine;
+    }
+  } else {
+    for (int j = 0; j < k; ++j) {
+      uint64_t best = 0;
+      for (int e = lane; e < E; e += 64)
+        if (keys[e]) best = key_max(best, make_key(keys[e], e));
+      best = wave_key_max(best);
+      if (lane == j) {
+        mine = best;
+        rank = j;
+      }
+      const uint32_t e = ~(uint32_t)best;
+      if (lane == 0 && e < (uint32_t)E) keys[e] = 0u;  // taken
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+  const float l = unord((uint32_t)(mine >> 32));
+  const float best = __uint_as_float((uint32_t)__builtin_amdgcn_readlane(
+      (int)__float_as_uint(l), __builtin_ctzll(__ballot(rank == 0) | 1ull << 63)));
+  const bool in = rank < k;
+  const float ex = in ? expf(l - best) : 0.f;
+  const float v = ex / row_sum(ex);
+  if (lane < k) ids[lane] = E - 1;  // (NaN logits may leave places without a pick)
+  if (lane < k) wts[lane] = 0.f;
+  if (in) {
+    const uint32_t e = ~(uint32_t)mine;
+    ids[rank] = e < (uint32_t)E ? (int)e : E - 1;
+    wts[rank] = page ? bf2f(f2bf(v)) : v;
+  }
 }
 
 // What a workgroup knows of the batch's routing.
 struct FewRoute {
-  uint32_t list[kFewRows + 1];  // touched experts ascending, then E for the shared one: expert | its tokens << 11
-  uint16_t base[kFewRows + 1];  // its first row of h
-  float w[kFewRows];         // per row of h: the routing weight
-  float sg[kSmallBatch];     // sigmoid of the shared gate logit
-  int wtot[FW], wrow[FW];
-  int next;                  // claimed item, block-wide
+  // groups: a touched expert and up to ROWS of its tokens, experts by first use; expert | tokens << 11
+  uint32_t list[kFewRows];
+  uint16_t base[kFewRows];       // its first row of h
+  float w[kFewRows];             // per row of h: the routing weight
+  uint8_t token[kFewRows];       // and the token
+  float sg[kSmallBatch];         // sigmoid of the shared gate logit
+  int groups;
+  int claim;                     // whether the workgroup's next chunk is its own
+  int left;                      // waves done with their gate/up work, their slabs << 8
+  int ready;                     // every h is written
 };
 
-// The blocks of a unit: part = H_rows [16 tokens, kbeg..kend) x W_down rows c0 .. c0 + 15.
-template <int WT>
-__device__ __forceinline__ f32x4 down_dot(const FfnArgs& f, int g, const bf16* a_row, const bf16* a_any, int c0, int K,
-                                          int kbeg, int kend, int lane, char* lds) {
-  const int m = lane & 15;
-  const int left = f.H - c0;  // columns from c0 to the end
-  const int nv[1] = {left};
-  f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
-  if constexpr (WT == kWtPlain) {
-    const bool shared = g >= f.E;
-    const bf16* mat = shared ? reinterpret_cast<const bf16*>(f.shd)
-                             : reinterpret_cast<const bf16*>(f.wd) + (int64_t)g * f.sd;
-    const bf16* w0[1] = {mat + (int64_t)c0 * K};
-    stream_dot_lds<1, false, 2>(a_row, a_any, w0, nv, K, kbeg, kend, lane, lds, acc);
-  } else if constexpr (WT == kWtFp8) {
-    const uint8_t* w0[1] = {reinterpret_cast<const uint8_t*>(f.wd) + (int64_t)g * f.sd + (int64_t)c0 * K};
-    const int col = m < left ? c0 + m : f.H - 1;
-    const int kb = K / 128;
-    const float* s0[1] = {reinterpret_cast<const float*>(f.scd) + (int64_t)g * (f.H / 128) * kb + (col / 128) * kb};
-    stream_dot_lds8<1>(a_row, a_any, w0, nv, K, s0, kbeg, kend, lane, lds, acc);
-  } else {
-    const int row = m < left ? c0 + m : f.H - 1;
-    const uint8_t* w0[1] = {reinterpret_cast<const uint8_t*>(f.wd) + ((int64_t)g * f.sd + (int64_t)row * K) / 2};
-    const uint8_t* s0[1] = {reinterpret_cast<const uint8_t*>(f.scd) + ((int64_t)g * f.H + row) * (K / 32)};
-    stream_dot_mx<1>(a_row, a_any, w0, s0, kbeg, kend, lane, acc);
-  }
-  return acc[0];
-}
-
-// K range of a unit: multiples of 256 (a batch of every weight form), so that
-// the groups' units number at least two per wave where K allows it.
-constexpr int kUnitK = 256;
+constexpr int kHelpAfter = 2048;  // polls (about 0.3 us each) between looks for unclaimed chunks
+constexpr int kUnitK = 128;     // K values per unit of the shares of K
 
 template <int WT>
 __global__ __launch_bounds__(FW * 64, 2) void few_experts_kernel(FfnArgs f, FewArgs a) {
-  constexpr int ROUTED = item_lds_bytes<WT, true>(), PLAIN = item_lds_bytes<kWtPlain, true>();
-  constexpr int STAGE = ROUTED > PLAIN ? ROUTED : PLAIN;  // per wave
-  __shared__ __attribute__((aligned(16))) char stage[FW * STAGE];
+  using F = fragdot::Form<WT>;
+  // per wave: the logits' keys and candidates, later activations; picks and expert tables; the waves' blocks
+  __shared__ __attribute__((aligned(16))) char act[FW][fragdot::kLds];
+  __shared__ __attribute__((aligned(16))) uint64_t cand[FW][64];
+  __shared__ int ids[kFewRows];
+  __shared__ float wts[kFewRows];
+  __shared__ uint32_t tmask[kMaxExperts];
+  __shared__ int lead[kMaxExperts];
+  __shared__ f32x4 part[FW][2][64];
   __shared__ FewRoute r;
-  static_assert(FW * STAGE >= (2 * kFewRows + kMaxExperts) * 4, "routing scratch in the stage");
-  static_assert(FW * STAGE >= FW * 64 * 16, "the waves' sums in the stage");
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = (int)uniform(tid >> 6);
   const int T = f.T, k = f.k, E = f.E, R = T * k;
   const bool shared = a.has_shared != 0;
   const int N = E + (shared ? 1 : 0);
+  const int grid = (int)gridDim.x, waves = grid * FW;
+  const int gw = (int)blockIdx.x * FW + wave;
+  int32_t* const claims = a.counters + (kFewDone + 1) * kFewCounterStride;
 
-  // ---- routing: every workgroup for itself ----
-  int* ids = reinterpret_cast<int*>(stage);
-  float* wts = reinterpret_cast<float*>(stage) + kFewRows;
-  uint32_t* tmask = reinterpret_cast<uint32_t*>(stage) + 2 * kFewRows;
-  for (int e = tid; e < E; e += FW * 64) tmask[e] = 0u;
+  // ---- routing: every workgroup for itself, a wave per token ----
   for (int t = wave; t < T; t += FW) {
-    int id;
-    float wj;
     const float* row = a.logits + (int64_t)t * N;
-    if (E <= 64) pick<1>(row, E, k, a.page, lane, &id, &wj);
-    else if (E <= 128) pick<2>(row, E, k, a.page, lane, &id, &wj);
-    else if (E <= 256) pick<4>(row, E, k, a.page, lane, &id, &wj);
-    else if (E <= 512) pick<8>(row, E, k, a.page, lane, &id, &wj);
-    else pick<16>(row, E, k, a.page, lane, &id, &wj);
-    if (lane < k) {
-      ids[t * k + lane] = id;
-      wts[t * k + lane] = wj;
-      if (blockIdx.x == 0 && a.ids) a.ids[t * k + lane] = id;
-      if (blockIdx.x == 0 && a.w) a.w[t * k + lane] = wj;
-    }
+    pick(row, E, k, a.page, lane, reinterpret_cast<uint32_t*>(act[wave]), cand[wave], ids + t * k, wts + t * k);
     if (shared && lane == 0) r.sg[t] = sigmoid(row[E]);
   }
   __syncthreads();
-  for (int i = tid; i < R; i += FW * 64) atomicOr(&tmask[ids[i]], 1u << (i / k));
-  __syncthreads();
-  // the touched experts in ascending order, with their first rows
-  int ng = 0, rows = 0;
-  for (int g0 = 0; g0 < E; g0 += FW * 64) {
-    const int g = g0 + tid;
-    const uint32_t mk = g < E ? tmask[g] : 0u;
-    const uint64_t bal = __ballot(mk != 0u);
-    int incl = __popc(mk);
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int u = __shfl_up(incl, o, 64);
-      if (lane >= o) incl += u;
+  // Wave 0 groups the assignments i = t * k + j by expert: an expert's token
+  // mask, its first assignment (its place in the list is by first use), its
+  // first row of h and its groups.  (An expert with more than ROWS tokens is
+  // read once per group; with 512 experts and 16 tokens 2 in 1000 have that many.)
+  // LDS operations of one wave are executed in order.
+  if (wave == 0) {
+    for (int i = lane; i < R; i += 64) {
+      tmask[ids[i]] = 0u;
+      lead[ids[i]] = R;
     }
-    if (lane == 63) {
-      r.wtot[wave] = __popcll(bal);
-      r.wrow[wave] = incl;
+    __builtin_amdgcn_wave_barrier();
+    for (int i = lane; i < R; i += 64) {
+      atomicOr(&tmask[ids[i]], 1u << (i / k));
+      atomicMin(&lead[ids[i]], i);
     }
-    __syncthreads();
-    int off = ng, roff = rows;
-    for (int w = 0; w < FW; ++w) {
-      if (w < wave) {
-        off += r.wtot[w];
-        roff += r.wrow[w];
+    __builtin_amdgcn_wave_barrier();
+    const uint64_t below = (1ull << lane) - 1ull;
+    int ng = 0, rows = 0;
+    for (int i0 = 0; i0 < R; i0 += 64) {
+      const int i = i0 + lane;
+      const int e = i < R ? ids[i] : 0;
+      const bool first = i < R && lead[e] == i;
+      const uint32_t mk = first ? tmask[e] : 0u;
+      const uint32_t n = (uint32_t)__popc(mk);                 // 0 .. 16 rows
+      const uint32_t parts = (n + F::ROWS - 1) / F::ROWS;      // groups
+      int rb = rows, gb = ng;  // rows and groups of lower lanes, by bit planes
+      for (int b = 0; b < 5; ++b) {
+        const uint64_t pr = __ballot(n >> b & 1u), pg = __ballot(parts >> b & 1u);
+        rb += __popcll(pr & below) << b;
+        gb += __popcll(pg & below) << b;
+        rows += __popcll(pr) << b;
+        ng += __popcll(pg) << b;
       }
-      ng += r.wtot[w];
-      rows += r.wrow[w];
+      if (first) {
+        tmask[e] = mk | (uint32_t)rb << 16;  // for the weights
+        uint32_t left = mk;
+        for (int at = gb; left; ++at) {
+          uint32_t sub = 0;
+          for (int j = 0; j < F::ROWS && left; ++j) {
+            sub |= left & -left;
+            left &= left - 1u;
+          }
+          r.list[at] = (uint32_t)e | sub << 11;
+          r.base[at] = (uint16_t)rb;
+          rb += __popc(sub);
+        }
+      }
     }
-    if (mk) {
-      const int at = off + __popcll(bal & ((1ull << lane) - 1ull));
-      r.list[at] = (uint32_t)g | mk << 11;
-      r.base[at] = (uint16_t)(roff + incl - __popc(mk));
-      tmask[g] = mk | (uint32_t)at << 16;  // the expert's place in the list, for the next loop
+    if (lane == 0) {
+      r.groups = ng;
+      r.ready = r.left = 0;
     }
-    __syncthreads();
-  }
-  if (tid == 0) {
-    r.list[ng] = (uint32_t)E | ((1u << T) - 1u) << 11;
-    r.base[ng] = 0;
-  }
-  for (int i = tid; i < R; i += FW * 64) {
-    const uint32_t v = tmask[ids[i]];
-    r.w[r.base[v >> 16] + __popc(v & ((1u << (i / k)) - 1u))] = wts[i];
-  }
-  // ---- gate/up: items of 8 hidden columns, a wave each, claimed 8 at a time ----
-  const int slabs_sh = shared ? (f.Is + 7) / 8 : 0, slabs = (f.I + 7) / 8;
-  const int total = slabs_sh + ng * slabs;  // the shared expert's first: bf16, the largest
-  int done = 0;                             // items of this workgroup
-  for (;;) {
-    __syncthreads();  // (also: the routing scratch is read out before the stage is used)
-    if (tid == 0) r.next = atomicAdd(a.counters, FW);
-    __syncthreads();
-    const int first = r.next;
-    if (first >= total) break;
-    done += total - first < FW ? total - first : FW;
-    const int it = first + wave;
-    if (it < slabs_sh) {
-      stream_item<1, kWtPlain, true>(f, E, 0, 0, T, nullptr, it, lane, stage + wave * STAGE);
-    } else if (it < total) {
-      const int i = (it - slabs_sh) / slabs, slab = (it - slabs_sh) % slabs;
-      const uint32_t mk = r.list[i] >> 11;
-      stream_item<1, WT, true>(f, r.list[i] & 2047, 0, r.base[i], __popc(mk), nullptr, slab, lane,
-                               stage + wave * STAGE, mk);
+    __builtin_amdgcn_wave_barrier();
+    for (int i = lane; i < R; i += 64) {
+      const uint32_t v = tmask[ids[i]], row = (v >> 16) + __popc(v & ((1u << (i / k)) - 1u));
+      r.w[row] = wts[i];
+      r.token[row] = (uint8_t)(i / k);
     }
-  }
-  // ---- every h is written before the first down product reads one ----
-  // (every wave's stores have left before the barrier; the fence makes them
-  // visible to the device before they are counted)
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
-  if (tid == 0) {
-    if (done) {
-      __threadfence();
-      atomicAdd(a.counters + kFewCounterStride, done);
+  } else if (wave == 1 && blockIdx.x == 0) {
+    for (int i = lane; i < R; i += 64) {
+      if (a.ids) a.ids[i] = ids[i];
+      if (a.w) a.w[i] = wts[i];
     }
-    while (__hip_atomic_load(a.counters + kFewCounterStride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < total)
-      __builtin_amdgcn_s_sleep(1);
-    __threadfence();
   }
   __syncthreads();
-
-  // ---- down and combine: 16 output columns over all groups ----
-  const int q = lane >> 4, m = lane & 15;
-  const int nslab = (f.H + 15) / 16;
-  // units of the routed groups and of the shared expert
-  auto split = [&](int K) {
-    const int most = (K + kUnitK - 1) / kUnitK;
-    const int want = (2 * FW + ng - 1) / ng;  // units per group for two per wave
-    const int n = want < most ? want : most;
-    const int len = ((K + n - 1) / n + kUnitK - 1) / kUnitK * kUnitK;
-    return len;
+  const int ng = r.groups;
+  // ---- gate/up: slabs of 16 hidden columns ----
+  // Chunk c is slab c, wave c mod waves.  With fewer slabs than waves, P waves of
+  // a workgroup share a slab's K range: chunk c is then FW / P slabs, workgroup
+  // c mod grid.
+  const int slabs = a.slabs.d, total = ng * slabs, units = a.units, cols = a.cols;
+  int lp = 0;  // P = 1 << lp
+  while (1 << lp < FW && (total << (lp + 1)) <= waves + waves / 4 && 2 << lp <= units) ++lp;
+  const int P = 1 << lp;
+  const int lper = lp > 0 ? kLogFW - lp : 0;
+  const int chunks = (total + (1 << lper) - 1) >> lper;
+  // Finished slabs are counted in kFewDone counters, by the chunk's owner; the
+  // one that completes a counter adds to the last counter, which is watched.
+  const int l_own = lp > 0 ? 0 : kLogFW;  // chunk c counts in counter (c >> l_own) % kFewDone
+  auto counted = [&](int i) {        // slabs of counter i
+    const int all = chunks >> l_own, rest = chunks & ((1 << l_own) - 1);  // owners in full, chunks of the last
+    int n = ((all + kFewDone - 1 - i) / kFewDone) << l_own;
+    if (all % kFewDone == i) n += rest;
+    n <<= lper;
+    if (((chunks - 1) >> l_own) % kFewDone == i) n -= (chunks << lper) - total;
+    return n;
   };
-  const int len = split(f.I), per = (f.I + len - 1) / len;
-  const int len_sh = WT == kWtPlain ? (shared ? split(f.Is) : kUnitK) : kUnitK;
-  const int units_sh = shared ? (f.Is + len_sh - 1) / len_sh : 0;
-  const int units = units_sh + ng * per;
-  for (int s = blockIdx.x; s < nslab; s += gridDim.x) {
-    const int c0 = s * 16;
+  const int counters = (chunks + (1 << l_own) - 1) >> l_own < kFewDone ? (chunks + (1 << l_own) - 1) >> l_own : kFewDone;
+  int32_t* const last = a.counters + kFewDone * kFewCounterStride;
+  auto count = [&](int i, int n) {  // n finished slabs of counter i (one lane)
+    const int got = n + __hip_atomic_fetch_add(a.counters + i * kFewCounterStride, n, __ATOMIC_RELAXED,
+                                               __HIP_MEMORY_SCOPE_AGENT);
+    if (got == counted(i)) __hip_atomic_fetch_add(last, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  };
+  const int q = lane >> 4, m = lane & 15;
+  auto finish = [&](int s, const f32x4& gate, const f32x4& up) {  // lane: column m, group rows 4 q + v
+    int i, c0;
+    a.slabs.divide(s, i, c0);
+    const int rows = __popc(uniform(r.list[i]) >> 11), col = c0 * kSlab + m;
+    uint16_t* h = reinterpret_cast<uint16_t*>(f.h) + (int64_t)uniform(r.base[i]) * f.I + col;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (col < f.I && 4 * q + v < rows)  // written through to the device's memory
+        __hip_atomic_store(h + (int64_t)(4 * q + v) * f.I, __builtin_bit_cast(uint16_t, f2bf(silu(gate[v]) * up[v])),
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  };
+  // a chunk that nobody has claimed (then this wave has), or -1
+  auto find_open = [&] {
+    const int stride = P > 1 ? FW : 1;
+    for (int c0 = 0; c0 < chunks; c0 += 64) {
+      const bool open = c0 + lane < chunks && __hip_atomic_load(claims + (c0 + lane) * stride, __ATOMIC_RELAXED,
+                                                                __HIP_MEMORY_SCOPE_AGENT) == 0;
+      for (uint64_t bal = __ballot(open); bal; bal &= bal - 1) {
+        const int c = c0 + __builtin_ctzll(bal);
+        int got = 1;
+        if (lane == 0)
+          got = __hip_atomic_exchange(claims + c * stride, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (uniform((uint32_t)got) == 0u) return c;
+      }
+    }
+    return -1;
+  };
+  // A wave's own chunks first, claimed up to 64 at a time.  Then it says so, and
+  // wave 0 watches the last counter for its workgroup; every so often it looks
+  // for a chunk that nobody has claimed (its owner may not be resident while this
+  // workgroup holds its place) and does it alone, with the same arithmetic.
+  bool own = true;
+  int polls = 0, done = 0;  // done: slabs of this wave (P > 1: of this workgroup, in wave 0)
+  int c = P > 1 ? (int)blockIdx.x : gw;
+  const int step = P > 1 ? grid : waves;
+  for (;;) {
+    // the next jobs: parts [p0, p1) of slabs s, s + step (P == 1: those of a mask), one for P > 1
+    uint64_t todo = 1;
+    int s, end, p0 = 0, p1 = P;
+    if (own && c < chunks) {
+      s = c << lper;
+      end = total;
+      if (P > 1) {
+        // (a workgroup's chunk has the flag claims[c * FW])
+        if (tid == 0)
+          r.claim = __hip_atomic_exchange(claims + c * FW, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        const bool mine = uniform((uint32_t)r.claim) == 0u;
+        __syncthreads();
+        c += grid;
+        if (!mine) continue;
+        end = s + (1 << lper) < total ? s + (1 << lper) : total;
+        if (wave == 0) done += end - s;
+        s += wave >> lp;
+        end = s < end ? s + 1 : s;
+        p0 = wave & (P - 1);
+        p1 = p0 + 1;
+        if (s >= end) todo = 0;
+      } else {
+        const int at = c + lane * waves;
+        int taken = 1;
+        if (at < chunks)
+          taken = __hip_atomic_exchange(claims + at, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        todo = __ballot(taken == 0);
+        done += __popcll(todo);
+        c += 64 * waves;
+      }
+    } else if (own) {
+      // Stores of h are written through, and acknowledged before they are
+      // counted; the workgroup's last wave adds its slabs to one of the counters
+      // (one counter for 256 workgroups took 2.9 us, a fence that writes the L2
+      // back 1.4 us).
+      own = false;
+      __builtin_amdgcn_s_waitcnt(0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (lane == 0) {
+        const int before =
+            __hip_atomic_fetch_add(&r.left, done << 8 | 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_WORKGROUP);
+        if ((before & 255) == FW - 1 && (before >> 8) + done > 0)
+          count((int)blockIdx.x % kFewDone, (before >> 8) + done);
+      }
+      if (wave != 0 || (int)blockIdx.x * cols >= f.H) break;  // (no down columns: nothing to wait for)
+      continue;
+    } else {
+      if (__hip_atomic_load(last, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >= counters) break;
+      int open = -1;
+      if (++polls % kHelpAfter == 0) open = find_open();
+      if (open < 0) {
+        __builtin_amdgcn_s_sleep(1);
+        continue;
+      }
+      s = open << lper;
+      end = s + (1 << lper) < total ? s + (1 << lper) : total;
+    }
+    const int first = s;
+    int p = p0, parts = 0;
+    f32x4 v[2] = {};
+    fragdot::run<WT, 2, 0>(
+        f.x, (uint32_t)T * (uint32_t)f.H * 2u, f.H, lane, act[wave],
+        [&](auto& j) {
+          if (!todo) return false;
+          int at = s;
+          if (P == 1) {
+            at += __builtin_ctzll(todo) * waves;
+            todo &= todo - 1;
+          }
+          int i, c0;
+          a.slabs.divide(at, i, c0);
+          c0 *= kSlab;
+          const uint32_t entry = uniform(r.list[i]);
+          const int g = entry & 2047;
+          const int left = f.I - c0 < kSlab ? f.I - c0 : kSlab;
+          j.w[0] = static_cast<const char*>(f.wg) + fragdot::wbytes<WT>((int64_t)g * f.sg + (int64_t)c0 * f.H);
+          j.w[2] = static_cast<const char*>(f.wu) + fragdot::wbytes<WT>((int64_t)g * f.su + (int64_t)c0 * f.H);
+          j.w[1] = j.w[0] + fragdot::wbytes<WT>(8 * (int64_t)f.H);
+          j.w[3] = j.w[2] + fragdot::wbytes<WT>(8 * (int64_t)f.H);
+          j.wrows[0] = j.wrows[2] = left < 8 ? left : 8;
+          j.wrows[1] = j.wrows[3] = left < 8 ? 0 : left - 8;
+          if constexpr (WT != kWtPlain) {
+            const int n = WT == kWtMx ? lane >> 2 : m;
+            const int col = c0 + (n < left ? n : left - 1);
+            const int64_t at = WT == kWtFp8 ? ((int64_t)g * (f.I / 128) + col / 128) * (f.H / 128) * 4
+                                            : ((int64_t)g * f.I + col) * (f.H / 32);
+            j.scale[0] = static_cast<const char*>(f.scg) + at;
+            j.scale[1] = static_cast<const char*>(f.scu) + at;
+          }
+          j.pick = r.token + uniform(r.base[i]);
+          j.rows = __popc(entry >> 11);
+          j.ar = m < j.rows ? m : 0;
+          j.k0 = ((p * units) >> lp) * kUnitK;
+          const int ke = (((p + 1) * units) >> lp) * kUnitK;
+          j.kend = ke < f.H ? ke : f.H;
+          j.tag = at;
+          if (P > 1 && ++p == p1) {
+            p = p0;
+            if (++s >= end) todo = 0;
+          }
+          return true;
+        },
+        [&](int at, const f32x4 (&acc)[2]) {
+          v[0] += acc[0];  // (parts of one slab follow each other in K order)
+          v[1] += acc[1];
+          if ((P > 1 && own) || ++parts < P) return;
+          parts = 0;
+          finish(at, v[0], v[1]);
+          v[0] = v[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        },
+        NoGate{});
+    if (own && P > 1) {
+      part[wave][0][lane] = v[0];  // added in K order
+      part[wave][1][lane] = v[1];
+      __syncthreads();
+      if (first < end && p0 == 0) {
+        for (int w = 1; w < P; ++w) {
+          v[0] += part[wave + w][0][lane];
+          v[1] += part[wave + w][1][lane];
+        }
+        finish(first, v[0], v[1]);
+      }
+      __syncthreads();
+    }
+    if (!own) {
+      __builtin_amdgcn_s_waitcnt(0);
+      if (lane == 0) count(((first >> lper) >> l_own) % kFewDone, end - first);
+    }
+  }
+  // every h is written: wave 0 knows, the others ask before their first activations
+  if (tid == 0) __hip_atomic_store(&r.ready, 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
+  auto gate = [&] {
+    while (!__hip_atomic_load(&r.ready, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP)) __builtin_amdgcn_s_sleep(1);
+  };
+
+  // ---- down and combine: up to 16 output columns over all groups ----
+  // units of 128 K values: the shared expert's (bf16, weighed by their size), then the groups'
+  constexpr int kWeigh = WT == kWtMx ? 4 : WT == kWtFp8 ? 2 : 1;  // a bf16 unit in units of this type
+  const int ud = a.down_units.d, u_sh = a.shared_units;
+  const int u_all = u_sh * kWeigh + ng * ud;
+  const int lo = (u_all * wave) >> kLogFW, hi = (u_all * (wave + 1)) >> kLogFW;
+  for (int c0 = (int)blockIdx.x * cols; c0 < f.H; c0 += grid * cols) {
+    const int ncol = f.H - c0 < cols ? f.H - c0 : cols;
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-    for (int u = wave; u < units; u += FW) {
-      const bool sh = u < units_sh;
-      const int i = sh ? ng : (u - units_sh) / per;
-      const int kbeg = sh ? u * len_sh : ((u - units_sh) % per) * len;
-      const int K = sh ? f.Is : f.I;
-      const int kend = kbeg + (sh ? len_sh : len) < K ? kbeg + (sh ? len_sh : len) : K;
-      const int mk = (int)(r.list[i] >> 11), base = r.base[i];
-      const bf16* h = reinterpret_cast<const bf16*>(sh ? f.h_sh : f.h);
-      const bool in = m < T && (mk >> m & 1);
-      const bf16* a_row = in ? h + (int64_t)(base + __popc(mk & ((1 << m) - 1))) * K : nullptr;
-      const f32x4 p = sh ? down_dot<kWtPlain>(f, E, a_row, h, c0, K, kbeg, kend, lane, stage + wave * STAGE)
-                         : down_dot<WT>(f, r.list[i] & 2047, a_row, h, c0, K, kbeg, kend, lane, stage + wave * STAGE);
+    auto add = [&](bool sh, uint32_t mask, int base, const f32x4& p) {
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const int t = 4 * q + v;
-        if (mk >> t & 1) sum[v] = fmaf(sh ? r.sg[t] : r.w[base + __popc(mk & ((1 << t) - 1))], p[v], sum[v]);
+        if (mask >> t & 1u) sum[v] = fmaf(sh ? r.sg[t] : r.w[base + __popc(mask & ((1u << t) - 1u))], p[v], sum[v]);
       }
-    }
-    __syncthreads();
-    f32x4* part = reinterpret_cast<f32x4*>(stage);
-    part[wave * 64 + lane] = sum;
+    };
+    auto rows_of = [&](auto& j) {  // w[0] is the first column's row
+      j.wrows[0] = ncol < 8 ? ncol : 8;
+      j.wrows[1] = ncol < 8 ? 0 : ncol - 8;
+    };
+    int u = lo > u_sh * kWeigh ? lo - u_sh * kWeigh : 0;
+    const int r_hi = hi - u_sh * kWeigh;
+    fragdot::run<WT, 1, fragdot::kSc1>(
+        f.h, (uint32_t)R * (uint32_t)f.I * 2u, f.I, lane, act[wave],
+        [&](auto& j) {
+          if (u >= r_hi) return false;
+          int i, u0;
+          a.down_units.divide(u, i, u0);
+          const int u1 = r_hi - u + u0 < ud ? r_hi - u + u0 : ud;
+          const uint32_t entry = uniform(r.list[i]);
+          const int g = entry & 2047;
+          j.w[0] = static_cast<const char*>(f.wd) + fragdot::wbytes<WT>((int64_t)g * f.sd + (int64_t)c0 * f.I);
+          j.w[1] = j.w[0] + fragdot::wbytes<WT>(8 * (int64_t)f.I);
+          rows_of(j);
+          auto scale_row = [&](int n) {
+            const int col = c0 + (n < ncol ? n : ncol - 1);
+            return WT == kWtFp8 ? static_cast<const void*>(static_cast<const float*>(f.scd) +
+                                                           ((int64_t)g * (f.H / 128) + col / 128) * (f.I / 128))
+                                : static_cast<const void*>(static_cast<const uint8_t*>(f.scd) +
+                                                           ((int64_t)g * f.H + col) * (f.I / 32));
+          };
+          if constexpr (WT != kWtPlain) j.scale[0] = scale_row(WT == kWtMx ? lane >> 2 : m);
+          // fragment row m is token m (a token without this expert reads some row of it; its sum is not used)
+          const uint32_t mask = entry >> 11;
+          const int rank = __popc(mask & ((1u << m) - 1u));
+          j.base = (int)uniform(r.base[i]);
+          j.rows = __popc(mask);
+          j.ar = rank < j.rows ? rank : j.rows - 1;
+          j.k0 = u0 * kUnitK;
+          j.kend = u1 * kUnitK < f.I ? u1 * kUnitK : f.I;
+          j.tag = i;
+          u += u1 - u0;
+          return true;
+        },
+        [&](int i, const f32x4 (&acc)[1]) { add(false, uniform(r.list[i]) >> 11, (int)uniform(r.base[i]), acc[0]); },
+        gate);
+    const int s_lo = lo / kWeigh, s_hi = hi < u_sh * kWeigh ? hi / kWeigh : u_sh;
+    bool todo = s_lo < s_hi;
+    fragdot::run<kWtPlain, 1, 0>(  // (h_sh is the first kernel's)
+        f.h_sh, (uint32_t)T * (uint32_t)f.Is * 2u, f.Is, lane, act[wave],
+        [&](auto& j) {
+          if (!todo) return false;
+          todo = false;
+          j.w[0] = static_cast<const char*>(f.shd) + (int64_t)c0 * f.Is * 2;
+          j.w[1] = j.w[0] + 16 * (int64_t)f.Is;
+          rows_of(j);
+          j.rows = T;
+          j.ar = m < T ? m : 0;
+          j.k0 = s_lo * kUnitK;
+          j.kend = s_hi * kUnitK < f.Is ? s_hi * kUnitK : f.Is;
+          return true;
+        },
+        [&](int, const f32x4 (&acc)[1]) { add(true, (1u << T) - 1u, 0, acc[0]); }, NoGate{});
+    part[wave][0][lane] = sum;
     __syncthreads();
     if (wave == 0) {
-      f32x4 t = part[lane];
 #pragma unroll
-      for (int w = 1; w < FW; ++w) t += part[w * 64 + lane];
+      for (int w = 1; w < FW; ++w) sum += part[w][0][lane];
       bf16* out = reinterpret_cast<bf16*>(a.out);
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        if (4 * q + v < T && c0 + m < f.H) out[(int64_t)(4 * q + v) * f.H + c0 + m] = f2bf(t[v]);
+        if (4 * q + v < T && m < ncol) out[(int64_t)(4 * q + v) * f.H + c0 + m] = f2bf(sum[v]);
     }
     __syncthreads();
   }
@@ -322,16 +632,32 @@ int few_cus() {
 
 }  // namespace
 
-hipError_t launch_layer_few(const FfnArgs& f, const void* w_router, const void* w_sg, const FewArgs& a, hipStream_t s) {
+size_t few_counter_ints(int64_t T, int64_t k, int64_t I) {
+  // done counters, then a claim flag per wave chunk: of one slab or more each,
+  // or FW flags per workgroup chunk where those are fewer than the waves
+  const int64_t slabs = T * k * ((I + kSlab - 1) / kSlab), least = (int64_t)2 * kFewMaxGrid * FW;
+  return (size_t)((kFewDone + 1) * kFewCounterStride + (slabs > least ? slabs : least));
+}
+
+hipError_t launch_layer_few(const FfnArgs& f, const void* w_router, const void* w_sg, FewArgs a, hipStream_t s) {
   if (f.T < 1 || f.T > kSmallBatch || f.E > kMaxExperts || f.k > 64) return hipErrorInvalidValue;
   const int N = f.E + (a.has_shared ? 1 : 0);
-  const int kchunk = ((f.H + RWF - 1) / RWF + KSTEP - 1) / KSTEP * KSTEP;
-  few_router_kernel<<<(N + 15) / 16, RWF * 64, 0, s>>>(
+  const int kchunk = ((f.H + RW - 1) / RW + 31) / 32 * 32;
+  const int nr = (f.E + 15) / 16, nsh = a.has_shared ? 1 + (f.Is + 7) / 8 : 0;
+  few_router_kernel<<<nr + nsh, RW * 64, 0, s>>>(
       reinterpret_cast<const bf16*>(f.x), reinterpret_cast<const bf16*>(w_router), reinterpret_cast<const bf16*>(w_sg),
-      a.logits, f.T, f.H, f.E, N, kchunk, a.counters);
+      a.logits, f.T, f.H, f.E, N, nr, reinterpret_cast<const bf16*>(f.shg), reinterpret_cast<const bf16*>(f.shu), f.Is,
+      reinterpret_cast<bf16*>(f.h_sh), kchunk, a.counters, (int)few_counter_ints(f.T, f.k, f.I));
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int grid = few_cus();
+  // a workgroup per compute unit, a multiple of kFewDone
+  int grid = (few_cus() < kFewMaxGrid ? few_cus() : kFewMaxGrid) / kFewDone * kFewDone;
+  grid = grid < kFewDone ? kFewDone : grid;
+  a.slabs = FewDivisor((f.I + kSlab - 1) / kSlab);
+  a.units = (f.H + kUnitK - 1) / kUnitK;
+  a.cols = (f.H + grid - 1) / grid < 16 ? (f.H + grid - 1) / grid : 16;
+  a.down_units = FewDivisor((f.I + kUnitK - 1) / kUnitK);
+  a.shared_units = a.has_shared ? (f.Is + kUnitK - 1) / kUnitK : 0;
   if (f.wt == kWtFp8) few_experts_kernel<kWtFp8><<<grid, FW * 64, 0, s>>>(f, a);
   else if (f.wt == kWtMx) few_experts_kernel<kWtMx><<<grid, FW * 64, 0, s>>>(f, a);
   else few_experts_kernel<kWtPlain><<<grid, FW * 64, 0, s>>>(f, a);

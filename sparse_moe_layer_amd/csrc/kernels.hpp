@@ -156,6 +156,22 @@ moe_status layer_forward_checks(const moe_problem* p, const moe_weights* w, cons
 moe_status layer_forward_run(const moe_problem* p, const moe_weights* w, const void* x, void* out,
                              int32_t* topk_ids, float* topk_w, void* ws, hipStream_t s, bool fork_ok = true);
 
+// Division by a size known to the host: floor(x / d) and the remainder for
+// 0 <= x < 2^31 through the high word of x * ceil(2^32 / d), which is at most
+// one off.
+struct FewDivisor {
+  int d = 1;
+  uint32_t inv = 0xFFFFFFFFu;
+  FewDivisor() = default;
+  explicit FewDivisor(int n) : d(n), inv(n > 1 ? 0xFFFFFFFFu / (uint32_t)n + 1u : 0xFFFFFFFFu) {}
+  __device__ void divide(int x, int& q, int& r) const {
+    q = (int)__umulhi((uint32_t)x, inv);
+    r = x - q * d;
+    if (r < 0) --q, r += d;
+    if (r >= d) ++q, r -= d;
+  }
+};
+
 // The layer for a few tokens (T <= kSmallBatch, bf16 activations) in two
 // kernels: arguments of the second one.
 struct FewArgs {
@@ -165,11 +181,17 @@ struct FewArgs {
   int32_t* ids;          // [T, k] or null
   float* w;              // [T, k] or null
   void* out;             // [T, H] bf16
-  int32_t* counters;     // two words kFewCounterStride ints apart: items claimed, items done
+  int32_t* counters;     // few_counter_ints words, zeroed by the first kernel
+  // sizes, filled in by the launcher
+  FewDivisor slabs;       // slabs of 16 hidden columns per group
+  FewDivisor down_units;  // units of K of a group's down rows
+  int units, shared_units, cols;  // units of the gate/up K and of the shared expert's; output columns at a time
 };
-constexpr int kFewCounterStride = 64;
+constexpr int kFewDone = 16, kFewCounterStride = 64;  // done counters, ints apart
+constexpr int kFewMaxGrid = 512;
+size_t few_counter_ints(int64_t T, int64_t k, int64_t I);
 // f.h [T*k, I] and f.h_sh [T, Is] are scratch; f.offsets and f.sorted are not used.
-hipError_t launch_layer_few(const FfnArgs& f, const void* w_router, const void* w_sg, const FewArgs& a, hipStream_t s);
+hipError_t launch_layer_few(const FfnArgs& f, const void* w_router, const void* w_sg, FewArgs a, hipStream_t s);
 
 // MXFP4 weights: rows of K values (bf16, or fp32 with f32) to codes and E8M0
 // scales, and back to bf16.
