@@ -238,9 +238,9 @@ FfnArgs ffn_args(const moe_problem* p, const moe_weights* w, const void* x, cons
   a.sg = w->stride_gate ? w->stride_gate : p->I * p->H;
   a.su = w->stride_up ? w->stride_up : p->I * p->H;
   a.sd = w->stride_down ? w->stride_down : p->H * p->I;
-  a.scg = w->s_gate;
-  a.scu = w->s_up;
-  a.scd = w->s_down;
+  a.scg = static_cast<const float*>(w->s_gate);
+  a.scu = static_cast<const float*>(w->s_up);
+  a.scd = static_cast<const float*>(w->s_down);
   a.shg = w->sh_gate;
   a.shu = w->sh_up;
   a.shd = w->sh_down;

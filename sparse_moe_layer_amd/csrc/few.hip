@@ -38,6 +38,7 @@ namespace moe {
 namespace {
 
 using fragdot::Job;
+using fragdot::BaseRows;
 using fragdot::NoGate;
 
 constexpr int RW = 16;                       // waves per workgroup of the router kernel
@@ -91,7 +92,7 @@ __global__ __launch_bounds__(RW * 64) void few_router_kernel(const bf16* __restr
   bool todo = kbeg < kend;
   part[w][lane] = f32x4{0.f, 0.f, 0.f, 0.f};
   fragdot::run<kWtPlain, 1, 0>(
-      x, (uint32_t)T * (uint32_t)H * 2u, H, lane, act[w],
+      x, (uint32_t)T * (uint32_t)H * 2u, H, lane, act[w], BaseRows{},
       [&](Job<1>& j) {
         if (todo) j = b;
         const bool was = todo;
@@ -393,7 +394,6 @@ __global__ __launch_bounds__(FW * 64, 2) void few_experts_kernel(FfnArgs f, FewA
   bool own = true;
   int polls = 0, done = 0;  // done: slabs of this wave (P > 1: of this workgroup, in wave 0)
   int c = P > 1 ? (int)blockIdx.x : gw;
-  const int step = P > 1 ? grid : waves;
   for (;;) {
     // the next jobs: parts [p0, p1) of slabs s, s + step (P == 1: those of a mask), one for P > 1
     uint64_t todo = 1;
@@ -458,6 +458,7 @@ __global__ __launch_bounds__(FW * 64, 2) void few_experts_kernel(FfnArgs f, FewA
     f32x4 v[2] = {};
     fragdot::run<WT, 2, 0>(
         f.x, (uint32_t)T * (uint32_t)f.H * 2u, f.H, lane, act[wave],
+        [&](const auto& j, int row) { return (int)r.token[j.base + row]; },
         [&](auto& j) {
           if (!todo) return false;
           int at = s;
@@ -482,10 +483,10 @@ __global__ __launch_bounds__(FW * 64, 2) void few_experts_kernel(FfnArgs f, FewA
             const int col = c0 + (n < left ? n : left - 1);
             const int64_t at = WT == kWtFp8 ? ((int64_t)g * (f.I / 128) + col / 128) * (f.H / 128) * 4
                                             : ((int64_t)g * f.I + col) * (f.H / 32);
-            j.scale[0] = static_cast<const char*>(f.scg) + at;
-            j.scale[1] = static_cast<const char*>(f.scu) + at;
+            j.scale[0] = reinterpret_cast<const char*>(f.scg) + at;
+            j.scale[1] = reinterpret_cast<const char*>(f.scu) + at;
           }
-          j.pick = r.token + uniform(r.base[i]);
+          j.base = (int)uniform(r.base[i]);
           j.rows = __popc(entry >> 11);
           j.ar = m < j.rows ? m : 0;
           j.k0 = ((p * units) >> lp) * kUnitK;
@@ -554,7 +555,7 @@ __global__ __launch_bounds__(FW * 64, 2) void few_experts_kernel(FfnArgs f, FewA
     int u = lo > u_sh * kWeigh ? lo - u_sh * kWeigh : 0;
     const int r_hi = hi - u_sh * kWeigh;
     fragdot::run<WT, 1, fragdot::kSc1>(
-        f.h, (uint32_t)R * (uint32_t)f.I * 2u, f.I, lane, act[wave],
+        f.h, (uint32_t)R * (uint32_t)f.I * 2u, f.I, lane, act[wave], BaseRows{},
         [&](auto& j) {
           if (u >= r_hi) return false;
           int i, u0;
@@ -567,9 +568,9 @@ __global__ __launch_bounds__(FW * 64, 2) void few_experts_kernel(FfnArgs f, FewA
           rows_of(j);
           auto scale_row = [&](int n) {
             const int col = c0 + (n < ncol ? n : ncol - 1);
-            return WT == kWtFp8 ? static_cast<const void*>(static_cast<const float*>(f.scd) +
+            return WT == kWtFp8 ? static_cast<const void*>(f.scd +
                                                            ((int64_t)g * (f.H / 128) + col / 128) * (f.I / 128))
-                                : static_cast<const void*>(static_cast<const uint8_t*>(f.scd) +
+                                : static_cast<const void*>(reinterpret_cast<const uint8_t*>(f.scd) +
                                                            ((int64_t)g * f.H + col) * (f.I / 32));
           };
           if constexpr (WT != kWtPlain) j.scale[0] = scale_row(WT == kWtMx ? lane >> 2 : m);
@@ -590,7 +591,7 @@ __global__ __launch_bounds__(FW * 64, 2) void few_experts_kernel(FfnArgs f, FewA
     const int s_lo = lo / kWeigh, s_hi = hi < u_sh * kWeigh ? hi / kWeigh : u_sh;
     bool todo = s_lo < s_hi;
     fragdot::run<kWtPlain, 1, 0>(  // (h_sh is the first kernel's)
-        f.h_sh, (uint32_t)T * (uint32_t)f.Is * 2u, f.Is, lane, act[wave],
+        f.h_sh, (uint32_t)T * (uint32_t)f.Is * 2u, f.Is, lane, act[wave], BaseRows{},
         [&](auto& j) {
           if (!todo) return false;
           todo = false;
@@ -653,10 +654,10 @@ hipError_t launch_layer_few(const FfnArgs& f, const void* w_router, const void* 
   // a workgroup per compute unit, a multiple of kFewDone
   int grid = (few_cus() < kFewMaxGrid ? few_cus() : kFewMaxGrid) / kFewDone * kFewDone;
   grid = grid < kFewDone ? kFewDone : grid;
-  a.slabs = FewDivisor((f.I + kSlab - 1) / kSlab);
+  a.slabs = Divisor((f.I + kSlab - 1) / kSlab);
   a.units = (f.H + kUnitK - 1) / kUnitK;
   a.cols = (f.H + grid - 1) / grid < 16 ? (f.H + grid - 1) / grid : 16;
-  a.down_units = FewDivisor((f.I + kUnitK - 1) / kUnitK);
+  a.down_units = Divisor((f.I + kUnitK - 1) / kUnitK);
   a.shared_units = a.has_shared ? (f.Is + kUnitK - 1) / kUnitK : 0;
   if (f.wt == kWtFp8) few_experts_kernel<kWtFp8><<<grid, FW * 64, 0, s>>>(f, a);
   else if (f.wt == kWtMx) few_experts_kernel<kWtMx><<<grid, FW * 64, 0, s>>>(f, a);

@@ -34,17 +34,21 @@ namespace fragdot {
 constexpr int kSc1 = 16;             // cache policy: coherent across the device's L2 caches
 constexpr int kNt = 2;               // non-temporal
 constexpr int kRunBytes = 256;       // of a weight row
-constexpr int kBuf = 16 * kRunBytes;  // a wave's buffer: a run of 16 rows, or activation rows
-constexpr int kLds = kBuf + 256;     // and 16 scale bytes of 16 rows (MXFP4)
+constexpr int kBuf = 16 * kRunBytes;  // a run of 16 rows
+constexpr int kLds = kBuf + 256;      // a wave's buffer, with 16 scale bytes of 16 rows (MXFP4)
 
-template <int WT>
+// AROWS: the most activation rows of a job; 0: as many as fit a run of 16 weight rows.
+template <int WT, int AROWS = 0>
 struct Form {
   static constexpr int G = WT == kWtMx ? 32 : WT == kWtFp8 ? 16 : 8;  // values per 16-byte chunk
   static constexpr int U = 4;                                         // chunks per lane and batch
   static constexpr int KB = 4 * G * U;                                // K values per batch: 128, 256, 512
-  static constexpr int ROWS = kBuf / (2 * KB);                        // activation rows that fit: 16, 8, 4
+  static constexpr int ROWS = AROWS ? AROWS : kBuf / (2 * KB);        // 0: 16, 8, 4
   static constexpr int RPL = 512 / KB;                                // rows per load of them: 4, 2, 1
-  static constexpr int NL = ROWS / RPL;                               // loads of all of them: 4
+  static constexpr int NL = ROWS / RPL;                               // loads of all of them: 4 (0)
+  static constexpr int BUF = 2 * KB * ROWS;                           // bytes of them
+  static constexpr int LDS = BUF + 256;
+  static_assert(BUF >= kBuf, "the weights pass through the same buffer");
   static constexpr int NS = WT == kWtMx ? 2 : KB / 128;               // scale registers of a batch
 };
 
@@ -62,36 +66,38 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* p, uint32
 struct NoGate {
   __device__ void operator()() const {}
 };
+struct BaseRows {
+  template <class J>
+  __device__ int operator()(const J& j, int r) const { return j.base + r; }
+};
 
 // NB blocks of 16 weight rows of K values over [k0, kend): rows 0-7 of block b
 // from w[2 b] on, rows 8-15 from w[2 b + 1] on, of which there are wrows[2 b + h]
 // in each half (the others read as zeros).  scale[b]: MXFP4, the scale bytes of
 // row lane / 4 (of a row there is); fp8, the scales of this lane's fragment row
 // lane % 16, by K / 128.
-// Activations: `rows` <= ROWS rows, the r-th at
-// index pick[r], or base + r without a pick; this lane's fragment row is row ar <
-// rows of them (results of rows that mean nothing are not used).
+// Activations: `rows` <= ROWS rows; this lane's fragment row is row ar < rows of
+// them (results of rows that mean nothing are not used).
 template <int NB>
 struct Job {
   const char* w[2 * NB];
   int wrows[2 * NB];
   const void* scale[NB];
-  const uint8_t* pick;
-  int base, rows, ar;
+  int base, rows, ar;  // base: for the caller's row_of
   int k0, kend;
   int tag;  // for the caller
 };
 
 // Runs the jobs that next(Job&) gives until it returns false, and after(tag,
 // acc) with each one's products A [16 rows] x W [16 rows]^T, NB blocks.  abase: the
-// activation rows, K values each, `abytes` in all.  k0 is a multiple of 128, K of
-// 128 (fp8), 32 (MXFP4) or 8.  lds: the wave's kLds bytes.  gate(): called once
-// if there is a job, after the first weights have been asked for and before any
-// activation is.
-template <int WT, int NB, int AUXA, class Next, class After, class Gate>
-__device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, int lane, char* lds, Next next,
-                                    After after, Gate gate) {
-  using F = Form<WT>;
+// activation rows, K values each, `abytes` in all; row_of(job, r) is the index of
+// a job's row r < rows.  k0 is a multiple of 128, K of 128 (fp8), 32 (MXFP4) or 8.
+// lds: the wave's Form::LDS bytes.  gate(): called once if there is a job, after
+// the first weights have been asked for and before any activation is.
+template <int WT, int NB, int AUXA, int AROWS = 0, class Rows, class Next, class After, class Gate>
+__device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, int lane, char* lds, Rows row_of,
+                                    Next next, After after, Gate gate) {
+  using F = Form<WT, AROWS>;
   constexpr int G = F::G, U = F::U;
   constexpr uint32_t kNone = 0x80000000u;  // past any of the buffers below: reads as zeros, fetches nothing
   constexpr int LPR = 64 / F::RPL;         // lanes per activation row
@@ -127,9 +133,9 @@ __device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, i
         for (int u = 0; u < U; ++u)
           wv[b][u] = *reinterpret_cast<const u32x4*>(lds + n * kRunBytes + (((4 * u + q) ^ n) << 4));
         if constexpr (WT == kWtMx) {
-          *reinterpret_cast<uint32_t*>(lds + kBuf + lane * 4) =
+          *reinterpret_cast<uint32_t*>(lds + F::BUF + lane * 4) =
               __builtin_amdgcn_alignbyte(sd[b][1], sd[b][0], shift[b]);
-          const u32x4 s = *reinterpret_cast<const u32x4*>(lds + kBuf + n * 16);
+          const u32x4 s = *reinterpret_cast<const u32x4*>(lds + F::BUF + n * 16);
 #pragma unroll
           for (int u = 0; u < U; ++u) sv[b][u] = (s[u] >> (8 * q)) & 255u;
           if (c_kb + F::KB > K) {  // what lies behind the row's scales is not one of them
@@ -198,7 +204,7 @@ __device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, i
           if (i * F::RPL < job.rows) {
             const int r = i * F::RPL + lane / LPR;
             const int at = r < job.rows ? r : 0;
-            aoff[i] = r < job.rows ? (uint32_t)(job.pick ? job.pick[at] : job.base + at) * (uint32_t)K * 2u +
+            aoff[i] = r < job.rows ? (uint32_t)row_of(job, at) * (uint32_t)K * 2u +
                                          16u * (uint32_t)(lane % LPR)
                                    : kNone;
           }

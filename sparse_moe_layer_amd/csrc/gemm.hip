@@ -15,8 +15,8 @@
 // so SiLU(g)*u is formed in registers.  Work is a device-built list of
 // (group, first row) m-tiles; the grid is persistent and walks
 // m-tile x n-tile indices, so no host sync is needed to size it.
-// fp8 and MXFP4 routed weights are decoded to bf16 on their way into LDS
-// (fp8: OCP e4m3fn x fp32 block scale; MXFP4: e2m1 x power of two, exactly).
+// fp8 routed weights are decoded (OCP e4m3fn x fp32 block scale -> bf16) on
+// their way into LDS.
 #include <type_traits>
 
 #include "common.hpp"
@@ -60,11 +60,10 @@ __device__ __forceinline__ int lds_off(int r, int c) {
 // (0: the layer; 1: the gated residual's read projection).  BKT is the K step:
 // 64 (two 64 KB LDS buffers, two workgroups per CU) or 32 (bf16 only: 32 KB,
 // three workgroups per CU).
-template <int MODE, int WT, int USE = 0, int BKT = 64>
+template <int MODE, bool FP8, int USE = 0, int BKT = 64>
 __global__ __launch_bounds__(NT, BKT == 32 ? 3 : 2) void gemm_kernel(FfnArgs f, RouterArgs ra, int n_tiles_n,
                                                      int list_begin_idx, int list_end_idx) {
-  constexpr bool FP8 = WT == kWtFp8, MX = WT == kWtMx;
-  static_assert(WT == kWtPlain || BKT == 64, "fp8 and MXFP4 tiles use the 64-wide K step");
+  static_assert(!FP8 || BKT == 64, "fp8 tiles use the 64-wide K step");
   constexpr int CPR = BKT / 8;     // 16-byte chunks per LDS row
   constexpr int RSTEP = NT / CPR;  // rows covered by one pass of the workgroup
   constexpr int NPASS = BM / RSTEP;
@@ -131,7 +130,7 @@ __global__ __launch_bounds__(NT, BKT == 32 ? 3 : 2) void gemm_kernel(FfnArgs f, 
     }
     nrows = nrows < BM ? nrows : BM;
     const bool shared = (MODE != M_ROUTER) && g >= f.E;
-    const bool fp8_tile = FP8 && !shared;  // (fp8 and MXFP4 launches cover routed tiles only)
+    const bool fp8_tile = FP8 && !shared;
     // n-tile coverage: GATEUP covers 64 hidden columns per tile, others 128.
     const int ncov = (MODE == M_GATEUP) ? 64 : BN;
     if (nt * ncov >= Ncols) continue;  // uniform across the block
@@ -157,16 +156,14 @@ __global__ __launch_bounds__(NT, BKT == 32 ? 3 : 2) void gemm_kernel(FfnArgs f, 
       }
     }
     // B rows: bf16 layout uses rows tid/CPR + RSTEP*i, chunk tid%CPR (NPASS
-    // chunks); fp8 layout uses rows (tid>>2)+64i, 16-code chunk tid&3 (2 chunks);
-    // MXFP4 row tid>>1, 32-code chunk tid&1 (one chunk: one scale group).
+    // chunks); fp8 layout uses rows (tid>>2)+64i, 16-code chunk tid&3 (2 chunks).
     const void* b_ptr[4];
     const float* s_ptr[4];
-    const uint8_t* mx_scale = nullptr;  // MXFP4: this thread's row of scale bytes
-    const int nb = MX ? 1 : fp8_tile ? 2 : NPASS;
+    const int nb = fp8_tile ? 2 : NPASS;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (i >= nb) { b_ptr[i] = nullptr; s_ptr[i] = nullptr; continue; }
-      const int n = MX ? tid >> 1 : fp8_tile ? (tid >> 2) + 64 * i : tid / CPR + RSTEP * i;
+      const int n = fp8_tile ? (tid >> 2) + 64 * i : tid / CPR + RSTEP * i;
       int col;  // matrix row of the weight (output column)
       bool up = false;
       if (MODE == M_GATEUP) {
@@ -184,17 +181,11 @@ __global__ __launch_bounds__(NT, BKT == 32 ? 3 : 2) void gemm_kernel(FfnArgs f, 
         if (shared) {
           b_ptr[i] = reinterpret_cast<const bf16*>(up ? f.shu : f.shg) + (int64_t)col * f.H;
           s_ptr[i] = nullptr;
-        } else if (MX) {
-          b_ptr[i] = reinterpret_cast<const uint8_t*>(up ? f.wu : f.wg) +
-                     ((int64_t)g * (up ? f.su : f.sg) + (int64_t)col * f.H) / 2;
-          s_ptr[i] = nullptr;
-          mx_scale = reinterpret_cast<const uint8_t*>(up ? f.scu : f.scg) + ((int64_t)g * f.I + col) * (f.H / 32);
         } else if (fp8_tile) {
           b_ptr[i] = reinterpret_cast<const uint8_t*>(up ? f.wu : f.wg) + (int64_t)g * (up ? f.su : f.sg) +
                      (int64_t)col * f.H;
           const int kb = f.H / 128;
-          s_ptr[i] = reinterpret_cast<const float*>(up ? f.scu : f.scg) + (int64_t)g * (f.I / 128) * kb +
-                     (col / 128) * kb;
+          s_ptr[i] = (up ? f.scu : f.scg) + (int64_t)g * (f.I / 128) * kb + (col / 128) * kb;
         } else {
           b_ptr[i] = reinterpret_cast<const bf16*>(up ? f.wu : f.wg) + (int64_t)g * (up ? f.su : f.sg) +
                      (int64_t)col * f.H;
@@ -204,14 +195,10 @@ __global__ __launch_bounds__(NT, BKT == 32 ? 3 : 2) void gemm_kernel(FfnArgs f, 
         if (shared) {
           b_ptr[i] = reinterpret_cast<const bf16*>(f.shd) + (int64_t)col * f.Is;
           s_ptr[i] = nullptr;
-        } else if (MX) {
-          b_ptr[i] = reinterpret_cast<const uint8_t*>(f.wd) + ((int64_t)g * f.sd + (int64_t)col * f.I) / 2;
-          s_ptr[i] = nullptr;
-          mx_scale = reinterpret_cast<const uint8_t*>(f.scd) + ((int64_t)g * f.H + col) * (f.I / 32);
         } else if (fp8_tile) {
           b_ptr[i] = reinterpret_cast<const uint8_t*>(f.wd) + (int64_t)g * f.sd + (int64_t)col * f.I;
           const int kb = f.I / 128;
-          s_ptr[i] = reinterpret_cast<const float*>(f.scd) + (int64_t)g * (f.H / 128) * kb + (col / 128) * kb;
+          s_ptr[i] = f.scd + (int64_t)g * (f.H / 128) * kb + (col / 128) * kb;
         } else {
           b_ptr[i] = reinterpret_cast<const bf16*>(f.wd) + (int64_t)g * f.sd + (int64_t)col * f.I;
           s_ptr[i] = nullptr;
@@ -228,13 +215,12 @@ __global__ __launch_bounds__(NT, BKT == 32 ? 3 : 2) void gemm_kernel(FfnArgs f, 
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
-    // fp8 and MXFP4 weights: two register stages, the loads of K step kt+2 are issued
+    // fp8 weights: two register stages, the loads of K step kt+2 are issued
     // while step kt computes from LDS and step kt+1's registers are decoded
     // into LDS, so two steps' loads are in flight per workgroup (past the last
     // step the loads repeat it, never stored).  bf16: one register stage.
     u32x4 ra_reg[2][4], rb_reg[2][4];
     float rs_reg[2][2];
-    uint32_t mx_reg[2];  // MXFP4: the chunk's scale byte
     const int kcol = tid % CPR;
     const int nk = (K - kbeg + BKT - 1) / BKT;
 
@@ -252,12 +238,7 @@ __global__ __launch_bounds__(NT, BKT == 32 ? 3 : 2) void gemm_kernel(FfnArgs f, 
         const u32x4 v = ld16(a_ptr[i] + kc);
         ra_reg[rb][i] = kin ? v : u32x4{0, 0, 0, 0};
       }
-      if constexpr (MX) {
-        const int kk = k0 + (tid & 1) * 32;  // K % 32 == 0: a chunk is all in or all out (its A is zero then)
-        const int kl = kk < K ? kk : K - 32;
-        rb_reg[rb][0] = ld16(reinterpret_cast<const uint8_t*>(b_ptr[0]) + (kl >> 1));
-        mx_reg[rb] = mx_scale[kl >> 5];
-      } else if (fp8_tile) {
+      if (fp8_tile) {
         const int kk = k0 + (tid & 3) * 16;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -280,13 +261,7 @@ __global__ __launch_bounds__(NT, BKT == 32 ? 3 : 2) void gemm_kernel(FfnArgs f, 
         const int r = tid / CPR + RSTEP * i;
         *reinterpret_cast<u32x4*>(a + lds_off<BKT>(r, kcol)) = ra_reg[rb][i];
       }
-      if constexpr (MX) {
-        const float sc = e8m0(mx_reg[rb]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<u32x4*>(b + lds_off<BKT>(tid >> 1, (tid & 1) * 4 + i)) =
-              mx8_to_bf16x8(rb_reg[rb][0][i], sc);
-      } else if (fp8_tile) {
+      if (fp8_tile) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = (tid >> 2) + 64 * i;
@@ -338,7 +313,7 @@ __global__ __launch_bounds__(NT, BKT == 32 ? 3 : 2) void gemm_kernel(FfnArgs f, 
       __syncthreads();
     };
 
-    if constexpr (WT != kWtPlain) {
+    if constexpr (FP8) {
       gload(0, 0);
       gload(1, 1);
       lstore(0, 0);
@@ -653,9 +628,9 @@ hipError_t launch_router_logits_bf16(const void* x, const void* w_router, const 
   const int grid = tiles < num_cus() * 2 ? (tiles + 7) / 8 * 8 : num_cus() * 2;
   FfnArgs none{};
   if (gated_residual)
-    gemm_kernel<M_ROUTER, kWtPlain, 1><<<grid, NT, 0, s>>>(none, ra, ntn, kPlanStart, kPlanTiles);
+    gemm_kernel<M_ROUTER, false, 1><<<grid, NT, 0, s>>>(none, ra, ntn, kPlanStart, kPlanTiles);
   else
-    gemm_kernel<M_ROUTER, kWtPlain><<<grid, NT, 0, s>>>(none, ra, ntn, kPlanStart, kPlanTiles);
+    gemm_kernel<M_ROUTER, false><<<grid, NT, 0, s>>>(none, ra, ntn, kPlanStart, kPlanTiles);
   return hipGetLastError();
 }
 
@@ -670,23 +645,21 @@ hipError_t launch_ffn_gemm(const FfnArgs& a, int phase, hipStream_t s) {
   RouterArgs none{};
   if (a.wt != kWtPlain) {
     // routed tiles [0, plan[2]) decode their codes; the shared expert stays bf16
-    if (a.wt == kWtFp8) {
-      if (phase == 1) gemm_kernel<M_GATEUP, kWtFp8><<<grid, NT, 0, s>>>(a, none, ntn, kPlanStart, kPlanRoutedTiles);
-      else gemm_kernel<M_DOWN, kWtFp8><<<grid, NT, 0, s>>>(a, none, ntn, kPlanStart, kPlanRoutedTiles);
-    } else {
-      if (phase == 1) gemm_kernel<M_GATEUP, kWtMx><<<grid, NT, 0, s>>>(a, none, ntn, kPlanStart, kPlanRoutedTiles);
-      else gemm_kernel<M_DOWN, kWtMx><<<grid, NT, 0, s>>>(a, none, ntn, kPlanStart, kPlanRoutedTiles);
-    }
+    if (a.wt == kWtMx) {
+      const hipError_t e = launch_mx_tiles(a, phase, s);
+      if (e != hipSuccess) return e;
+    } else if (phase == 1) gemm_kernel<M_GATEUP, true><<<grid, NT, 0, s>>>(a, none, ntn, kPlanStart, kPlanRoutedTiles);
+    else gemm_kernel<M_DOWN, true><<<grid, NT, 0, s>>>(a, none, ntn, kPlanStart, kPlanRoutedTiles);
     if (sh) {
-      if (phase == 1) gemm_kernel<M_GATEUP, kWtPlain><<<grid, NT, 0, s>>>(a, none, ntn, kPlanRoutedTiles, kPlanTiles);
-      else gemm_kernel<M_DOWN, kWtPlain><<<grid, NT, 0, s>>>(a, none, ntn, kPlanRoutedTiles, kPlanTiles);
+      if (phase == 1) gemm_kernel<M_GATEUP, false><<<grid, NT, 0, s>>>(a, none, ntn, kPlanRoutedTiles, kPlanTiles);
+      else gemm_kernel<M_DOWN, false><<<grid, NT, 0, s>>>(a, none, ntn, kPlanRoutedTiles, kPlanTiles);
     }
   } else {
     constexpr int per_cu = kBf16FfnBK == 32 ? 3 : 2;
     const int g3 = (int)(tiles < num_cus() * per_cu ? (tiles + 7) / 8 * 8 : num_cus() * per_cu);
     if (phase == 1)
-      gemm_kernel<M_GATEUP, kWtPlain, 0, kBf16FfnBK><<<g3, NT, 0, s>>>(a, none, ntn, kPlanStart, kPlanTiles);
-    else gemm_kernel<M_DOWN, kWtPlain, 0, kBf16FfnBK><<<g3, NT, 0, s>>>(a, none, ntn, kPlanStart, kPlanTiles);
+      gemm_kernel<M_GATEUP, false, 0, kBf16FfnBK><<<g3, NT, 0, s>>>(a, none, ntn, kPlanStart, kPlanTiles);
+    else gemm_kernel<M_DOWN, false, 0, kBf16FfnBK><<<g3, NT, 0, s>>>(a, none, ntn, kPlanStart, kPlanTiles);
   }
   return hipGetLastError();
 }

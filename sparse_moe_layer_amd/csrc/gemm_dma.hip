@@ -538,11 +538,11 @@ __device__ __forceinline__ void run_tile(const FfnArgs& f, int mt, int nt, bf16*
       const int sel = t / nkb, kb = t - sel * nkb;
       float v;
       if (MODE == 1) {
-        v = reinterpret_cast<const float*>(sel ? f.scu : f.scg)[((int64_t)g * (f.I / 128) + nt) * nkb + kb];
+        v = (sel ? f.scu : f.scg)[((int64_t)g * (f.I / 128) + nt) * nkb + kb];
       } else {
         int rb = 2 * nt + sel;
         rb = rb < f.H / 128 ? rb : f.H / 128 - 1;
-        v = reinterpret_cast<const float*>(f.scd)[((int64_t)g * (f.H / 128) + rb) * nkb + kb];
+        v = f.scd[((int64_t)g * (f.H / 128) + rb) * nkb + kb];
       }
       ssc[t] = v;
     }
@@ -747,7 +747,7 @@ hipError_t launch(const FfnArgs& a, int phase, hipStream_t s, int tb, int te, in
 
 bool ffn_dma_supported(const FfnArgs& a) {
   constexpr int k = BigCfg::BK;
-  if (a.wt == kWtMx) return false;  // MXFP4 groups run on the 128-row tiles
+  if (a.wt == kWtMx) return false;  // MXFP4 groups have their own 128-row tiles
   if (a.Is != 0 && a.Is % k != 0) return false;
   // fp8: whole 128 x 128 scale blocks, at most 128 K blocks (the LDS scale table)
   if (a.wt == kWtFp8) return a.H % 128 == 0 && a.I % 128 == 0 && a.H <= 128 * 128 && a.I <= 128 * 128;

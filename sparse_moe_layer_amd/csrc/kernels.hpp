@@ -52,7 +52,7 @@ struct FfnArgs {
   const int32_t* sorted;      // [R]
   const void* wg; const void* wu; const void* wd;  // routed, elements: bf16, u8 codes or packed 4-bit codes
   int64_t sg, su, sd;         // expert strides (elements)
-  const void* scg; const void* scu; const void* scd;  // fp8: fp32 block scales; MXFP4: E8M0 bytes
+  const float* scg; const float* scu; const float* scd;  // fp8: block scales; MXFP4: where the E8M0 bytes are
   const void* shg; const void* shu; const void* shd;     // shared expert (bf16) or null
   void* h;                    // [R, I]  bf16 hidden of routed rows
   void* h_sh;                 // [T, Is] bf16 hidden of the shared expert
@@ -137,6 +137,10 @@ struct SmallRoute {
 // (route, phase 1 with bf16 weights and T <= kSmallBatch) from the ids.
 hipError_t launch_ffn_stream(const FfnArgs& a, int phase, hipStream_t s, bool self_plan = false,
                              const SmallRoute* route = nullptr);
+// The routed groups of an MXFP4 layer, called by the two launchers above: the
+// m-tiles [0, plan[kPlanRoutedTiles]) and the m-blocks [0, plan[kPlanRoutedBlocks]).
+hipError_t launch_mx_tiles(const FfnArgs& a, int phase, hipStream_t s);
+hipError_t launch_mx_stream(const FfnArgs& a, int phase, hipStream_t s, bool self_plan);
 hipError_t launch_ffn_f32(const FfnArgs& a, int phases, hipStream_t s);  // bit 0 gate/up, bit 1 down
 hipError_t launch_combine(const void* y, const int32_t* pos, const float* w, const void* y_sh,
                           const float* shared_logit, void* out, int T, int H, int k, int f32,
@@ -159,11 +163,11 @@ moe_status layer_forward_run(const moe_problem* p, const moe_weights* w, const v
 // Division by a size known to the host: floor(x / d) and the remainder for
 // 0 <= x < 2^31 through the high word of x * ceil(2^32 / d), which is at most
 // one off.
-struct FewDivisor {
+struct Divisor {
   int d = 1;
   uint32_t inv = 0xFFFFFFFFu;
-  FewDivisor() = default;
-  explicit FewDivisor(int n) : d(n), inv(n > 1 ? 0xFFFFFFFFu / (uint32_t)n + 1u : 0xFFFFFFFFu) {}
+  Divisor() = default;
+  explicit Divisor(int n) : d(n), inv(n > 1 ? 0xFFFFFFFFu / (uint32_t)n + 1u : 0xFFFFFFFFu) {}
   __device__ void divide(int x, int& q, int& r) const {
     q = (int)__umulhi((uint32_t)x, inv);
     r = x - q * d;
@@ -183,8 +187,8 @@ struct FewArgs {
   void* out;             // [T, H] bf16
   int32_t* counters;     // few_counter_ints words, zeroed by the first kernel
   // sizes, filled in by the launcher
-  FewDivisor slabs;       // slabs of 16 hidden columns per group
-  FewDivisor down_units;  // units of K of a group's down rows
+  Divisor slabs;       // slabs of 16 hidden columns per group
+  Divisor down_units;  // units of K of a group's down rows
   int units, shared_units, cols;  // units of the gate/up K and of the shared expert's; output columns at a time
 };
 constexpr int kFewDone = 16, kFewCounterStride = 64;  // done counters, ints apart

@@ -21,6 +21,48 @@ namespace {
 using namespace streamk;
 constexpr int WAVES = 4;
 
+// acc[j] += A[16 rows, kbeg..kend) x B_j[16 rows, kbeg..kend)^T for NB bf16
+// weight blocks, operands loaded straight into MFMA fragments (the small-batch
+// router).  a_row: this lane's A row (row lane%16) or null (zero row);
+// b_row[j]: this lane's row of weight block j.  kq = 8*(lane/16) is the
+// lane's K offset inside a 32-wide K step.  U K steps per batch, two batches
+// in flight.
+template <int NB>
+__device__ __forceinline__ void stream_dot(const bf16* a_row, const bf16* const* b_row, int kbeg, int kend, int kq,
+                                           f32x4* acc) {
+  u32x4 av[2][U];
+  u32x4 bv[2][U][NB];
+  const int nsteps = (kend - kbeg + KSTEP - 1) / KSTEP;
+  auto load = [&](int buf, int s0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kk = kbeg + (s0 + u) * KSTEP + kq;
+      const bool in = kk < kend;
+      av[buf][u] = (in && a_row) ? ld16(a_row + kk) : u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < NB; ++j) bv[buf][u][j] = in ? ld16(b_row[j] + kk) : u32x4{0, 0, 0, 0};
+    }
+  };
+  auto mma = [&](int buf) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(av[buf][u]), as_bf16x8(bv[buf][u][j]), acc[j],
+                                                         0, 0, 0);
+  };
+  load(0, 0);
+  for (int s0 = 0; s0 < nsteps; s0 += 2 * U) {
+    const bool more = s0 + U < nsteps;
+    if (more) load(1, s0 + U);
+    mma(0);
+    if (more) {
+      if (s0 + 2 * U < nsteps) load(0, s0 + 2 * U);
+      mma(1);
+    }
+  }
+}
+
 // SPLIT (bf16 gate/up only): items of 8 hidden columns, one 16-row block of
 // 8 gate rows and the 8 up rows of the same columns.  Half-size items end a
 // launch with less idle time; they pay off when the whole batch streams
@@ -41,15 +83,15 @@ constexpr int WAVES = 4;
 // number of rows of the experts listed before it: the stable order of the
 // dispatch kernels, in which an expert's rows are its tokens ascending.
 // Wave 0 of workgroup 0 also writes offsets, sorted and pos from the masks.
-template <int PHASE, int WT, bool SPLIT = false>
+template <int PHASE, bool FP8, bool SPLIT = false>
 __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(FfnArgs f, int list_begin_idx, int list_end_idx,
                                                                int self_plan, SmallRoute route) {
-  static_assert(!SPLIT || (PHASE == 1 && WT != kWtFp8), "split items are bf16 or MXFP4 gate/up");
-  constexpr int STAGE_BYTES = item_lds_bytes<WT, SPLIT>();         // per wave
-  constexpr bool ROUTES = PHASE == 1 && WT == kWtPlain && SPLIT;  // may take the dispatch (self_plan == 2)
+  static_assert(!SPLIT || (PHASE == 1 && !FP8), "split items are bf16 gate/up");
+  constexpr int STAGE_BYTES = item_lds_bytes<FP8, SPLIT>();  // per wave
+  constexpr bool ROUTES = PHASE == 1 && !FP8 && SPLIT;       // may take the dispatch (self_plan == 2)
   // the masks and (workgroup 0) the experts' first rows fit wave 0's own stage buffer
   static_assert(!ROUTES || 2 * kMaxExperts * 4 <= STAGE_BYTES, "route scratch in the stage");
-  __shared__ __attribute__((aligned(16))) char stage[STAGE_BYTES ? WAVES * STAGE_BYTES : 16];
+  __shared__ __attribute__((aligned(16))) char stage[WAVES * STAGE_BYTES];
   __shared__ int glist[kMaxExperts + 1];  // SELF_PLAN: touched groups
   __shared__ int wtot[WAVES];
   const int lane = threadIdx.x & 63;
@@ -179,7 +221,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(FfnArgs f, int li
       base = f.sb_base[sb];
       nrows = f.sb_nrows[sb];
     }
-    stream_item<PHASE, WT, SPLIT>(f, g, r0, base, nrows, self_plan ? nullptr : f.sb_tok + sb * kStreamBM, slab,
+    stream_item<PHASE, FP8, SPLIT>(f, g, r0, base, nrows, self_plan ? nullptr : f.sb_tok + sb * kStreamBM, slab,
                                    lane, stage + wave * STAGE_BYTES, mk);
   }
 }
@@ -280,24 +322,21 @@ hipError_t launch_ffn_stream(const FfnArgs& a, int phase, hipStream_t s, bool se
     sp = 2;
   }
   if (a.wt != kWtPlain) {
-    if (a.wt == kWtFp8) {
-      if (phase == 1) stream_kernel<1, kWtFp8><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
-      else stream_kernel<2, kWtFp8><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
-    } else {
-      if (phase == 1 && split) stream_kernel<1, kWtMx, true><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
-      else if (phase == 1) stream_kernel<1, kWtMx><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
-      else stream_kernel<2, kWtMx><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
-    }
+    if (a.wt == kWtMx) {
+      const hipError_t e = launch_mx_stream(a, phase, s, self_plan);
+      if (e != hipSuccess) return e;
+    } else if (phase == 1) stream_kernel<1, true><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
+    else stream_kernel<2, true><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
     if (a.Is > 0) {
       if (phase == 1 && split)
-        stream_kernel<1, kWtPlain, true><<<grid, blk, 0, s>>>(a, kPlanRoutedBlocks, kPlanBlocks, sp, r);
-      else if (phase == 1) stream_kernel<1, kWtPlain><<<grid, blk, 0, s>>>(a, kPlanRoutedBlocks, kPlanBlocks, sp, r);
-      else stream_kernel<2, kWtPlain><<<grid, blk, 0, s>>>(a, kPlanRoutedBlocks, kPlanBlocks, sp, r);
+        stream_kernel<1, false, true><<<grid, blk, 0, s>>>(a, kPlanRoutedBlocks, kPlanBlocks, sp, r);
+      else if (phase == 1) stream_kernel<1, false><<<grid, blk, 0, s>>>(a, kPlanRoutedBlocks, kPlanBlocks, sp, r);
+      else stream_kernel<2, false><<<grid, blk, 0, s>>>(a, kPlanRoutedBlocks, kPlanBlocks, sp, r);
     }
   } else {
-    if (phase == 1 && split) stream_kernel<1, kWtPlain, true><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanBlocks, sp, r);
-    else if (phase == 1) stream_kernel<1, kWtPlain><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanBlocks, sp, r);
-    else stream_kernel<2, kWtPlain><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanBlocks, sp, r);
+    if (phase == 1 && split) stream_kernel<1, false, true><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanBlocks, sp, r);
+    else if (phase == 1) stream_kernel<1, false><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanBlocks, sp, r);
+    else stream_kernel<2, false><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanBlocks, sp, r);
   }
   return hipGetLastError();
 }

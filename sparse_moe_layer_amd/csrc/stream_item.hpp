@@ -25,48 +25,6 @@ constexpr int KSTEP = 32;
 
 __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
-// acc[j] += A[16 rows, kbeg..kend) x B_j[16 rows, kbeg..kend)^T for NB bf16
-// weight blocks, operands loaded straight into MFMA fragments (the
-// small-batch routers).  a_row: this lane's A row (row lane%16) or null (zero row);
-// b_row[j]: this lane's row of weight block j.  kq = 8*(lane/16) is the
-// lane's K offset inside a 32-wide K step.  U K steps per batch, two batches
-// in flight.
-template <int NB>
-__device__ __forceinline__ void stream_dot(const bf16* a_row, const bf16* const* b_row, int kbeg, int kend, int kq,
-                                           f32x4* acc) {
-  u32x4 av[2][U];
-  u32x4 bv[2][U][NB];
-  const int nsteps = (kend - kbeg + KSTEP - 1) / KSTEP;
-  auto load = [&](int buf, int s0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int kk = kbeg + (s0 + u) * KSTEP + kq;
-      const bool in = kk < kend;
-      av[buf][u] = (in && a_row) ? ld16(a_row + kk) : u32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int j = 0; j < NB; ++j) bv[buf][u][j] = in ? ld16(b_row[j] + kk) : u32x4{0, 0, 0, 0};
-    }
-  };
-  auto mma = [&](int buf) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int j = 0; j < NB; ++j)
-        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(av[buf][u]), as_bf16x8(bv[buf][u][j]), acc[j],
-                                                         0, 0, 0);
-  };
-  load(0, 0);
-  for (int s0 = 0; s0 < nsteps; s0 += 2 * U) {
-    const bool more = s0 + U < nsteps;
-    if (more) load(1, s0 + U);
-    mma(0);
-    if (more) {
-      if (s0 + 2 * U < nsteps) load(0, s0 + 2 * U);
-      mma(1);
-    }
-  }
-}
-
 // ---- LDS-staged bf16 streaming -------------------------------------------
 // A batch holds SB = 256 K values (512 B) of NB*16 weight rows.  Rows 2i and
 // 2i+1 of the batch sit in 1 KB at i * 1040 B (1 KB + 16 B pad); odd rows
@@ -214,13 +172,10 @@ __device__ __forceinline__ void stream_dot_lds(const bf16* a_row, const bf16* a_
 constexpr int SB8 = 256;
 constexpr int PAIR8 = 528;
 
-// SPLIT (NB == 1): rows 0-7 from wrow0[0] and rows 8-15 from wrow0[1], with
-// nvalid[0] and nvalid[1] valid rows (s_row[0] is the lane's own row's either way).
-template <int NB, bool SPLIT = false>
+template <int NB>
 __device__ __forceinline__ void stream_dot_lds8(const bf16* a_row, const bf16* a_any, const uint8_t* const* wrow0,
                                                 const int* nvalid, int ldw, const float* const* s_row, int kbeg,
                                                 int kend, int lane, char* lds, f32x4* acc) {
-  static_assert(!SPLIT || NB == 1, "a split block is the only block");
   constexpr int NL = NB * 4;       // weight loads per batch (4 rows each)
   constexpr int NA = SB8 / KSTEP;  // activation loads per batch
   const int kq = (lane >> 4) * 8;
@@ -238,14 +193,8 @@ __device__ __forceinline__ void stream_dot_lds8(const bf16* a_row, const bf16* a
     for (int j = 0; j < NB; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if constexpr (SPLIT) {
-          const int half = i >> 1, rh = (4 * i + q4) & 7;
-          const int r = rh < nvalid[half] ? rh : nvalid[half] - 1;
-          wb[i] = ld16_nt(wrow0[half] + (uint32_t)(r * ldw + k));
-        } else {
-          const int r = 4 * i + q4 < nvalid[j] ? 4 * i + q4 : nvalid[j] - 1;
-          wb[j * 4 + i] = ld16_nt(wrow0[j] + (uint32_t)(r * ldw + k));
-        }
+        const int r = 4 * i + q4 < nvalid[j] ? 4 * i + q4 : nvalid[j] - 1;
+        wb[j * 4 + i] = ld16_nt(wrow0[j] + (uint32_t)(r * ldw + k));
       }
   };
   auto load_a = [&](int x, int b) {
@@ -328,68 +277,10 @@ __device__ __forceinline__ void stream_dot_lds8(const bf16* a_row, const bf16* a
   }
 }
 
-// ---- MXFP4 streaming -------------------------------------------------------
-// A 16-byte load of E2M1 codes is 32 values of one row: one scale group, and
-// this lane's share of four MFMA steps.  The K order inside an MFMA is free as
-// long as both operands use it, so step s of a 128-wide K run takes values
-// kb + 32 q + 8 s .. + 8 from lane group q of weights and activations alike,
-// and codes go from global memory straight into fragments: no LDS.
-// w_row[j] / s_row[j]: this lane's row (lane % 16) of weight block j, as codes
-// and as scale bytes.
-constexpr int KB4 = 128;  // K values per load of the wave
-constexpr int U4 = 2;     // loads per row and batch; two batches in flight
-
-template <int NB>
-__device__ __forceinline__ void stream_dot_mx(const bf16* a_row, const bf16* a_any, const uint8_t* const* w_row,
-                                              const uint8_t* const* s_row, int kbeg, int kend, int lane,
-                                              f32x4* acc) {
-  const int q = lane >> 4;
-  const int nb = (kend - kbeg + KB4 - 1) / KB4;
-  const bf16* arow = a_row ? a_row : a_any;
-  u32x4 wv[2][U4][NB], av[2][U4][4];
-  uint32_t sv[2][U4][NB];
-  // past the end every load reads the row's last group, whose activations are zeroed
-  auto load = [&](int x, int b0) {
-#pragma unroll
-    for (int u = 0; u < U4; ++u) {
-      int k = kbeg + (b0 + u) * KB4 + q * 32;
-      k = k < kend ? k : kend - 32;
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        wv[x][u][j] = ld16_nt(w_row[j] + (k >> 1));
-        sv[x][u][j] = s_row[j][k >> 5];
-      }
-#pragma unroll
-      for (int s = 0; s < 4; ++s) av[x][u][s] = ld16(arow + k + 8 * s);
-    }
-  };
-  auto compute = [&](int x, int b0) {
-#pragma unroll
-    for (int u = 0; u < U4; ++u) {
-      const bool in = a_row && kbeg + (b0 + u) * KB4 + q * 32 < kend;
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const u32x4 am = in ? av[x][u][s] : u32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < NB; ++j)
-          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              as_bf16x8(am), as_bf16x8(mx8_to_bf16x8(wv[x][u][j][s], e8m0(sv[x][u][j]))), acc[j], 0, 0, 0);
-      }
-    }
-  };
-  load(0, 0);
-  for (int b = 0; b < nb; b += 2 * U4) {
-    load(1, b + U4);
-    compute(0, b);
-    load(0, b + 2 * U4);
-    compute(1, b + U4);
-  }
-}
-
 // Bytes of wave-private LDS one item needs.
-template <int WT, bool SPLIT>
+template <bool FP8, bool SPLIT>
 constexpr int item_lds_bytes() {
-  return WT == kWtMx ? 0 : (SPLIT ? 1 : 2) * 8 * (WT == kWtFp8 ? PAIR8 : PAIR);
+  return (SPLIT ? 1 : 2) * 8 * (FP8 ? PAIR8 : PAIR);
 }
 
 // One item: slab `slab` of group g (routed expert g < E, or the shared
@@ -398,14 +289,13 @@ constexpr int item_lds_bytes() {
 // (the plan's list); else, when tok_mask is nonzero, the group's tokens as a
 // bit mask (row m is the token of its m-th set bit: a batch of at most 32
 // tokens whose dispatch is not in memory yet); else f.sorted.  lds: this
-// wave's item_lds_bytes<WT, SPLIT>() bytes.  Returns at once if the slab
+// wave's item_lds_bytes<FP8, SPLIT>() bytes.  Returns at once if the slab
 // lies past the group's columns.
-template <int PHASE, int WT, bool SPLIT>
+template <int PHASE, bool FP8, bool SPLIT>
 __device__ __forceinline__ void stream_item(const FfnArgs& f, int g, int r0, int base, int nrows,
                                             const int32_t* tok_row, int slab, int lane, char* lds,
                                             uint32_t tok_mask = 0u) {
-  constexpr bool FP8 = WT == kWtFp8;
-  static_assert(!SPLIT || PHASE == 1, "split items are gate/up");
+  static_assert(!SPLIT || (PHASE == 1 && !FP8), "split items are bf16 gate/up");
   constexpr int NB = SPLIT ? 1 : 2;
   const int cols_per_item = PHASE == 1 ? (SPLIT ? 8 : 16) : 32;
   const int m = lane & 15;  // A row / B column within a 16-block
@@ -447,15 +337,10 @@ __device__ __forceinline__ void stream_item(const FfnArgs& f, int g, int r0, int
       col = col < Ncols ? col : Ncols - 1;
       if (PHASE == 1) {
         const int kb = f.H / 128;
-        const bool up = SPLIT ? m >= 8 : j == 1;
-        if (SPLIT) {
-          col = c0 + (m & 7);
-          col = col < Ncols ? col : Ncols - 1;
-        }
-        s_row[j] = reinterpret_cast<const float*>(up ? f.scu : f.scg) + (int64_t)g * (f.I / 128) * kb + (col / 128) * kb;
+        s_row[j] = (j ? f.scu : f.scg) + (int64_t)g * (f.I / 128) * kb + (col / 128) * kb;
       } else {
         const int kb = f.I / 128;
-        s_row[j] = reinterpret_cast<const float*>(f.scd) + (int64_t)g * (f.H / 128) * kb + (col / 128) * kb;
+        s_row[j] = f.scd + (int64_t)g * (f.H / 128) * kb + (col / 128) * kb;
       }
     }
   }
@@ -463,33 +348,15 @@ __device__ __forceinline__ void stream_item(const FfnArgs& f, int g, int r0, int
   f32x4 acc[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if constexpr (WT == kWtMx) {
-    // this lane's row of each block (split: gate rows 0-7, up rows 8-15);
-    // rows past the matrix read its last one and are never stored
-    const uint8_t* w_row[NB];
-    const uint8_t* s_row4[NB];
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const bool up = PHASE == 1 && (SPLIT ? m >= 8 : j == 1);
-      int row = PHASE == 1 ? c0 + (SPLIT ? m & 7 : m) : c0 + j * 16 + m;
-      row = row < Ncols ? row : Ncols - 1;
-      const void* mat = PHASE == 1 ? (up ? f.wu : f.wg) : f.wd;
-      const void* sc = PHASE == 1 ? (up ? f.scu : f.scg) : f.scd;
-      const int64_t stride = PHASE == 1 ? (up ? f.su : f.sg) : f.sd;
-      w_row[j] = reinterpret_cast<const uint8_t*>(mat) + ((int64_t)g * stride + (int64_t)row * K) / 2;
-      s_row4[j] = reinterpret_cast<const uint8_t*>(sc) + ((int64_t)g * Ncols + row) * (K / 32);
-    }
-    stream_dot_mx<NB>(a_row, reinterpret_cast<const bf16*>(PHASE == 1 ? f.x : f.h), w_row, s_row4, 0, K, lane, acc);
-  } else if constexpr (FP8) {
+  if constexpr (FP8) {
     // (an fp8 launch covers the routed groups only; the shared expert's
     // bf16 weights go through the bf16 launch)
     // first row and valid-row count of each 16-row weight block, and this
     // lane's fragment row's scale row
-    constexpr int NW0 = SPLIT ? 2 : NB;
-    const uint8_t* w0[NW0];
-    int nv[NW0];
+    const uint8_t* w0[NB];
+    int nv[NB];
 #pragma unroll
-    for (int j = 0; j < NW0; ++j) {
+    for (int j = 0; j < NB; ++j) {
       int first = PHASE == 1 ? c0 : c0 + j * 16;
       first = first < Ncols ? first : Ncols - 1;
       nv[j] = Ncols - first;
@@ -499,7 +366,7 @@ __device__ __forceinline__ void stream_item(const FfnArgs& f, int g, int r0, int
       w0[j] = mat + (int64_t)first * K;
     }
     const bf16* a_any = reinterpret_cast<const bf16*>(PHASE == 1 ? f.x : f.h);
-    stream_dot_lds8<NB, SPLIT>(a_row, a_any, w0, nv, K, s_row, 0, K, lane, lds, acc);
+    stream_dot_lds8<NB>(a_row, a_any, w0, nv, K, s_row, 0, K, lane, lds, acc);
   } else {
     // first row and valid-row count of each weight block (gate/up: of the
     // gate half and the up half of the one split block)
