@@ -7,6 +7,7 @@
 
 #include <cstdint>
 #include <cstring>
+#include <cstdlib>
 #include <mutex>
 
 #include "kernels.hpp"
@@ -307,6 +308,49 @@ Aux* aux_stream() {
 // overlap them.
 constexpr int kStreamReserve = 32;
 
+// From this many rows per expert on average, an MXFP4 layer's groups of at most
+// 16 rows run as m-tiles as well.
+static int kMxTileRows = getenv("MXTR") ? atoi(getenv("MXTR")) : 16;
+
+// The same for an MXFP4 layer: its routed groups have kernels of their own, and
+// the bf16 shared expert, which needs none of their results, is a chain of
+// launches beside theirs.
+moe_status run_ffn_mx(const moe_problem* p, FfnArgs& a, int phases, int32_t* plan, hipStream_t s, bool fork_ok) {
+  const bool force_gemm = p->flags & MOE_FLAG_FORCE_GEMM, force_stream = p->flags & MOE_FLAG_FORCE_STREAM;
+  const bool few = p->T <= moe::kStreamMaxRows;  // every group is one m-block
+  const bool tiles_only = force_gemm || (!force_stream && p->T * p->k >= kMxTileRows * p->E);
+  const int stream_rows = tiles_only ? 0 : moe::kStreamMaxRows;
+  const bool any_gemm = tiles_only || (!force_stream && !few), any_stream = !tiles_only;
+  const bool self_plan = !any_gemm && few;
+  if (!self_plan) {
+    if (moe::launch_ffn_plan(a.offsets, a.sorted, a.T, a.E, a.k, a.Is > 0 ? 1 : 0, p->flags, moe::kGemmBM,
+                             stream_rows, plan, s) != hipSuccess)
+      return MOE_ERR_HIP;
+    moe::ffn_bind_plan(a, plan);
+  }
+  const bool sh_stream = force_stream || (!force_gemm && p->T <= stream_rows);
+  Aux* x = fork_ok && a.Is > 0 && !self_plan ? aux_stream() : nullptr;
+  std::unique_lock<std::mutex> lk;
+  if (x) {
+    lk = std::unique_lock<std::mutex>(x->mu);
+    if (hipEventRecord(x->fork, s) != hipSuccess || hipStreamWaitEvent(x->s2, x->fork, 0) != hipSuccess)
+      return MOE_ERR_HIP;
+  }
+  bool ok = true;
+  for (int phase = 1; phase <= 2; ++phase) {
+    if (!(phases & phase)) continue;
+    if (a.Is > 0) {
+      const hipStream_t t = x ? x->s2 : s;
+      ok = ok && (sh_stream ? moe::launch_ffn_stream(a, phase, t, self_plan) : moe::launch_ffn_gemm(a, phase, t)) == hipSuccess;
+    }
+    if (any_gemm) ok = ok && moe::launch_mx_tiles(a, phase, s) == hipSuccess;
+    if (any_stream) ok = ok && moe::launch_mx_stream(a, phase, s, self_plan) == hipSuccess;
+  }
+  if (x && (hipEventRecord(x->join, x->s2) != hipSuccess || hipStreamWaitEvent(s, x->join, 0) != hipSuccess))
+    return MOE_ERR_HIP;
+  return ok ? MOE_OK : MOE_ERR_HIP;
+}
+
 // phases: bit 0 gate/up, bit 1 down.  The plan kernel runs first (bf16/fp8).
 // fork_ok: the streaming launches may run on the device's second stream.
 // route (may be null): the gate/up streaming launch takes the small batch's
@@ -315,6 +359,7 @@ moe_status run_ffn(const moe_problem* p, FfnArgs& a, int phases, void* plan_ws, 
                    const moe::SmallRoute* route = nullptr) {
   if (p->act_dtype == MOE_F32) return hip_status(moe::launch_ffn_f32(a, phases, s));
   int32_t* plan = static_cast<int32_t*>(plan_ws);
+  if (a.wt == moe::kWtMx) return run_ffn_mx(p, a, phases, plan, s, fork_ok);
   const bool big = use_big_tiles(p, a);
   // Groups of at most kStreamMaxRows rows stream their weights after the
   // tiles.  (As ragged 256-row tiles they measured slower: the 2.4T fp8

@@ -99,7 +99,8 @@ __device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, i
                                     Next next, After after, Gate gate) {
   using F = Form<WT, AROWS>;
   constexpr int G = F::G, U = F::U;
-  constexpr uint32_t kNone = 0x80000000u;  // past any of the buffers below: reads as zeros, fetches nothing
+  constexpr uint32_t kNone = 0x80000000u;  // past any weight rows: reads as zeros, fetches nothing
+  constexpr uint32_t kOut = 0xFFFFFFF0u;   // past any activations
   constexpr int LPR = 64 / F::RPL;         // lanes per activation row
   const int q = lane >> 4, n = lane & 15;
   const uint32_t rowb = (uint32_t)wbytes<WT>(K);
@@ -206,7 +207,7 @@ __device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, i
             const int at = r < job.rows ? r : 0;
             aoff[i] = r < job.rows ? (uint32_t)row_of(job, at) * (uint32_t)K * 2u +
                                          16u * (uint32_t)(lane % LPR)
-                                   : kNone;
+                                   : kNone;  // (some place or none: its results are not used)
           }
       }
 #pragma unroll
@@ -214,7 +215,7 @@ __device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, i
         if (i * F::RPL < job.rows)
           at[i] = __builtin_bit_cast(
               u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                         ares, kb + (lane % LPR) * 8 < job.kend ? aoff[i] + 2u * (uint32_t)kb : kNone, 0, AUXA));
+                         ares, kb + (lane % LPR) * 8 < job.kend ? aoff[i] + 2u * (uint32_t)kb : kOut, 0, AUXA));
       n_rows = job.rows, n_ar = job.ar, n_kb = kb, n_tag = job.tag;
       kb += F::KB;
       fresh = n_last = kb >= job.kend;

@@ -645,10 +645,9 @@ hipError_t launch_ffn_gemm(const FfnArgs& a, int phase, hipStream_t s) {
   RouterArgs none{};
   if (a.wt != kWtPlain) {
     // routed tiles [0, plan[2]) decode their codes; the shared expert stays bf16
-    if (a.wt == kWtMx) {
-      const hipError_t e = launch_mx_tiles(a, phase, s);
-      if (e != hipSuccess) return e;
-    } else if (phase == 1) gemm_kernel<M_GATEUP, true><<<grid, NT, 0, s>>>(a, none, ntn, kPlanStart, kPlanRoutedTiles);
+    // (launch_mx_tiles has the routed tiles of an MXFP4 layer)
+    if (a.wt == kWtMx) ;
+    else if (phase == 1) gemm_kernel<M_GATEUP, true><<<grid, NT, 0, s>>>(a, none, ntn, kPlanStart, kPlanRoutedTiles);
     else gemm_kernel<M_DOWN, true><<<grid, NT, 0, s>>>(a, none, ntn, kPlanStart, kPlanRoutedTiles);
     if (sh) {
       if (phase == 1) gemm_kernel<M_GATEUP, false><<<grid, NT, 0, s>>>(a, none, ntn, kPlanRoutedTiles, kPlanTiles);

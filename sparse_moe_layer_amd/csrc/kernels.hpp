@@ -137,8 +137,9 @@ struct SmallRoute {
 // (route, phase 1 with bf16 weights and T <= kSmallBatch) from the ids.
 hipError_t launch_ffn_stream(const FfnArgs& a, int phase, hipStream_t s, bool self_plan = false,
                              const SmallRoute* route = nullptr);
-// The routed groups of an MXFP4 layer, called by the two launchers above: the
-// m-tiles [0, plan[kPlanRoutedTiles]) and the m-blocks [0, plan[kPlanRoutedBlocks]).
+// The routed groups of an MXFP4 layer (the launchers above have its shared expert
+// alone): the m-tiles [0, plan[kPlanRoutedTiles]) and the m-blocks [0,
+// plan[kPlanRoutedBlocks]).
 hipError_t launch_mx_tiles(const FfnArgs& a, int phase, hipStream_t s);
 hipError_t launch_mx_stream(const FfnArgs& a, int phase, hipStream_t s, bool self_plan);
 hipError_t launch_ffn_f32(const FfnArgs& a, int phases, hipStream_t s);  // bit 0 gate/up, bit 1 down

@@ -193,15 +193,20 @@ __global__ __launch_bounds__(SW * 64, 2) void mx_stream_kernel(FfnArgs f, int se
 // rows.  A step is 128 values of K: activations go to LDS by direct loads, one
 // step ahead in the other of two buffers, chunk c (16 bytes) of row r at
 // c ^ (r % 16) of its 256 bytes, so a fragment read's 16 rows lie in 16 bank
-// groups; codes and scales go straight to registers, also a step ahead, 64 bytes
-// of 16 rows a load, and become bf16 there.  So LDS carries the activations
-// alone, 1 KB per four matrix instructions, half of what it can.
+// groups.  Codes go to registers, also a step ahead, 64 bytes of 16 rows a load
+// with four consecutive lanes to a row, take their fragment order through 1 KB of
+// LDS of the wave, and become bf16 in registers (loaded in fragment order, a lane
+// to a row, they cost the address unit a quarter of the kernel's time; a skewed
+// layer of 1023 tokens took 1265 us with scale bytes loaded so as well, 857
+// without the codes' loads, 980 without the scales').  The scale bytes of 7 steps
+// go to LDS by direct loads, 32 bytes of a row.
 constexpr int TW = 4;          // waves
 constexpr int TK = 128;        // K per step
 constexpr int TN = 256;        // weight rows per tile
 constexpr int TBUF = kGemmBM * TK * 2;
 constexpr int kAhead = 3;      // activation fragments read ahead of their use
-constexpr uint32_t kOut = 0xFFFFFF00u;  // an offset past any buffer: reads as zeros
+constexpr int kScaleSteps = 7;  // steps whose scale bytes lie in LDS: 28 bytes and up to 3 before them
+constexpr uint32_t kOut = 0xFFFFFFF0u;  // an offset past any buffer: reads as zeros
 
 struct MxTile {  // a tile's rows and columns
   int g, base, r0, nrows, nt;
@@ -245,8 +250,8 @@ __device__ __forceinline__ void mx_step(f32x4 (&acc)[NBLK][4], const char* buf, 
 }
 
 template <int PHASE, int NBLK>
-__device__ __forceinline__ void mx_tile(const FfnArgs& f, const MxTile& t, char* lds0, char* lds1, int lane,
-                                        int wave) {
+__device__ __forceinline__ void mx_tile(const FfnArgs& f, const MxTile& t, char* lds0, char* lds1, char* codes,
+                                        char* scales, int lane, int wave) {
   const int K = PHASE == 1 ? f.H : f.I, N = PHASE == 1 ? f.I : f.H;
   asm volatile("" : "+v"(lane));  // (so that no address is computed ahead of the tile loop and held through it)
   int q = lane >> 4, m = lane & 15;
@@ -267,14 +272,20 @@ __device__ __forceinline__ void mx_tile(const FfnArgs& f, const MxTile& t, char*
     }
     aoff[i] = (uint32_t)row * (uint32_t)K * 2u + 16u * (uint32_t)ac;
   }
-  // weight rows: block b's row m, chunk q of a step
+  // weight rows; columns past the matrix are computed, never stored
   __amdgpu_buffer_rsrc_t wres[PHASE == 1 ? 2 : 1], sres[PHASE == 1 ? 2 : 1];
-  uint32_t wrow[4];  // the row; its codes and scale bytes lie in order from the expert's (which are aligned)
+  auto row_of = [&](int b, int r) {  // of block b: its first scale byte, in the expert's (which are aligned)
+    const int n = (PHASE == 1 ? t.nt * (TN / 2) + wave * 32 + (b & 1) * 16 : t.nt * TN + wave * 64 + b * 16) + r;
+    return (uint32_t)(n < N ? n : N - 1) * (uint32_t)groups;
+  };
+  uint32_t wrow[4], soff[4];  // codes: row lane / 4, chunk lane % 4 of a step; scales in LDS: of row m, chunk q
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
-    const int n = PHASE == 1 ? t.nt * (TN / 2) + wave * 32 + (b & 1) * 16 + m : t.nt * TN + wave * 64 + b * 16 + m;
-    wrow[b] = (uint32_t)(n < N ? n : N - 1) * (uint32_t)groups;  // columns past the matrix are computed, never stored
+    wrow[b] = row_of(b, lane >> 2) * 16u + 16u * (lane & 3);
+    soff[b] = (b * 16 + m) * 32 + (row_of(b, m) & 3u) + q;
   }
+  char* const cput = codes + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 4)) << 4);  // 16 rows of a chunk in 16 bank groups
+  const char* const cget = codes + m * 64 + ((q ^ (m >> 2)) << 4);
   const uint32_t sbytes = (uint32_t)N * (uint32_t)groups;
 #pragma unroll
   for (int j = 0; j < (PHASE == 1 ? 2 : 1); ++j) {
@@ -295,25 +306,29 @@ __device__ __forceinline__ void mx_tile(const FfnArgs& f, const MxTile& t, char*
     for (int b = 0; b < 4; ++b) acc[i][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   u32x4 wn[4];
-  uint32_t sn[4];
+  auto load_scales = [&](int kt) {  // of steps kt .. + 6: 32 rows a load, 16 bytes a lane from an aligned place on
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t at = (row_of(2 * j + (lane >> 5), (lane >> 1) & 15) & ~3u) + kt * 4 + 16 * (lane & 1);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(sres[PHASE == 1 ? j : 0],
+                                               (__attribute__((address_space(3))) void*)(scales + j * 1024), 16, at, 0, 0,
+                                               0);
+    }
+  };
   auto load = [&](int kt, char* buf) {
     const uint32_t k = (uint32_t)kt * TK;
-    const bool win = (int)k + q * 32 < K, in = (int)k + ac * 8 < K;
+    const bool win = (int)k + (lane & 3) * 32 < K, in = (int)k + ac * 8 < K;
 #pragma unroll
     for (int b = 0; b < 4; ++b)
-      wn[b] = __builtin_bit_cast(
-          u32x4, __builtin_amdgcn_raw_buffer_load_b128(wres[PHASE == 1 ? b >> 1 : 0],
-                                                       win ? wrow[b] * 16u + 16u * q + k / 2 : kOut, 0, 0));
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-      sn[b] = __builtin_amdgcn_raw_buffer_load_b8(sres[PHASE == 1 ? b >> 1 : 0],
-                                                  win ? wrow[b] + (uint32_t)(kt * 4 + q) : kOut, 0, 0);
+      wn[b] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wres[PHASE == 1 ? b >> 1 : 0],
+                                                                              win ? wrow[b] + k / 2 : kOut, 0, 0));
 #pragma unroll
     for (int i = 0; i < NBLK; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           ares, (__attribute__((address_space(3))) void*)(buf + i * 4096 + wave * 1024), 16,
           in ? aoff[i] + 2u * k : kOut, 0, 0, 0);
   };
+  int sk = 0;  // the step's place among those whose scales lie in LDS
   auto step = [&](int kt, const char* here, char* there) {
     __builtin_amdgcn_s_waitcnt(0xF70);  // vmcnt(0): this wave's loads of the step have arrived
     asm volatile("" ::: "memory");
@@ -323,13 +338,23 @@ __device__ __forceinline__ void mx_tile(const FfnArgs& f, const MxTile& t, char*
     float sc[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      w[b] = wn[b];
-      sc[b] = e8m0(sn[b]);
+      // (LDS operations of one wave are executed in order)
+      *reinterpret_cast<u32x4*>(cput) = wn[b];
+      w[b] = *reinterpret_cast<const u32x4*>(cget);
+      const uint32_t s = *reinterpret_cast<const uint8_t*>(scales + soff[b] + 4 * sk);
+      sc[b] = e8m0(kt * TK + q * 32 < K ? s : 0u);  // (what lies behind a row's scales is not one of them)
     }
     mx_step<NBLK>(acc, here, w, sc, aswz, [&] {
+      if (++sk == kScaleSteps && kt + 1 < steps) {
+        sk = 0;
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this step's scales have been read
+        asm volatile("" ::: "memory");
+        load_scales(kt + 1);
+      }
       if (kt + 1 < steps) load(kt + 1, there);
     });
   };
+  load_scales(0);
   load(0, lds0);
 #pragma unroll 1
   for (int kt = 0; kt < steps; kt += 2) {
@@ -373,6 +398,8 @@ template <int PHASE>
 __global__ __launch_bounds__(TW * 64, 2) void mx_tiles_kernel(FfnArgs f, Divisor ntn, int32_t* counters) {
   __shared__ __attribute__((aligned(1024))) char lds0[TBUF];
   __shared__ __attribute__((aligned(1024))) char lds1[TBUF];  // (apart: a read of one waits for no load to the other)
+  __shared__ __attribute__((aligned(16))) char wcodes[TW][1024];  // per wave: a block's codes
+  __shared__ __attribute__((aligned(16))) char wscales[TW][64 * 32];  // and its 64 rows' scale bytes
   __shared__ int claim;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int mts = uniform(f.plan[kPlanRoutedTiles]);
@@ -425,14 +452,14 @@ __global__ __launch_bounds__(TW * 64, 2) void mx_tiles_kernel(FfnArgs f, Divisor
     t.nrows = uniform(f.offsets[t.g + 1]) - t.base - t.r0;
     t.nrows = t.nrows < kGemmBM ? t.nrows : kGemmBM;
     switch ((t.nrows + 15) >> 4) {
-      case 1: mx_tile<PHASE, 1>(f, t, lds0, lds1, lane, wave); break;
-      case 2: mx_tile<PHASE, 2>(f, t, lds0, lds1, lane, wave); break;
-      case 3: mx_tile<PHASE, 3>(f, t, lds0, lds1, lane, wave); break;
-      case 4: mx_tile<PHASE, 4>(f, t, lds0, lds1, lane, wave); break;
-      case 5: mx_tile<PHASE, 5>(f, t, lds0, lds1, lane, wave); break;
-      case 6: mx_tile<PHASE, 6>(f, t, lds0, lds1, lane, wave); break;
-      case 7: mx_tile<PHASE, 7>(f, t, lds0, lds1, lane, wave); break;
-      default: mx_tile<PHASE, 8>(f, t, lds0, lds1, lane, wave); break;
+      case 1: mx_tile<PHASE, 1>(f, t, lds0, lds1, wcodes[wave], wscales[wave], lane, wave); break;
+      case 2: mx_tile<PHASE, 2>(f, t, lds0, lds1, wcodes[wave], wscales[wave], lane, wave); break;
+      case 3: mx_tile<PHASE, 3>(f, t, lds0, lds1, wcodes[wave], wscales[wave], lane, wave); break;
+      case 4: mx_tile<PHASE, 4>(f, t, lds0, lds1, wcodes[wave], wscales[wave], lane, wave); break;
+      case 5: mx_tile<PHASE, 5>(f, t, lds0, lds1, wcodes[wave], wscales[wave], lane, wave); break;
+      case 6: mx_tile<PHASE, 6>(f, t, lds0, lds1, wcodes[wave], wscales[wave], lane, wave); break;
+      case 7: mx_tile<PHASE, 7>(f, t, lds0, lds1, wcodes[wave], wscales[wave], lane, wave); break;
+      default: mx_tile<PHASE, 8>(f, t, lds0, lds1, wcodes[wave], wscales[wave], lane, wave); break;
     }
   }
 }

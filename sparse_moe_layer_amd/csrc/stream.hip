@@ -322,10 +322,9 @@ hipError_t launch_ffn_stream(const FfnArgs& a, int phase, hipStream_t s, bool se
     sp = 2;
   }
   if (a.wt != kWtPlain) {
-    if (a.wt == kWtMx) {
-      const hipError_t e = launch_mx_stream(a, phase, s, self_plan);
-      if (e != hipSuccess) return e;
-    } else if (phase == 1) stream_kernel<1, true><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
+    // (launch_mx_stream has the routed groups of an MXFP4 layer)
+    if (a.wt == kWtMx) ;
+    else if (phase == 1) stream_kernel<1, true><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
     else stream_kernel<2, true><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
     if (a.Is > 0) {
       if (phase == 1 && split)
