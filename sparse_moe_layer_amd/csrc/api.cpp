@@ -7,7 +7,6 @@
 
 #include <cstdint>
 #include <cstring>
-#include <cstdlib>
 #include <mutex>
 
 #include "kernels.hpp"
@@ -309,16 +308,18 @@ Aux* aux_stream() {
 constexpr int kStreamReserve = 32;
 
 // From this many rows per expert on average, an MXFP4 layer's groups of at most
-// 16 rows run as m-tiles as well.
-static int kMxTileRows = getenv("MXTR") ? atoi(getenv("MXTR")) : 16;
+// 16 rows run as m-tiles as well: two launches less, and their reading overlaps
+// the large groups' products (4096 tokens over 512 experts 649 against 675 us, a
+// skewed 1023 over 64 1251 against 1257; 24 tokens over 512 experts 198 against 128).
+constexpr int kMxTileRows = 16;
 
-// The same for an MXFP4 layer: its routed groups have kernels of their own, and
-// the bf16 shared expert, which needs none of their results, is a chain of
-// launches beside theirs.
+// The FFN of an MXFP4 layer: its routed groups have kernels of their own, and the
+// bf16 shared expert, which needs none of their results, is a chain of launches
+// beside theirs (4096 tokens with a shared expert of 640: 681 -> 651 us).
 moe_status run_ffn_mx(const moe_problem* p, FfnArgs& a, int phases, int32_t* plan, hipStream_t s, bool fork_ok) {
   const bool force_gemm = p->flags & MOE_FLAG_FORCE_GEMM, force_stream = p->flags & MOE_FLAG_FORCE_STREAM;
   const bool few = p->T <= moe::kStreamMaxRows;  // every group is one m-block
-  const bool tiles_only = force_gemm || (!force_stream && p->T * p->k >= kMxTileRows * p->E);
+  const bool tiles_only = force_gemm || (!force_stream && !few && p->T * p->k >= kMxTileRows * p->E);
   const int stream_rows = tiles_only ? 0 : moe::kStreamMaxRows;
   const bool any_gemm = tiles_only || (!force_stream && !few), any_stream = !tiles_only;
   const bool self_plan = !any_gemm && few;
@@ -341,7 +342,8 @@ moe_status run_ffn_mx(const moe_problem* p, FfnArgs& a, int phases, int32_t* pla
     if (!(phases & phase)) continue;
     if (a.Is > 0) {
       const hipStream_t t = x ? x->s2 : s;
-      ok = ok && (sh_stream ? moe::launch_ffn_stream(a, phase, t, self_plan) : moe::launch_ffn_gemm(a, phase, t)) == hipSuccess;
+      ok = ok && (sh_stream ? moe::launch_ffn_stream(a, phase, t, self_plan)
+                            : moe::launch_ffn_gemm(a, phase, t)) == hipSuccess;
     }
     if (any_gemm) ok = ok && moe::launch_mx_tiles(a, phase, s) == hipSuccess;
     if (any_stream) ok = ok && moe::launch_mx_stream(a, phase, s, self_plan) == hipSuccess;

@@ -33,24 +33,31 @@ namespace fragdot {
 
 constexpr int kSc1 = 16;             // cache policy: coherent across the device's L2 caches
 constexpr int kNt = 2;               // non-temporal
-constexpr int kRunBytes = 256;       // of a weight row
-constexpr int kBuf = 16 * kRunBytes;  // a run of 16 rows
-constexpr int kLds = kBuf + 256;      // a wave's buffer, with 16 scale bytes of 16 rows (MXFP4)
+constexpr int kLds = 16 * 256 + 256;  // a wave's buffer: runs of 16 rows, and their scale bytes (MXFP4)
 
-// AROWS: the most activation rows of a job; 0: as many as fit a run of 16 weight rows.
-template <int WT, int AROWS = 0>
+// AROWS: the most activation rows of a job; 0: as many as fit a run of 16 weight
+// rows.  U_: 16-byte chunks per lane and 16 rows, 4 (runs of 256 bytes) or 2 (of 128).
+template <int WT, int AROWS = 0, int U_ = 4>
 struct Form {
   static constexpr int G = WT == kWtMx ? 32 : WT == kWtFp8 ? 16 : 8;  // values per 16-byte chunk
-  static constexpr int U = 4;                                         // chunks per lane and batch
-  static constexpr int KB = 4 * G * U;                                // K values per batch: 128, 256, 512
-  static constexpr int ROWS = AROWS ? AROWS : kBuf / (2 * KB);        // 0: 16, 8, 4
-  static constexpr int RPL = 512 / KB;                                // rows per load of them: 4, 2, 1
-  static constexpr int NL = ROWS / RPL;                               // loads of all of them: 4 (0)
+  static constexpr int U = U_;
+  static constexpr int KB = 4 * G * U;                                // K values per batch; U = 4: 128, 256, 512
+  static constexpr int RUN = 64 * U;                                  // bytes of a weight row's run
+  static constexpr int CPR = 4 * U;                                   // chunks of it
+  static constexpr int WPL = 64 / CPR;                                // weight rows per load: 4 or 8
+  static constexpr int NW = 16 / WPL;                                 // loads of 16 weight rows
+  static constexpr int ROWS = AROWS ? AROWS : 16 * RUN / (2 * KB);    // 0: 16, 8, 4
+  static constexpr int RPL = 512 / KB;                                // activation rows per load; U = 4: 4, 2, 1
+  static constexpr int NL = ROWS / RPL;                               // loads of all of them
   static constexpr int BUF = 2 * KB * ROWS;                           // bytes of them
   static constexpr int LDS = BUF + 256;
-  static_assert(BUF >= kBuf, "the weights pass through the same buffer");
   static constexpr int NS = WT == kWtMx ? 2 : KB / 128;               // scale registers of a batch
+  static_assert(U == 4 || (U == 2 && WT == kWtMx), "half runs: MXFP4");
+  static_assert(BUF >= 16 * RUN, "the weights pass through the same buffer");
+  // Chunk c of row r lies at c ^ swizzle(r): the 16 rows of a chunk in 16 bank groups.
+  static __device__ __forceinline__ int swizzle(int r) { return U == 4 ? r : (r >> 1) & 7; }
 };
+
 
 // bytes of n weights along K
 template <int WT>
@@ -94,10 +101,10 @@ struct Job {
 // a job's row r < rows.  k0 is a multiple of 128, K of 128 (fp8), 32 (MXFP4) or 8.
 // lds: the wave's Form::LDS bytes.  gate(): called once if there is a job, after
 // the first weights have been asked for and before any activation is.
-template <int WT, int NB, int AUXA, int AROWS = 0, class Rows, class Next, class After, class Gate>
+template <int WT, int NB, int AUXA, int AROWS = 0, int U_ = 4, class Rows, class Next, class After, class Gate>
 __device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, int lane, char* lds, Rows row_of,
                                     Next next, After after, Gate gate) {
-  using F = Form<WT, AROWS>;
+  using F = Form<WT, AROWS, U_>;
   constexpr int G = F::G, U = F::U;
   constexpr uint32_t kNone = 0x80000000u;  // past any weight rows: reads as zeros, fetches nothing
   constexpr uint32_t kOut = 0xFFFFFFF0u;   // past any activations
@@ -105,12 +112,12 @@ __device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, i
   const int q = lane >> 4, n = lane & 15;
   const uint32_t rowb = (uint32_t)wbytes<WT>(K);
   const __amdgpu_buffer_rsrc_t ares = resource(abase, abytes);
-  char* const put = lds + q * kRunBytes;  // chunk c of row r lies at c ^ r: the 16 rows of a chunk in 16 bank groups
+  const int wr = lane / F::CPR, wc = lane % F::CPR;  // this lane's row and chunk of a weight load
   Job<NB> job{};
   bool have = true, fresh = true, pending = false, first = true;  // fresh: a new job is due
   int kb = 0;
   // the batch in flight
-  u32x4 t[NB][4], at[F::NL];
+  u32x4 t[NB][F::NW], at[F::NL];
   uint32_t sd[NB][F::NS], shift[NB];
   uint32_t aoff[F::NL];
   // the batch being multiplied
@@ -128,17 +135,18 @@ __device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, i
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<u32x4*>(put + i * 4 * kRunBytes + ((n ^ (4 * i + q)) << 4)) = t[b][i];
+        for (int i = 0; i < F::NW; ++i)
+          *reinterpret_cast<u32x4*>(lds + (i * F::WPL + wr) * F::RUN + ((wc ^ F::swizzle(i * F::WPL + wr)) << 4)) =
+              t[b][i];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          wv[b][u] = *reinterpret_cast<const u32x4*>(lds + n * kRunBytes + (((4 * u + q) ^ n) << 4));
+          wv[b][u] = *reinterpret_cast<const u32x4*>(lds + n * F::RUN + (((4 * u + q) ^ F::swizzle(n)) << 4));
         if constexpr (WT == kWtMx) {
-          *reinterpret_cast<uint32_t*>(lds + F::BUF + lane * 4) =
+          *reinterpret_cast<uint32_t*>(lds + F::BUF + (lane >> 2) * 4 * U + (lane & (U - 1)) * 4) =
               __builtin_amdgcn_alignbyte(sd[b][1], sd[b][0], shift[b]);
-          const u32x4 s = *reinterpret_cast<const u32x4*>(lds + F::BUF + n * 16);
 #pragma unroll
-          for (int u = 0; u < U; ++u) sv[b][u] = (s[u] >> (8 * q)) & 255u;
+          for (int u = 0; u < U; ++u)
+            sv[b][u] = (*reinterpret_cast<const uint32_t*>(lds + F::BUF + n * 4 * U + 4 * u) >> (8 * q)) & 255u;
           if (c_kb + F::KB > K) {  // what lies behind the row's scales is not one of them
 #pragma unroll
             for (int u = 0; u < U; ++u) sv[b][u] = c_kb + 4 * G * u + G * q < K ? sv[b][u] : 0u;
@@ -161,23 +169,24 @@ __device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, i
     int n_rows = 0, n_ar = 0, n_kb = 0, n_tag = 0;
     bool n_last = false;
     if (have) {
-      const uint32_t k0 = (uint32_t)wbytes<WT>(kb) + (uint32_t)n * 16u, k1 = (uint32_t)wbytes<WT>(job.kend);
-      const uint32_t v = k0 < k1 ? (uint32_t)q * rowb + k0 : kNone;
+      const uint32_t k0 = (uint32_t)wbytes<WT>(kb) + (uint32_t)wc * 16u, k1 = (uint32_t)wbytes<WT>(job.kend);
+      const uint32_t v = k0 < k1 ? (uint32_t)wr * rowb + k0 : kNone;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const __amdgpu_buffer_rsrc_t w0 = resource(job.w[2 * b], (uint32_t)job.wrows[2 * b] * rowb);
         const __amdgpu_buffer_rsrc_t w1 = resource(job.w[2 * b + 1], (uint32_t)job.wrows[2 * b + 1] * rowb);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          t[b][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                  i < 2 ? w0 : w1, v + (uint32_t)(i & 1) * 4u * rowb, 0, kNt));
+        for (int i = 0; i < F::NW; ++i)
+          t[b][i] = __builtin_bit_cast(
+              u32x4, __builtin_amdgcn_raw_buffer_load_b128(i < F::NW / 2 ? w0 : w1,
+                                                           v + (uint32_t)(i % (F::NW / 2) * F::WPL) * rowb, 0, kNt));
       }
       if constexpr (WT == kWtMx) {
-        // The 4 scale bytes of chunks 4 (lane % 4) .. + 3 of a run: a dword, or, with
+        // The 4 scale bytes of chunks 4 (lane % U) .. + 3 of a run: a dword, or, with
         // rows that are no multiple of 4 scales, its parts in two aligned dwords
         // (each holding a byte of the row, so that none lies outside the tensor).
         const int groups = K >> 5;
-        int i = (kb >> 5) + 4 * (lane & 3);
+        int i = (kb >> 5) + 4 * (lane & (U - 1));
         i = i < groups ? i : 0;
         const int e = i + 3 < groups ? i + 3 : groups - 1;
 #pragma unroll

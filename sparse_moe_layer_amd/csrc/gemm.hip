@@ -645,10 +645,10 @@ hipError_t launch_ffn_gemm(const FfnArgs& a, int phase, hipStream_t s) {
   RouterArgs none{};
   if (a.wt != kWtPlain) {
     // routed tiles [0, plan[2]) decode their codes; the shared expert stays bf16
-    // (launch_mx_tiles has the routed tiles of an MXFP4 layer)
-    if (a.wt == kWtMx) ;
-    else if (phase == 1) gemm_kernel<M_GATEUP, true><<<grid, NT, 0, s>>>(a, none, ntn, kPlanStart, kPlanRoutedTiles);
-    else gemm_kernel<M_DOWN, true><<<grid, NT, 0, s>>>(a, none, ntn, kPlanStart, kPlanRoutedTiles);
+    // (an MXFP4 layer's routed tiles: launch_mx_tiles)
+    if (a.wt == kWtFp8 && phase == 1)
+      gemm_kernel<M_GATEUP, true><<<grid, NT, 0, s>>>(a, none, ntn, kPlanStart, kPlanRoutedTiles);
+    else if (a.wt == kWtFp8) gemm_kernel<M_DOWN, true><<<grid, NT, 0, s>>>(a, none, ntn, kPlanStart, kPlanRoutedTiles);
     if (sh) {
       if (phase == 1) gemm_kernel<M_GATEUP, false><<<grid, NT, 0, s>>>(a, none, ntn, kPlanRoutedTiles, kPlanTiles);
       else gemm_kernel<M_DOWN, false><<<grid, NT, 0, s>>>(a, none, ntn, kPlanRoutedTiles, kPlanTiles);

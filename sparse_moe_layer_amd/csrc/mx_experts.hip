@@ -13,6 +13,8 @@
 //
 //   mx_stream_kernel: groups of at most 16 rows; bound by reading the codes once
 //   mx_tiles_kernel : 128-row m-tiles; bound by the matrix rate
+#include <type_traits>
+
 #include "common.hpp"
 #include "frag_dot.hpp"
 #include "kernels.hpp"
@@ -35,22 +37,147 @@ int cu_count() {
 }
 
 // ---- groups of at most 16 rows ---------------------------------------------
-// An item is 32 weight rows (gate/up: 16 gate rows and the 16 up rows of the same
-// hidden columns; down: 32 output columns) and all rows of a group's m-block; a
-// wave goes through its items in one stream of loads.  With fewer items than
-// waves, P waves of a workgroup share an item's K range and add their blocks in
-// LDS in K order.
+// An item is SB blocks of 16 weight rows and all rows of a group's m-block: with 4
+// blocks 32 gate rows and the 32 up rows of the same hidden columns, or 64 output
+// columns; with one, 8 gate and 8 up rows, or 16 output columns.  A wave goes
+// through its items in one stream of loads, 128 bytes of 8 rows each.  With fewer
+// items than waves, P waves of a workgroup share an item's K range and add their
+// blocks in LDS in K order.
+//   4 blocks use each activation fragment four times, which a batch of 24 tokens
+// needs (512 experts, 2560 x 640: 120.5 us; 2 blocks and 256-byte runs, whose K
+// step of 512 also fits a K of 640 badly, 128.4).  One block is for the few items
+// of a small group list, where 4 leave compute units idle even with K split 8 ways
+// (one token, a dense 8192 x 2048: 22.2 us with 4, 17.5 with 2).
 constexpr int kLogSW = 3, SW = 1 << kLogSW;  // waves per workgroup, one workgroup per compute unit
-using SF = fragdot::Form<kWtMx, kStreamBM>;
+using SF = fragdot::Form<kWtMx, kStreamBM, 2>;
+
+template <int PHASE, int SB>
+__device__ __forceinline__ void mx_stream_items(const FfnArgs& f, int self_plan, int nblocks, const Divisor& slabs,
+                                                const int* glist, char* act, f32x4 (*part)[4][64], int lane,
+                                                int wave) {
+  constexpr int COLS = (PHASE == 1 ? 8 : 16) * SB;  // output columns of an item
+  const int K = PHASE == 1 ? f.H : f.I, N = PHASE == 1 ? f.I : f.H;
+  const int grid = (int)gridDim.x, waves = grid * SW;
+  const int total = nblocks * slabs.d, units = (K + 127) >> 7;
+  int lp = 0;  // P = 1 << lp
+  while (1 << lp < SW && (total << (lp + 1)) <= waves + waves / 4 && 2 << lp <= units) ++lp;
+  const int P = 1 << lp, p = wave & (P - 1);
+  const int q = lane >> 4, m = lane & 15;
+
+  auto finish = [&](int item, const f32x4 (&v)[SB]) {  // lane: column m, rows 4 q + i
+    int sb, slab;
+    slabs.divide(item, sb, slab);
+    int base, nrows;
+    if (self_plan) {
+      const int g = glist[sb];
+      base = f.offsets[g];
+      nrows = f.offsets[g + 1] - base;
+    } else {
+      base = f.sb_base[sb] + f.sb_row0[sb];
+      nrows = f.sb_nrows[sb];
+    }
+    const int ld = PHASE == 1 ? f.I : f.H;
+    bf16* out = reinterpret_cast<bf16*>(PHASE == 1 ? f.h : f.y) + (int64_t)(base + 4 * q) * ld;
+#pragma unroll
+    for (int b = 0; b < (PHASE == 1 && SB > 1 ? SB / 2 : SB); ++b) {
+      const int col = slab * COLS + 16 * b + m;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float o = v[b][i];
+        if (PHASE == 1) o = silu(o) * (SB > 1 ? v[(b + SB / 2) % SB][i] : __shfl_xor(o, 8, 64));  // (lane m + 8's)
+        if (4 * q + i < nrows && col < N && (PHASE != 1 || SB > 1 || m < 8)) out[(int64_t)i * ld + col] = f2bf(o);
+      }
+    }
+  };
+  // P > 1: the workgroup takes SW / P items at a time
+  const int step = P > 1 ? grid * (SW >> lp) : waves;
+  int item = P > 1 ? ((int)blockIdx.x << (kLogSW - lp)) + (wave >> lp) : (int)blockIdx.x * SW + wave;
+  const int rounds = P > 1 ? (total - ((int)blockIdx.x << (kLogSW - lp)) + step - 1) / step : 1;
+  for (int round = 0; round < rounds; ++round) {
+    bool todo = item < total;
+    const int first = item;
+    f32x4 v[SB] = {};
+    fragdot::run<kWtMx, SB, 0, kStreamBM, 2>(
+        PHASE == 1 ? f.x : f.h, (uint32_t)(PHASE == 1 ? f.T : f.T * f.k) * (uint32_t)K * 2u, K, lane, act,
+        [&](const auto& j, int r) {
+          if (PHASE != 1) return j.base + r;
+          int tok = self_plan ? f.sorted[j.base + r] / f.k : f.sb_tok[j.base + r];
+          return (unsigned)tok < (unsigned)f.T ? tok : f.T - 1;  // also clamps a negative index
+        },
+        [&](auto& j) {
+          if (!todo) return false;
+          int sb, slab, g;
+          slabs.divide(item, sb, slab);
+          if (self_plan) {
+            g = uniform(glist[sb]);
+            j.base = uniform(f.offsets[g]);
+            j.rows = uniform(f.offsets[g + 1]) - j.base;
+          } else {
+            g = uniform(f.sb_group[sb]);
+            j.base = PHASE == 1 ? sb * kStreamBM : uniform(f.sb_base[sb]) + uniform(f.sb_row0[sb]);
+            j.rows = uniform(f.sb_nrows[sb]);
+          }
+          j.rows = j.rows < kStreamBM ? j.rows : kStreamBM;
+          j.ar = m < j.rows ? m : 0;
+          const int c0 = slab * COLS;
+#pragma unroll
+          for (int i = 0; i < 2 * SB; ++i) {  // half blocks of 8 rows
+            const bool up = i >= SB;
+            const void* w = PHASE != 1 ? f.wd : up ? f.wu : f.wg;
+            const int64_t stride = PHASE != 1 ? f.sd : up ? f.su : f.sg;
+            const int r0 = c0 + 8 * (PHASE == 1 ? i % SB : i), left = N - r0;
+            j.w[i] = static_cast<const char*>(w) + ((int64_t)g * stride + (int64_t)(left > 0 ? r0 : 0) * K) / 2;
+            j.wrows[i] = left < 8 ? (left > 0 ? left : 0) : 8;
+          }
+#pragma unroll
+          for (int b = 0; b < SB; ++b) {  // of row lane / 4
+            const int r = 16 * b + (lane >> 2);
+            const bool up = r >= 8 * SB;
+            const float* sc = PHASE != 1 ? f.scd : up ? f.scu : f.scg;
+            const int n = c0 + (PHASE == 1 && up ? r - 8 * SB : r);
+            j.scale[b] = reinterpret_cast<const uint8_t*>(sc) + ((int64_t)g * N + (n < N ? n : N - 1)) * (K / 32);
+          }
+          j.k0 = ((p * units) >> lp) * 128;
+          const int ke = (((p + 1) * units) >> lp) * 128;
+          j.kend = ke < K ? ke : K;
+          j.tag = item;
+          item += step;
+          todo = P == 1 && item < total;
+          return true;
+        },
+        [&](int at, const f32x4 (&acc)[SB]) {
+          if (P == 1) {
+            finish(at, acc);
+          } else {
+#pragma unroll
+            for (int b = 0; b < SB; ++b) v[b] = acc[b];
+          }
+        },
+        fragdot::NoGate{});
+    if (P > 1) {
+#pragma unroll
+      for (int b = 0; b < SB; ++b) part[wave][b][lane] = v[b];  // added in K order
+      __syncthreads();
+      if (p == 0 && first < total) {
+        for (int w = 1; w < P; ++w)
+#pragma unroll
+          for (int b = 0; b < SB; ++b) v[b] += part[wave + w][b][lane];
+        finish(first, v);
+      }
+      __syncthreads();
+      if (first >= total) item += step;  // (not taken in this round)
+    }
+  }
+}
 
 template <int PHASE>
-__global__ __launch_bounds__(SW * 64, 2) void mx_stream_kernel(FfnArgs f, int self_plan, Divisor slabs) {
+__global__ __launch_bounds__(SW * 64, 2) void mx_stream_kernel(FfnArgs f, int self_plan, Divisor wide,
+                                                               Divisor narrow) {
   __shared__ __attribute__((aligned(16))) char act[SW][SF::LDS];
-  __shared__ f32x4 part[SW][2][64];
+  __shared__ f32x4 part[SW][4][64];
   __shared__ int glist[kMaxExperts];  // self_plan: the touched groups, ascending
   __shared__ int wtot[SW];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-  const int K = PHASE == 1 ? f.H : f.I, N = PHASE == 1 ? f.I : f.H;
   int nblocks;
   if (self_plan) {
     nblocks = 0;
@@ -72,118 +199,11 @@ __global__ __launch_bounds__(SW * 64, 2) void mx_stream_kernel(FfnArgs f, int se
   } else {
     nblocks = uniform(f.plan[kPlanRoutedBlocks]);
   }
-  const int grid = (int)gridDim.x, waves = grid * SW;
-  const int total = nblocks * slabs.d, units = (K + 127) >> 7;
-  int lp = 0;  // P = 1 << lp
-  while (1 << lp < SW && (total << (lp + 1)) <= waves + waves / 4 && 2 << lp <= units) ++lp;
-  const int P = 1 << lp, p = wave & (P - 1);
-  const int q = lane >> 4, m = lane & 15;
-
-  auto finish = [&](int item, const f32x4& v0, const f32x4& v1) {  // lane: column m, rows 4 q + i
-    int sb, slab;
-    slabs.divide(item, sb, slab);
-    int base, nrows;
-    if (self_plan) {
-      const int g = glist[sb];
-      base = f.offsets[g];
-      nrows = f.offsets[g + 1] - base;
-    } else {
-      base = f.sb_base[sb] + f.sb_row0[sb];
-      nrows = f.sb_nrows[sb];
-    }
-    if (PHASE == 1) {
-      const int col = slab * 16 + m;
-      bf16* h = reinterpret_cast<bf16*>(f.h) + (int64_t)base * f.I + col;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (4 * q + i < nrows && col < f.I) h[(int64_t)(4 * q + i) * f.I] = f2bf(silu(v0[i]) * v1[i]);
-    } else {
-      const int col = slab * 32 + m;
-      bf16* y = reinterpret_cast<bf16*>(f.y) + (int64_t)base * f.H + col;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (4 * q + i < nrows && col < f.H) y[(int64_t)(4 * q + i) * f.H] = f2bf(v0[i]);
-        if (4 * q + i < nrows && col + 16 < f.H) y[(int64_t)(4 * q + i) * f.H + 16] = f2bf(v1[i]);
-      }
-    }
-  };
-  // P > 1: the workgroup takes SW / P items at a time
-  const int step = P > 1 ? grid * (SW >> lp) : waves;
-  int item = P > 1 ? ((int)blockIdx.x << (kLogSW - lp)) + (wave >> lp) : (int)blockIdx.x * SW + wave;
-  const int rounds = P > 1 ? (total - ((int)blockIdx.x << (kLogSW - lp)) + step - 1) / step : 1;
-  for (int round = 0; round < rounds; ++round) {
-    bool todo = item < total;
-    const int first = item;
-    f32x4 v[2] = {};
-    fragdot::run<kWtMx, 2, 0, kStreamBM>(
-        PHASE == 1 ? f.x : f.h, (uint32_t)(PHASE == 1 ? f.T : f.T * f.k) * (uint32_t)K * 2u, K, lane, act[wave],
-        [&](const auto& j, int r) {
-          if (PHASE != 1) return j.base + r;
-          int tok = self_plan ? f.sorted[j.base + r] / f.k : f.sb_tok[j.base + r];
-          return (unsigned)tok < (unsigned)f.T ? tok : f.T - 1;  // also clamps a negative index
-        },
-        [&](auto& j) {
-          if (!todo) return false;
-          int sb, slab, g;
-          slabs.divide(item, sb, slab);
-          if (self_plan) {
-            g = uniform(glist[sb]);
-            j.base = uniform(f.offsets[g]);
-            j.rows = uniform(f.offsets[g + 1]) - j.base;
-          } else {
-            g = uniform(f.sb_group[sb]);
-            j.base = PHASE == 1 ? sb * kStreamBM : uniform(f.sb_base[sb]) + uniform(f.sb_row0[sb]);
-            j.rows = uniform(f.sb_nrows[sb]);
-          }
-          j.rows = j.rows < kStreamBM ? j.rows : kStreamBM;
-          j.ar = m < j.rows ? m : 0;
-          const int c0 = slab * (PHASE == 1 ? 16 : 32);
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const void* w = PHASE != 1 ? f.wd : b ? f.wu : f.wg;
-            const float* sc = PHASE != 1 ? f.scd : b ? f.scu : f.scg;
-            const int64_t stride = PHASE != 1 ? f.sd : b ? f.su : f.sg;
-            const int r0 = PHASE == 1 ? c0 : c0 + 16 * b;
-            const int left = N - r0 < 16 ? (N > r0 ? N - r0 : 0) : 16;
-            j.w[2 * b] = static_cast<const char*>(w) + ((int64_t)g * stride + (int64_t)(left ? r0 : 0) * K) / 2;
-            j.w[2 * b + 1] = j.w[2 * b] + 4 * (int64_t)K;
-            j.wrows[2 * b] = left < 8 ? left : 8;
-            j.wrows[2 * b + 1] = left < 8 ? 0 : left - 8;
-            const int n = r0 + (lane >> 2);
-            j.scale[b] = reinterpret_cast<const uint8_t*>(sc) + ((int64_t)g * N + (n < N ? n : N - 1)) * (K / 32);
-          }
-          j.k0 = ((p * units) >> lp) * 128;
-          const int ke = (((p + 1) * units) >> lp) * 128;
-          j.kend = ke < K ? ke : K;
-          j.tag = item;
-          item += step;
-          todo = P == 1 && item < total;
-          return true;
-        },
-        [&](int at, const f32x4 (&acc)[2]) {
-          if (P == 1) {
-            finish(at, acc[0], acc[1]);
-          } else {
-            v[0] = acc[0];
-            v[1] = acc[1];
-          }
-        },
-        fragdot::NoGate{});
-    if (P > 1) {
-      part[wave][0][lane] = v[0];  // added in K order
-      part[wave][1][lane] = v[1];
-      __syncthreads();
-      if (p == 0 && first < total) {
-        for (int w = 1; w < P; ++w) {
-          v[0] += part[wave + w][0][lane];
-          v[1] += part[wave + w][1][lane];
-        }
-        finish(first, v[0], v[1]);
-      }
-      __syncthreads();
-      if (first >= total) item += step;  // (not taken in this round)
-    }
-  }
+  // one block an item where items of 4 do not even give every workgroup one
+  if (nblocks * wide.d >= (int)gridDim.x)
+    mx_stream_items<PHASE, 4>(f, self_plan, nblocks, wide, glist, act[wave], part, lane, wave);
+  else
+    mx_stream_items<PHASE, 1>(f, self_plan, nblocks, narrow, glist, act[wave], part, lane, wave);
 }
 
 // ---- 128-row m-tiles ---------------------------------------------------------
@@ -193,23 +213,25 @@ __global__ __launch_bounds__(SW * 64, 2) void mx_stream_kernel(FfnArgs f, int se
 // rows.  A step is 128 values of K: activations go to LDS by direct loads, one
 // step ahead in the other of two buffers, chunk c (16 bytes) of row r at
 // c ^ (r % 16) of its 256 bytes, so a fragment read's 16 rows lie in 16 bank
-// groups.  Codes go to registers, also a step ahead, 64 bytes of 16 rows a load
-// with four consecutive lanes to a row, take their fragment order through 1 KB of
-// LDS of the wave, and become bf16 in registers (loaded in fragment order, a lane
-// to a row, they cost the address unit a quarter of the kernel's time; a skewed
-// layer of 1023 tokens took 1265 us with scale bytes loaded so as well, 857
-// without the codes' loads, 980 without the scales').  The scale bytes of 7 steps
-// go to LDS by direct loads, 32 bytes of a row.
+// groups.  Codes go to registers two steps at a time, whole 128-byte lines of 8
+// rows a load, take their fragment order through 2 KB of LDS of the wave, and
+// become bf16 in registers.  The scale bytes of 3 steps go to LDS by a direct load,
+// 16 bytes of a row.
+//   A skewed layer of 1023 tokens (8192 x 2048, 64 experts) took 1265 us with codes
+// and scale bytes loaded in fragment order, a lane to a row, which kept the address
+// unit busy; 1061 with 64-byte rows, which cross L2 in two halves; 1035 so.  Of
+// those 690 remain without any load.
 constexpr int TW = 4;          // waves
 constexpr int TK = 128;        // K per step
 constexpr int TN = 256;        // weight rows per tile
 constexpr int TBUF = kGemmBM * TK * 2;
 constexpr int kAhead = 3;      // activation fragments read ahead of their use
-constexpr int kScaleSteps = 7;  // steps whose scale bytes lie in LDS: 28 bytes and up to 3 before them
+constexpr int kScaleSteps = 3;  // steps whose scale bytes lie in LDS: 12 bytes and up to 3 before them
 constexpr uint32_t kOut = 0xFFFFFFF0u;  // an offset past any buffer: reads as zeros
 
 struct MxTile {  // a tile's rows and columns
   int g, base, r0, nrows, nt;
+  bool once;  // the group's only m-tile: its codes are read once
 };
 
 // Fragments of step kt from one buffer times the step's codes, while `fetch`
@@ -272,20 +294,17 @@ __device__ __forceinline__ void mx_tile(const FfnArgs& f, const MxTile& t, char*
     }
     aoff[i] = (uint32_t)row * (uint32_t)K * 2u + 16u * (uint32_t)ac;
   }
-  // weight rows; columns past the matrix are computed, never stored
+  // weight rows, each `groups` scale bytes and 16 times as many of codes in the
+  // expert's (which are aligned); what lies past the matrix reads as zeros
   __amdgpu_buffer_rsrc_t wres[PHASE == 1 ? 2 : 1], sres[PHASE == 1 ? 2 : 1];
-  auto row_of = [&](int b, int r) {  // of block b: its first scale byte, in the expert's (which are aligned)
-    const int n = (PHASE == 1 ? t.nt * (TN / 2) + wave * 32 + (b & 1) * 16 : t.nt * TN + wave * 64 + b * 16) + r;
-    return (uint32_t)(n < N ? n : N - 1) * (uint32_t)groups;
-  };
-  uint32_t wrow[4], soff[4];  // codes: row lane / 4, chunk lane % 4 of a step; scales in LDS: of row m, chunk q
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    wrow[b] = row_of(b, lane >> 2) * 16u + 16u * (lane & 3);
-    soff[b] = (b * 16 + m) * 32 + (row_of(b, m) & 3u) + q;
-  }
-  char* const cput = codes + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 4)) << 4);  // 16 rows of a chunk in 16 bank groups
-  const char* const cget = codes + m * 64 + ((q ^ (m >> 2)) << 4);
+  const uint32_t n0 = PHASE == 1 ? t.nt * (TN / 2) + wave * 32 : t.nt * TN + wave * 64;
+  const uint32_t block = 16u * (uint32_t)groups;  // scale bytes of a block's rows (a multiple of 4)
+  // codes: row lane / 8, chunk lane % 8 of two steps; scales in LDS: of row m, chunk q
+  const uint32_t wrow = (n0 + (lane >> 3)) * block + 16u * (lane & 7);
+  const uint32_t soff = m * 16 + (((n0 + m) * (uint32_t)groups) & 3u) + q;
+  // chunk c of row r lies at c ^ (r / 2 % 8): 16 rows of a chunk in 16 bank groups
+  const int cput = (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 4)) << 4);
+  const int cget = m * 128 + ((q ^ (m >> 1)) << 4);
   const uint32_t sbytes = (uint32_t)N * (uint32_t)groups;
 #pragma unroll
   for (int j = 0; j < (PHASE == 1 ? 2 : 1); ++j) {
@@ -305,23 +324,35 @@ __device__ __forceinline__ void mx_tile(const FfnArgs& f, const MxTile& t, char*
 #pragma unroll
     for (int b = 0; b < 4; ++b) acc[i][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  u32x4 wn[4];
-  auto load_scales = [&](int kt) {  // of steps kt .. + 6: 32 rows a load, 16 bytes a lane from an aligned place on
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t at = (row_of(2 * j + (lane >> 5), (lane >> 1) & 15) & ~3u) + kt * 4 + 16 * (lane & 1);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(sres[PHASE == 1 ? j : 0],
-                                               (__attribute__((address_space(3))) void*)(scales + j * 1024), 16, at, 0, 0,
-                                               0);
+  u32x4 wa[4], wb[4];  // codes of the next two steps: rows 0-7 and 8-15 of each block, then (wb) of the odd step
+  auto load_scales = [&](int kt) {  // of steps kt .. + 2: 64 rows, 16 bytes a lane from an aligned place on
+    const uint32_t r = n0 + (PHASE == 1 ? lane & 31 : lane);
+    const uint32_t at = ((r * (uint32_t)groups) & ~3u) + kt * 4;
+    auto* const to = (__attribute__((address_space(3))) void*)scales;
+    if (PHASE == 1) {  // half the lanes from each matrix
+      if (lane < 32) __builtin_amdgcn_raw_ptr_buffer_load_lds(sres[0], to, 16, at, 0, 0, 0);
+      else __builtin_amdgcn_raw_ptr_buffer_load_lds(sres[PHASE == 1 ? 1 : 0], to, 16, at, 0, 0, 0);
+    } else {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(sres[0], to, 16, at, 0, 0, 0);
     }
+  };
+  auto load_codes = [&](int kt) {  // of steps kt and kt + 1: 128 bytes of 8 rows a load
+    const uint32_t k = (uint32_t)kt * TK;
+    const uint32_t at = (int)k + (lane & 7) * 32 < K ? wrow + k / 2 : kOut;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t row = ((PHASE == 1 ? b & 1 : b) * 16 + 8 * j) * block;
+        const __amdgpu_buffer_rsrc_t r = wres[PHASE == 1 ? b >> 1 : 0];
+        (j ? wb : wa)[b] =
+            __builtin_bit_cast(u32x4, t.once ? __builtin_amdgcn_raw_buffer_load_b128(r, at, row, fragdot::kNt)
+                                             : __builtin_amdgcn_raw_buffer_load_b128(r, at, row, 0));
+      }
   };
   auto load = [&](int kt, char* buf) {
     const uint32_t k = (uint32_t)kt * TK;
-    const bool win = (int)k + (lane & 3) * 32 < K, in = (int)k + ac * 8 < K;
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-      wn[b] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wres[PHASE == 1 ? b >> 1 : 0],
-                                                                              win ? wrow[b] + k / 2 : kOut, 0, 0));
+    const bool in = (int)k + ac * 8 < K;
 #pragma unroll
     for (int i = 0; i < NBLK; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -329,7 +360,7 @@ __device__ __forceinline__ void mx_tile(const FfnArgs& f, const MxTile& t, char*
           in ? aoff[i] + 2u * k : kOut, 0, 0, 0);
   };
   int sk = 0;  // the step's place among those whose scales lie in LDS
-  auto step = [&](int kt, const char* here, char* there) {
+  auto step = [&](int kt, const char* here, char* there, auto odd) {
     __builtin_amdgcn_s_waitcnt(0xF70);  // vmcnt(0): this wave's loads of the step have arrived
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();  // every wave's have, and every wave is done with the other buffer
@@ -339,9 +370,15 @@ __device__ __forceinline__ void mx_tile(const FfnArgs& f, const MxTile& t, char*
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       // (LDS operations of one wave are executed in order)
-      *reinterpret_cast<u32x4*>(cput) = wn[b];
-      w[b] = *reinterpret_cast<const u32x4*>(cget);
-      const uint32_t s = *reinterpret_cast<const uint8_t*>(scales + soff[b] + 4 * sk);
+      if (odd) {
+        w[b] = wb[b];
+      } else {
+        *reinterpret_cast<u32x4*>(codes + cput) = wa[b];
+        *reinterpret_cast<u32x4*>(codes + 1024 + (cput ^ 64)) = wb[b];
+        w[b] = *reinterpret_cast<const u32x4*>(codes + cget);
+        wb[b] = *reinterpret_cast<const u32x4*>(codes + (cget ^ 64));
+      }
+      const uint32_t s = *reinterpret_cast<const uint8_t*>(scales + soff + b * 256 + 4 * sk);
       sc[b] = e8m0(kt * TK + q * 32 < K ? s : 0u);  // (what lies behind a row's scales is not one of them)
     }
     mx_step<NBLK>(acc, here, w, sc, aswz, [&] {
@@ -352,14 +389,16 @@ __device__ __forceinline__ void mx_tile(const FfnArgs& f, const MxTile& t, char*
         load_scales(kt + 1);
       }
       if (kt + 1 < steps) load(kt + 1, there);
+      if (odd && kt + 1 < steps) load_codes(kt + 1);
     });
   };
   load_scales(0);
+  load_codes(0);
   load(0, lds0);
 #pragma unroll 1
   for (int kt = 0; kt < steps; kt += 2) {
-    step(kt, lds0, lds1);
-    if (kt + 1 < steps) step(kt + 1, lds1, lds0);
+    step(kt, lds0, lds1, std::false_type{});
+    if (kt + 1 < steps) step(kt + 1, lds1, lds0, std::true_type{});
   }
   asm volatile("" : "+v"(lane));
   q = lane >> 4, m = lane & 15;
@@ -398,15 +437,16 @@ template <int PHASE>
 __global__ __launch_bounds__(TW * 64, 2) void mx_tiles_kernel(FfnArgs f, Divisor ntn, int32_t* counters) {
   __shared__ __attribute__((aligned(1024))) char lds0[TBUF];
   __shared__ __attribute__((aligned(1024))) char lds1[TBUF];  // (apart: a read of one waits for no load to the other)
-  __shared__ __attribute__((aligned(16))) char wcodes[TW][1024];  // per wave: a block's codes
-  __shared__ __attribute__((aligned(16))) char wscales[TW][64 * 32];  // and its 64 rows' scale bytes
+  __shared__ __attribute__((aligned(16))) char wcodes[TW][2048];  // per wave: a block's codes of two steps
+  __shared__ __attribute__((aligned(16))) char wscales[TW][64 * 16];  // and its 64 rows' scale bytes
   __shared__ int claim;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int mts = uniform(f.plan[kPlanRoutedTiles]);
   // Each XCD (workgroup i runs on XCD i % 8) has every eighth m-tile with all its
   // n-tiles, n fastest, so that an m-tile's activations are read into one L2; its
-  // workgroups claim them one by one, then help the XCD that has most left.
-  auto tiles_of = [&](int x) { return (mts - x + 7) / 8 * ntn.d; };
+  // workgroups claim them one by one, then help the XCD that has most left.  (Sets of
+  // 4 consecutive m-tiles to an XCD, for a large group's codes, measured the same.)
+  auto tiles_of = [&](int x) { return ((mts - x + 7) >> 3) * ntn.d; };
   bool own = true;
   for (;;) {
     if (wave == 0) {
@@ -450,6 +490,7 @@ __global__ __launch_bounds__(TW * 64, 2) void mx_tiles_kernel(FfnArgs f, Divisor
     t.r0 = uniform(f.mt_row0[mt]);
     t.base = uniform(f.offsets[t.g]);
     t.nrows = uniform(f.offsets[t.g + 1]) - t.base - t.r0;
+    t.once = t.r0 == 0 && t.nrows <= kGemmBM;
     t.nrows = t.nrows < kGemmBM ? t.nrows : kGemmBM;
     switch ((t.nrows + 15) >> 4) {
       case 1: mx_tile<PHASE, 1>(f, t, lds0, lds1, wcodes[wave], wscales[wave], lane, wave); break;
@@ -468,8 +509,8 @@ __global__ __launch_bounds__(TW * 64, 2) void mx_tiles_kernel(FfnArgs f, Divisor
 
 hipError_t launch_mx_stream(const FfnArgs& a, int phase, hipStream_t s, bool self_plan) {
   const int grid = cu_count();
-  if (phase == 1) mx_stream_kernel<1><<<grid, SW * 64, 0, s>>>(a, self_plan ? 1 : 0, Divisor((a.I + 15) / 16));
-  else mx_stream_kernel<2><<<grid, SW * 64, 0, s>>>(a, self_plan ? 1 : 0, Divisor((a.H + 31) / 32));
+  if (phase == 1) mx_stream_kernel<1><<<grid, SW * 64, 0, s>>>(a, self_plan ? 1 : 0, Divisor((a.I + 31) / 32), Divisor((a.I + 7) / 8));
+  else mx_stream_kernel<2><<<grid, SW * 64, 0, s>>>(a, self_plan ? 1 : 0, Divisor((a.H + 63) / 64), Divisor((a.H + 15) / 16));
   return hipGetLastError();
 }
 

@@ -322,10 +322,10 @@ hipError_t launch_ffn_stream(const FfnArgs& a, int phase, hipStream_t s, bool se
     sp = 2;
   }
   if (a.wt != kWtPlain) {
-    // (launch_mx_stream has the routed groups of an MXFP4 layer)
-    if (a.wt == kWtMx) ;
-    else if (phase == 1) stream_kernel<1, true><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
-    else stream_kernel<2, true><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
+    // (an MXFP4 layer's routed groups: launch_mx_stream)
+    if (a.wt == kWtFp8 && phase == 1)
+      stream_kernel<1, true><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
+    else if (a.wt == kWtFp8) stream_kernel<2, true><<<grid, blk, 0, s>>>(a, kPlanStart, kPlanRoutedBlocks, sp, r);
     if (a.Is > 0) {
       if (phase == 1 && split)
         stream_kernel<1, false, true><<<grid, blk, 0, s>>>(a, kPlanRoutedBlocks, kPlanBlocks, sp, r);
