@@ -315,7 +315,8 @@ constexpr int kMxTileRows = 16;
 
 // The FFN of an MXFP4 layer: its routed groups have kernels of their own, and the
 // bf16 shared expert, which needs none of their results, is a chain of launches
-// beside theirs (4096 tokens with a shared expert of 640: 681 -> 651 us).
+// beside theirs where the products bound them (4096 tokens with a shared expert of
+// 640: 681 -> 651 us).
 moe_status run_ffn_mx(const moe_problem* p, FfnArgs& a, int phases, int32_t* plan, hipStream_t s, bool fork_ok) {
   const bool force_gemm = p->flags & MOE_FLAG_FORCE_GEMM, force_stream = p->flags & MOE_FLAG_FORCE_STREAM;
   const bool few = p->T <= moe::kStreamMaxRows;  // every group is one m-block
@@ -330,7 +331,7 @@ moe_status run_ffn_mx(const moe_problem* p, FfnArgs& a, int phases, int32_t* pla
     moe::ffn_bind_plan(a, plan);
   }
   const bool sh_stream = force_stream || (!force_gemm && p->T <= stream_rows);
-  Aux* x = fork_ok && a.Is > 0 && !self_plan ? aux_stream() : nullptr;
+  Aux* x = fork_ok && a.Is > 0 && tiles_only ? aux_stream() : nullptr;
   std::unique_lock<std::mutex> lk;
   if (x) {
     lk = std::unique_lock<std::mutex>(x->mu);

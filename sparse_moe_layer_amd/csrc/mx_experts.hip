@@ -50,6 +50,7 @@ int cu_count() {
 // (one token, a dense 8192 x 2048: 22.2 us with 4, 17.5 with 2).
 constexpr int kLogSW = 3, SW = 1 << kLogSW;  // waves per workgroup, one workgroup per compute unit
 using SF = fragdot::Form<kWtMx, kStreamBM, 2>;
+static_assert(kMaxExperts <= 1024, "packed list entries");
 
 template <int PHASE, int SB>
 __device__ __forceinline__ void mx_stream_items(const FfnArgs& f, int self_plan, int nblocks, const Divisor& slabs,
@@ -69,8 +70,8 @@ __device__ __forceinline__ void mx_stream_items(const FfnArgs& f, int self_plan,
     slabs.divide(item, sb, slab);
     int base, nrows;
     if (self_plan) {
-      const int g = glist[sb];
-      base = f.offsets[g];
+      const int g = glist[sb] & 1023, r0 = (glist[sb] >> 10) * kStreamBM;
+      base = f.offsets[g] + r0;
       nrows = f.offsets[g + 1] - base;
     } else {
       base = f.sb_base[sb] + f.sb_row0[sb];
@@ -109,8 +110,8 @@ __device__ __forceinline__ void mx_stream_items(const FfnArgs& f, int self_plan,
           int sb, slab, g;
           slabs.divide(item, sb, slab);
           if (self_plan) {
-            g = uniform(glist[sb]);
-            j.base = uniform(f.offsets[g]);
+            g = uniform(glist[sb] & 1023);
+            j.base = uniform(f.offsets[g] + (glist[sb] >> 10) * kStreamBM);
             j.rows = uniform(f.offsets[g + 1]) - j.base;
           } else {
             g = uniform(f.sb_group[sb]);
@@ -175,7 +176,8 @@ __global__ __launch_bounds__(SW * 64, 2) void mx_stream_kernel(FfnArgs f, int se
                                                                Divisor narrow) {
   __shared__ __attribute__((aligned(16))) char act[SW][SF::LDS];
   __shared__ f32x4 part[SW][4][64];
-  __shared__ int glist[kMaxExperts];  // self_plan: the touched groups, ascending
+  // self_plan: the m-blocks, group | block << 10, ascending (with distinct ids a group has one)
+  __shared__ int glist[kMaxExperts + kStreamMaxRows * 64 / kStreamBM];
   __shared__ int wtot[SW];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   int nblocks;
@@ -183,16 +185,21 @@ __global__ __launch_bounds__(SW * 64, 2) void mx_stream_kernel(FfnArgs f, int se
     nblocks = 0;
     for (int g0 = 0; g0 < f.E; g0 += SW * 64) {
       const int g = g0 + tid;
-      const bool t = g < f.E && f.offsets[g + 1] > f.offsets[g];
-      const uint64_t bal = __ballot(t);
-      if (lane == 0) wtot[wave] = __popcll(bal);
+      const int n = g < f.E ? (f.offsets[g + 1] - f.offsets[g] + kStreamBM - 1) / kStreamBM : 0;
+      int upto = n;  // inclusive scan over the wave
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(upto, o, 64);
+        if (lane >= o) upto += u;
+      }
+      if (lane == 63) wtot[wave] = upto;
       __syncthreads();
-      int off = nblocks;
+      int off = nblocks + upto - n;
       for (int w = 0; w < SW; ++w) {
         if (w < wave) off += wtot[w];
         nblocks += wtot[w];
       }
-      if (t) glist[off + __popcll(bal & ((1ull << lane) - 1ull))] = g;
+      for (int i = 0; i < n; ++i) glist[off + i] = g | i << 10;
       __syncthreads();
     }
     nblocks = uniform(nblocks);
@@ -225,7 +232,6 @@ constexpr int TW = 4;          // waves
 constexpr int TK = 128;        // K per step
 constexpr int TN = 256;        // weight rows per tile
 constexpr int TBUF = kGemmBM * TK * 2;
-constexpr int kAhead = 3;      // activation fragments read ahead of their use
 constexpr int kScaleSteps = 3;  // steps whose scale bytes lie in LDS: 12 bytes and up to 3 before them
 constexpr uint32_t kOut = 0xFFFFFFF0u;  // an offset past any buffer: reads as zeros
 
@@ -240,6 +246,7 @@ template <int NBLK, class Fetch>
 __device__ __forceinline__ void mx_step(f32x4 (&acc)[NBLK][4], const char* buf, const u32x4 (&w)[4],
                                         const float (&sc)[4], const uint32_t (&aswz)[4], Fetch fetch) {
   constexpr int NF = 4 * NBLK;  // activation fragments of the step, in order of use
+  constexpr int kAhead = NBLK < 8 ? 3 : 2;  // read so many ahead of their use (8 blocks: what the registers allow)
   auto decode = [&](int s, bf16x8 (&bf)[4]) {
 #pragma unroll
     for (int b = 0; b < 4; ++b) bf[b] = fragdot::frag(mx8_to_bf16x8(w[b][s], sc[b]));
@@ -338,16 +345,16 @@ __device__ __forceinline__ void mx_tile(const FfnArgs& f, const MxTile& t, char*
   };
   auto load_codes = [&](int kt) {  // of steps kt and kt + 1: 128 bytes of 8 rows a load
     const uint32_t k = (uint32_t)kt * TK;
-    const uint32_t at = (int)k + (lane & 7) * 32 < K ? wrow + k / 2 : kOut;
+    const bool in = (int)k + (lane & 7) * 32 < K;
 #pragma unroll
     for (int b = 0; b < 4; ++b)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const uint32_t row = ((PHASE == 1 ? b & 1 : b) * 16 + 8 * j) * block;
+        const uint32_t at = in ? wrow + ((PHASE == 1 ? b & 1 : b) * 16 + 8 * j) * block + k / 2 : kOut;
         const __amdgpu_buffer_rsrc_t r = wres[PHASE == 1 ? b >> 1 : 0];
         (j ? wb : wa)[b] =
-            __builtin_bit_cast(u32x4, t.once ? __builtin_amdgcn_raw_buffer_load_b128(r, at, row, fragdot::kNt)
-                                             : __builtin_amdgcn_raw_buffer_load_b128(r, at, row, 0));
+            __builtin_bit_cast(u32x4, t.once ? __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, fragdot::kNt)
+                                             : __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
       }
   };
   auto load = [&](int kt, char* buf) {
