@@ -220,20 +220,30 @@ def audit_records(stats: torch.Tensor) -> list:
 def _mx_shape(values, codes, scales, where: str):
     """(rows, K, row stride) of a matrix of values [.., K] (the last dimension contiguous, the ones before it one
     run of rows) with packed codes [.., K/2] and scales [.., K/32]."""
-    K = values.shape[-1]
-    lead = tuple(values.shape[:-1])
-    if tuple(codes.shape) != (*lead, K // 2) or tuple(scales.shape) != (*lead, K // 32) or K % 32 or K < 32:
+    shape = values.shape
+    K = shape[-1]
+    lead = shape[:-1]
+    if codes.shape != (*lead, K // 2) or scales.shape != (*lead, K // 32) or K % 32 or K < 32:
         raise ValueError(f"{where}: codes must be [.., K/2] and scales [.., K/32] for values [.., K], K a multiple of 32")
     if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
         raise ValueError(f"{where}: codes and scales are uint8 tensors")
-    if not (values.device == codes.device == scales.device):
+    if values.get_device() != codes.get_device() or values.get_device() != scales.get_device():
         raise ValueError(f"{where}: tensors on different devices")
     rows = codes.numel() // (K // 2)
     if values.is_contiguous():
-        return rows, K, K
-    if values.dim() != 2 or values.stride(1) != 1 or values.stride(0) < K:
+        stride = K
+    elif values.dim() != 2 or values.stride(1) != 1 or values.stride(0) < K:
         raise ValueError(f"{where}: values must be contiguous, or 2-D with contiguous rows")
-    return rows, K, values.stride(0)
+    else:
+        stride = values.stride(0)
+    _on_current_device(values, where)
+    return rows, K, stride
+
+
+def _on_current_device(t, where: str):
+    """The entry points launch on the current device's stream, so their tensors lie there."""
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{where}: tensors must be on the current CUDA device")
 
 
 def moe_mx_quantize(w, codes, scales, stream=None):
