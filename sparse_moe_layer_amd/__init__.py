@@ -34,8 +34,14 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it (2.8 -> 0.4 us of a call), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 

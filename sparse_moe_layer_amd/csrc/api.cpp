@@ -319,11 +319,23 @@ constexpr int kMxTileRows = 16;
 // 640: 681 -> 651 us).
 moe_status run_ffn_mx(const moe_problem* p, FfnArgs& a, int phases, int32_t* plan, hipStream_t s, bool fork_ok) {
   const bool force_gemm = p->flags & MOE_FLAG_FORCE_GEMM, force_stream = p->flags & MOE_FLAG_FORCE_STREAM;
-  const bool few = p->T <= moe::kStreamMaxRows;  // every group is one m-block
-  const bool tiles_only = force_gemm || (!force_stream && !few && p->T * p->k >= kMxTileRows * p->E);
-  const int stream_rows = tiles_only ? 0 : moe::kStreamMaxRows;
-  const bool any_gemm = tiles_only || (!force_stream && !few), any_stream = !tiles_only;
-  const bool self_plan = !any_gemm && few;
+  // A batch of up to 32 tokens streams every group, as m-blocks that the kernels list
+  // themselves, where a shared expert of more than 16 rows does not need
+  // the plan: a plan kernel and two launches without tiles less (24 tokens over 512
+  // experts 124 -> 113 us).
+  const bool few = p->T <= moe::kMxFewTokens;
+  // So do the few groups of a larger batch whose m-tiles would leave most compute
+  // units idle: an m-tile's time is its K steps', however few they are, where the
+  // streaming kernel splits K (a dense 8192 x 2048, streamed and as tiles: 64 tokens
+  // 46 and 115 us, 128 tokens 73 and 165, 256 tokens 128 and 172).
+  const int64_t R = p->T * p->k;
+  const bool few_tiles = a.Is == 0 && R <= 256 * p->E &&
+                         (R / moe::kGemmBM + (p->E < R ? p->E : R)) * ((p->I + 127) / 128) < 64;
+  const bool all_stream = !force_gemm && (force_stream || few || few_tiles);
+  const bool tiles_only = force_gemm || (!all_stream && R >= kMxTileRows * p->E);
+  const int stream_rows = tiles_only ? 0 : all_stream ? (int)R : moe::kStreamMaxRows;
+  const bool any_gemm = !all_stream, any_stream = !tiles_only;
+  const bool self_plan = !any_gemm && few && (a.Is == 0 || p->T <= moe::kStreamMaxRows);
   if (!self_plan) {
     if (moe::launch_ffn_plan(a.offsets, a.sorted, a.T, a.E, a.k, a.Is > 0 ? 1 : 0, p->flags, moe::kGemmBM,
                              stream_rows, plan, s) != hipSuccess)

@@ -137,6 +137,8 @@ struct SmallRoute {
 // (route, phase 1 with bf16 weights and T <= kSmallBatch) from the ids.
 hipError_t launch_ffn_stream(const FfnArgs& a, int phase, hipStream_t s, bool self_plan = false,
                              const SmallRoute* route = nullptr);
+// MXFP4 batches of at most this many tokens stream every group.
+constexpr int kMxFewTokens = 32;
 // The routed groups of an MXFP4 layer (the launchers above have its shared expert
 // alone): the m-tiles [0, plan[kPlanRoutedTiles]) and the m-blocks [0,
 // plan[kPlanRoutedBlocks]).

@@ -176,8 +176,7 @@ __global__ __launch_bounds__(SW * 64, 2) void mx_stream_kernel(FfnArgs f, int se
                                                                Divisor narrow) {
   __shared__ __attribute__((aligned(16))) char act[SW][SF::LDS];
   __shared__ f32x4 part[SW][4][64];
-  // self_plan: the m-blocks, group | block << 10, ascending (with distinct ids a group has one)
-  __shared__ int glist[kMaxExperts + kStreamMaxRows * 64 / kStreamBM];
+  __shared__ int glist[kMaxExperts + kMxFewTokens * 64 / kStreamBM];  // self_plan: m-blocks, group | block << 10
   __shared__ int wtot[SW];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   int nblocks;

@@ -76,7 +76,7 @@ def test_group_sizes_around_every_block(H, I, flag):
     Ffn(sum(sizes), H, len(sizes), 1, I, ids_of(sizes), seed=H, flags=FLAGS[flag]).check()
 
 
-@pytest.mark.parametrize("T", [1, 2, 7, 16, 17, 40])
+@pytest.mark.parametrize("T", [1, 2, 7, 16, 17, 32, 33, 40, 130, 300])
 def test_one_dense_expert(T):
     Ffn(T, 1024, 1, 1, 512, torch.zeros((T, 1)), seed=T).check()
 
@@ -203,3 +203,25 @@ def test_layer_with_a_shared_expert_beside_the_tiles():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out.view(torch.int16), ref.view(torch.int16)), f"replay {i}"
+
+
+def test_repeated_ids_beside_a_shared_expert():
+    """24 tokens whose groups hold up to 72 rows: the routed rows are the same bits as without the shared expert."""
+    T, H, E, k, I, Is = 24, 160, 5, 4, 96, 72
+    ids = torch.zeros((T, k))
+    ids[:, -1] = torch.arange(T) % 5
+    f = Ffn(T, H, E, k, I, ids, seed=7)
+    ref, srt, off = f.run()
+    g = torch.Generator().manual_seed(8)
+    sh = [(torch.randn(s, generator=g) * 0.05).bfloat16().cuda() for s in ((Is, H), (Is, H), (H, Is))]
+    (cg, sg), (cu, su), (cd, sd) = (f.m[n] for n in ("gate", "up", "down"))
+    P = lib.problem(T, H, E, k, I, Is, "bf16", "mxfp4", 32)
+    W = lib.weights(None, cg, cu, cd, sg, su, sd, *sh)
+    y = torch.full((T * k, H), float("nan"), dtype=torch.bfloat16, device="cuda")
+    ysh = torch.full((T, H), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lib.moe_expert_ffn(P, W, f.x, off, srt, y, ysh, lib.workspace(P))
+    torch.cuda.synchronize()
+    assert torch.equal(y.view(torch.int16), ref.view(torch.int16))
+    x, m = f.x.double().cpu().numpy(), [t.double().cpu().numpy() for t in sh]
+    want, dy = expert_bounds.expert(x, *m)
+    assert (np.abs(ysh.double().cpu().numpy() - want) <= expert_bounds.rounded(want, dy)).all()
