@@ -533,10 +533,10 @@ __global__ __launch_bounds__(FW * 64, 2) void few_experts_kernel(FfnArgs f, FewA
   };
 
   // ---- down and combine: up to 16 output columns over all groups ----
-  // units of 128 K values: the shared expert's (bf16, weighed by their size), then the groups'
+  // units of 128 K values: the groups', then the shared expert's (bf16, weighed by their size)
   constexpr int kWeigh = WT == kWtMx ? 4 : WT == kWtFp8 ? 2 : 1;  // a bf16 unit in units of this type
   const int ud = a.down_units.d, u_sh = a.shared_units;
-  const int u_all = u_sh * kWeigh + ng * ud;
+  const int u_r = ng * ud, u_all = u_r + u_sh * kWeigh;
   const int lo = (u_all * wave) >> kLogFW, hi = (u_all * (wave + 1)) >> kLogFW;
   for (int c0 = (int)blockIdx.x * cols; c0 < f.H; c0 += grid * cols) {
     const int ncol = f.H - c0 < cols ? f.H - c0 : cols;
@@ -552,8 +552,27 @@ __global__ __launch_bounds__(FW * 64, 2) void few_experts_kernel(FfnArgs f, FewA
       j.wrows[0] = ncol < 8 ? ncol : 8;
       j.wrows[1] = ncol < 8 ? 0 : ncol - 8;
     };
-    int u = lo > u_sh * kWeigh ? lo - u_sh * kWeigh : 0;
-    const int r_hi = hi - u_sh * kWeigh;
+    // the shared expert's part first: it waits for no h of this kernel, and wave 0,
+    // which watches the counter, has none of it
+    const int s_lo = lo > u_r ? (lo - u_r) / kWeigh : 0, s_hi = hi > u_r ? (hi - u_r) / kWeigh : 0;
+    bool todo = s_lo < s_hi;
+    fragdot::run<kWtPlain, 1, 0>(  // (h_sh is the first kernel's)
+        f.h_sh, (uint32_t)T * (uint32_t)f.Is * 2u, f.Is, lane, act[wave], BaseRows{},
+        [&](auto& j) {
+          if (!todo) return false;
+          todo = false;
+          j.w[0] = static_cast<const char*>(f.shd) + (int64_t)c0 * f.Is * 2;
+          j.w[1] = j.w[0] + 16 * (int64_t)f.Is;
+          rows_of(j);
+          j.rows = T;
+          j.ar = m < T ? m : 0;
+          j.k0 = s_lo * kUnitK;
+          j.kend = s_hi * kUnitK < f.Is ? s_hi * kUnitK : f.Is;
+          return true;
+        },
+        [&](int, const f32x4 (&acc)[1]) { add(true, (1u << T) - 1u, 0, acc[0]); }, NoGate{});
+    int u = lo;
+    const int r_hi = hi < u_r ? hi : u_r;
     fragdot::run<WT, 1, fragdot::kSc1>(
         f.h, (uint32_t)R * (uint32_t)f.I * 2u, f.I, lane, act[wave], BaseRows{},
         [&](auto& j) {
@@ -588,23 +607,6 @@ __global__ __launch_bounds__(FW * 64, 2) void few_experts_kernel(FfnArgs f, FewA
         },
         [&](int i, const f32x4 (&acc)[1]) { add(false, uniform(r.list[i]) >> 11, (int)uniform(r.base[i]), acc[0]); },
         gate);
-    const int s_lo = lo / kWeigh, s_hi = hi < u_sh * kWeigh ? hi / kWeigh : u_sh;
-    bool todo = s_lo < s_hi;
-    fragdot::run<kWtPlain, 1, 0>(  // (h_sh is the first kernel's)
-        f.h_sh, (uint32_t)T * (uint32_t)f.Is * 2u, f.Is, lane, act[wave], BaseRows{},
-        [&](auto& j) {
-          if (!todo) return false;
-          todo = false;
-          j.w[0] = static_cast<const char*>(f.shd) + (int64_t)c0 * f.Is * 2;
-          j.w[1] = j.w[0] + 16 * (int64_t)f.Is;
-          rows_of(j);
-          j.rows = T;
-          j.ar = m < T ? m : 0;
-          j.k0 = s_lo * kUnitK;
-          j.kend = s_hi * kUnitK < f.Is ? s_hi * kUnitK : f.Is;
-          return true;
-        },
-        [&](int, const f32x4 (&acc)[1]) { add(true, (1u << T) - 1u, 0, acc[0]); }, NoGate{});
     part[wave][0][lane] = sum;
     __syncthreads();
     if (wave == 0) {
