@@ -145,7 +145,8 @@ typedef struct {
  *             bits: [E][I, H/2] bytes ([E][H, I/2] for w_down), strides still
  *             counted in values (multiples of 32); s_gate/s_up [E, I, H/32]
  *             and s_down [E, H, I/32] are E8M0 bytes: value = code * 2^(s - 127),
- *             s = 255 is NaN.  moe_mx_quantize writes both.
+ *             s = 255 is NaN.  moe_mx_quantize writes both.  (The tile flags
+ *             change nothing: MXFP4 groups have 128-row tiles of their own.)
  *   sh_gate, sh_up [I_shared, H], sh_down [H, I_shared], sh_gate_w [1, H]:
  *             shared expert and its gate projection, act dtype; NULL iff
  *             I_shared == 0.                                                 */

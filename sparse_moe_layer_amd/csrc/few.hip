@@ -29,6 +29,14 @@
 // output is stored or rounded, and no sum depends on timing.  A wave asks for
 // its first down weights before it waits for h, so the memory stays busy
 // across the dependency.
+//
+// Measured (2560 x 640, 512 experts, 10 a token): one token 35.6 us with bf16
+// experts (111 MB, 17.7 us at the rate of a read probe), 30.4 with MXFP4 (39 MB,
+// 6.2); 16 tokens fp8 148 us (692 MB, 110).  One token is bound by the steps'
+// latency, in us of the MXFP4 call: router and the gap after it 6.5, top-k 4.4, list and
+// first loads 2.3, gate/up 7.4, the counters 3.9, down 5.7.  Sixteen waves of 128
+// registers instead of 8 of 256 spilled in the MXFP4 loop (43.9 us); two batches of
+// down weights in flight were slower (31.8: the compiler waits for both).
 #include "common.hpp"
 #include "frag_dot.hpp"
 #include "kernels.hpp"
