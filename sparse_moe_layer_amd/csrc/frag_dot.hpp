@@ -166,6 +166,19 @@ __device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, i
       kb = job.k0;
     }
     const bool issued = have;
+    auto offsets = [&] {  // of a new job's activation rows
+#pragma unroll
+      for (int i = 0; i < F::NL; ++i)
+        if (i * F::RPL < job.rows) {
+          const int r = i * F::RPL + lane / LPR;
+          const int at = r < job.rows ? r : 0;
+          aoff[i] = r < job.rows ? (uint32_t)row_of(job, at) * (uint32_t)K * 2u + 16u * (uint32_t)(lane % LPR)
+                                 : kNone;  // (some place or none: its results are not used)
+        }
+    };
+    // Before the weights where a row's index may come from memory: its wait is for
+    // every load before it.
+    if (AROWS && have && fresh) offsets();
     int n_rows = 0, n_ar = 0, n_kb = 0, n_tag = 0;
     bool n_last = false;
     if (have) {
@@ -208,17 +221,7 @@ __device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, i
       }
       if (first) gate();
       first = false;
-      if (fresh) {
-#pragma unroll
-        for (int i = 0; i < F::NL; ++i)
-          if (i * F::RPL < job.rows) {
-            const int r = i * F::RPL + lane / LPR;
-            const int at = r < job.rows ? r : 0;
-            aoff[i] = r < job.rows ? (uint32_t)row_of(job, at) * (uint32_t)K * 2u +
-                                         16u * (uint32_t)(lane % LPR)
-                                   : kNone;  // (some place or none: its results are not used)
-          }
-      }
+      if (!AROWS && fresh) offsets();
 #pragma unroll
       for (int i = 0; i < F::NL; ++i)
         if (i * F::RPL < job.rows)
@@ -262,6 +265,7 @@ __device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, i
       } else {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+          if (U == 2 && u > 0 && c_kb + 4 * G * u >= K) break;  // (nothing behind the rows' ends)
           float f[NB];
 #pragma unroll
           for (int b = 0; b < NB; ++b) f[b] = e8m0(sv[b][u]);

@@ -45,17 +45,19 @@ int cu_count() {
 // blocks in LDS in K order.
 //   4 blocks use each activation fragment four times, which a batch of 24 tokens
 // needs (512 experts, 2560 x 640: 120.5 us; 2 blocks and 256-byte runs, whose K
-// step of 512 also fits a K of 640 badly, 128.4).  One block is for the few items
+// step of 512 also fits a K of 640 badly, 128.4; both with a plan kernel before).  One block is for the few items
 // of a small group list, where 4 leave compute units idle even with K split 8 ways
-// (one token, a dense 8192 x 2048: 22.2 us with 4, 17.5 with 2).
+// (one token, a dense 8192 x 2048: 22.2 us with 4, 17.4 with one).
+//   Bound by the loads: without the products the 24 tokens take 110 of 119 us in the
+// two kernels.
 constexpr int kLogSW = 3, SW = 1 << kLogSW;  // waves per workgroup, one workgroup per compute unit
 using SF = fragdot::Form<kWtMx, kStreamBM, 2>;
 static_assert(kMaxExperts <= 1024, "packed list entries");
 
 template <int PHASE, int SB>
 __device__ __forceinline__ void mx_stream_items(const FfnArgs& f, int self_plan, int nblocks, const Divisor& slabs,
-                                                const int* glist, char* act, f32x4 (*part)[4][64], int lane,
-                                                int wave) {
+                                                const int* glist, const uint8_t* tokens, char* act,
+                                                f32x4 (*part)[4][64], int lane, int wave) {
   constexpr int COLS = (PHASE == 1 ? 8 : 16) * SB;  // output columns of an item
   const int K = PHASE == 1 ? f.H : f.I, N = PHASE == 1 ? f.I : f.H;
   const int grid = (int)gridDim.x, waves = grid * SW;
@@ -102,8 +104,7 @@ __device__ __forceinline__ void mx_stream_items(const FfnArgs& f, int self_plan,
         PHASE == 1 ? f.x : f.h, (uint32_t)(PHASE == 1 ? f.T : f.T * f.k) * (uint32_t)K * 2u, K, lane, act,
         [&](const auto& j, int r) {
           if (PHASE != 1) return j.base + r;
-          int tok = self_plan ? f.sorted[j.base + r] / f.k : f.sb_tok[j.base + r];
-          return (unsigned)tok < (unsigned)f.T ? tok : f.T - 1;  // also clamps a negative index
+          return self_plan ? (int)tokens[j.base + r] : f.sb_tok[j.base + r];
         },
         [&](auto& j) {
           if (!todo) return false;
@@ -166,7 +167,7 @@ __device__ __forceinline__ void mx_stream_items(const FfnArgs& f, int self_plan,
         finish(first, v);
       }
       __syncthreads();
-      if (first >= total) item += step;  // (not taken in this round)
+      if (first >= total) item += step;  // (it had none this time)
     }
   }
 }
@@ -177,10 +178,16 @@ __global__ __launch_bounds__(SW * 64, 2) void mx_stream_kernel(FfnArgs f, int se
   __shared__ __attribute__((aligned(16))) char act[SW][SF::LDS];
   __shared__ f32x4 part[SW][4][64];
   __shared__ int glist[kMaxExperts + kMxFewTokens * 64 / kStreamBM];  // self_plan: m-blocks, group | block << 10
+  __shared__ uint8_t tokens[kMxFewTokens * 64];  // and the dispatched rows' tokens
   __shared__ int wtot[SW];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   int nblocks;
   if (self_plan) {
+    if (PHASE == 1)
+      for (int i = tid; i < f.T * f.k; i += SW * 64) {
+        const int tok = f.sorted[i] / f.k;
+        tokens[i] = (uint8_t)((unsigned)tok < (unsigned)f.T ? tok : f.T - 1);  // also clamps a negative index
+      }
     nblocks = 0;
     for (int g0 = 0; g0 < f.E; g0 += SW * 64) {
       const int g = g0 + tid;
@@ -207,9 +214,9 @@ __global__ __launch_bounds__(SW * 64, 2) void mx_stream_kernel(FfnArgs f, int se
   }
   // one block an item where items of 4 do not even give every workgroup one
   if (nblocks * wide.d >= (int)gridDim.x)
-    mx_stream_items<PHASE, 4>(f, self_plan, nblocks, wide, glist, act[wave], part, lane, wave);
+    mx_stream_items<PHASE, 4>(f, self_plan, nblocks, wide, glist, tokens, act[wave], part, lane, wave);
   else
-    mx_stream_items<PHASE, 1>(f, self_plan, nblocks, narrow, glist, act[wave], part, lane, wave);
+    mx_stream_items<PHASE, 1>(f, self_plan, nblocks, narrow, glist, tokens, act[wave], part, lane, wave);
 }
 
 // ---- 128-row m-tiles ---------------------------------------------------------
