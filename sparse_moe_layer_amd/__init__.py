@@ -14,7 +14,8 @@ import torch
 
 from ._lib import (LIB, MOE_BF16, MOE_F32, MOE_FLAG_FORCE_GEMM, MOE_FLAG_FORCE_STREAM,  # noqa: F401
                    MOE_FLAG_GEMM_TILE_128, MOE_FLAG_GEMM_TILE_256, MOE_FLAG_PAGE_ROUTING, MOE_FP8_E4M3FN,
-                   MOE_FEW_MAX_TOKENS, MOE_MXFP4, MOE_NOALLOC_SCRATCH_BYTES, MOE_OK, EXPORTS, moe_audit_stats, moe_gr_weights, moe_problem,
+                   MOE_FEW_MAX_TOKENS, MOE_MXFP4, MOE_NOALLOC_SCRATCH_BYTES, MOE_OK, EXPORTS, moe_audit_stats,
+                   moe_gr_weights, moe_problem,
                    moe_weights)
 
 _DT = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8": MOE_FP8_E4M3FN, "mxfp4": MOE_MXFP4}
@@ -230,7 +231,8 @@ def _mx_shape(values, codes, scales, where: str):
     K = shape[-1]
     lead = shape[:-1]
     if codes.shape != (*lead, K // 2) or scales.shape != (*lead, K // 32) or K % 32 or K < 32:
-        raise ValueError(f"{where}: codes must be [.., K/2] and scales [.., K/32] for values [.., K], K a multiple of 32")
+        raise ValueError(f"{where}: codes must be [.., K/2] and scales [.., K/32] for values [.., K], K a multiple "
+                         "of 32")
     if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
         raise ValueError(f"{where}: codes and scales are uint8 tensors")
     if values.get_device() != codes.get_device() or values.get_device() != scales.get_device():
@@ -289,7 +291,8 @@ def layer_forward(x, k: int, w_router, w_gate, w_up, w_down, s_gate=None, s_up=N
 
     Shapes come from the tensors: x [T, H] (bf16 or fp32), w_router [E, H], w_gate / w_up [E, I, H],
     w_down [E, H, I] (bf16, fp32, or uint8 e4m3fn codes with fp32 128 x 128 block scales s_*; or
-    MXFP4: uint8 codes [E, I, H/2], [E, H, I/2] with uint8 scales s_*, as mx_quantize makes them), and the optional shared expert sh_gate / sh_up [I_s, H], sh_down [H, I_s], sh_gate_w [1, H].
+    MXFP4: uint8 codes [E, I, H/2], [E, H, I/2] with uint8 scales s_*, as mx_quantize makes them), and
+    the optional shared expert sh_gate / sh_up [I_s, H], sh_down [H, I_s], sh_gate_w [1, H].
     Outputs and the workspace are allocated on x's device; every computation runs in the library.
     """
     T, H = x.shape

@@ -360,7 +360,7 @@ __global__ __launch_bounds__(FW * 64, 2) void few_experts_kernel(FfnArgs f, FewA
     if (((chunks - 1) >> l_own) % kFewDone == i) n -= (chunks << lper) - total;
     return n;
   };
-  const int counters = (chunks + (1 << l_own) - 1) >> l_own < kFewDone ? (chunks + (1 << l_own) - 1) >> l_own : kFewDone;
+  const int owners = (chunks + (1 << l_own) - 1) >> l_own, counters = owners < kFewDone ? owners : kFewDone;
   int32_t* const last = a.counters + kFewDone * kFewCounterStride;
   auto count = [&](int i, int n) {  // n finished slabs of counter i (one lane)
     const int got = n + __hip_atomic_fetch_add(a.counters + i * kFewCounterStride, n, __ATOMIC_RELAXED,

@@ -274,7 +274,8 @@ __device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, i
             const bf16x8 x = act(4 * G * u + 8 * j);
 #pragma unroll
             for (int b = 0; b < NB; ++b)
-              acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, frag(mx8_to_bf16x8(wv[b][u][j], f[b])), acc[b], 0, 0, 0);
+              acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, frag(mx8_to_bf16x8(wv[b][u][j], f[b])), acc[b], 0,
+                                                               0, 0);
           }
         }
       }

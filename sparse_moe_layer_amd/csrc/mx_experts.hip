@@ -521,9 +521,11 @@ __global__ __launch_bounds__(TW * 64, 2) void mx_tiles_kernel(FfnArgs f, Divisor
 }  // namespace
 
 hipError_t launch_mx_stream(const FfnArgs& a, int phase, hipStream_t s, bool self_plan) {
-  const int grid = cu_count();
-  if (phase == 1) mx_stream_kernel<1><<<grid, SW * 64, 0, s>>>(a, self_plan ? 1 : 0, Divisor((a.I + 31) / 32), Divisor((a.I + 7) / 8));
-  else mx_stream_kernel<2><<<grid, SW * 64, 0, s>>>(a, self_plan ? 1 : 0, Divisor((a.H + 63) / 64), Divisor((a.H + 15) / 16));
+  const int grid = cu_count(), sp = self_plan ? 1 : 0;
+  if (phase == 1)
+    mx_stream_kernel<1><<<grid, SW * 64, 0, s>>>(a, sp, Divisor((a.I + 31) / 32), Divisor((a.I + 7) / 8));
+  else
+    mx_stream_kernel<2><<<grid, SW * 64, 0, s>>>(a, sp, Divisor((a.H + 63) / 64), Divisor((a.H + 15) / 16));
   return hipGetLastError();
 }
 
