@@ -272,10 +272,11 @@ moe_status moe_layer_forward_noalloc(const moe_problem* p, const moe_weights* w,
  * bf16 activations with any routed weight type; T > MOE_FEW_MAX_TOKENS or
  * fp32 layers return MOE_ERR_UNSUPPORTED.
  *   Routing as moe_route (MOE_FLAG_PAGE_ROUTING included; the other flags name
- *   kernels that this call does not use and change nothing).  The hidden h is
- *   rounded to bf16 as everywhere; the experts' outputs y are not: each token's
- *   sum over its experts and the shared one stays fp32 until out is rounded,
- *   so out may differ from moe_layer_forward's in its last bits.  Results are
+ *   kernels that this call does not use and change nothing).  The routed hidden
+ *   h is rounded to bf16 as everywhere; the shared expert's keeps 16 significant
+ *   bits (two bf16), and the experts' outputs are not rounded: each token's sum
+ *   over its experts and the shared one stays fp32 until out is rounded, so out
+ *   may differ from moe_layer_forward's in its last bits.  Results are
  *   deterministic run to run.
  * ws: moe_few_workspace_bytes(p) bytes, 256-byte aligned (0 if p is invalid or
  * unsupported); concurrent calls need distinct workspaces.  topk_ids and

@@ -463,7 +463,7 @@ FewWs few_layout(const moe_problem* p, void* base) {
   L.logits = reinterpret_cast<float*>(take((size_t)p->T * (p->E + 1) * 4));
   L.counters = reinterpret_cast<int32_t*>(take(moe::few_counter_ints(p->T, p->k, p->I) * 4));
   L.h = take((size_t)p->T * p->k * p->I * 2);
-  L.h_sh = take((size_t)p->T * p->I_shared * 2);
+  L.h_sh = take((size_t)p->T * p->I_shared * 4);  // two bf16 a value
   L.total = o;
   return L;
 }

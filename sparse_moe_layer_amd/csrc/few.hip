@@ -30,9 +30,9 @@
 // its first down weights before it waits for h, so the memory stays busy
 // across the dependency.
 //
-// Measured (2560 x 640, 512 experts, 10 a token): one token 35.6 us with bf16
-// experts (111 MB, 17.7 us at the rate of a read probe), 30.4 with MXFP4 (39 MB,
-// 6.2); 16 tokens fp8 148 us (692 MB, 110).  One token is bound by the steps'
+// Measured (2560 x 640, 512 experts, 10 a token): one token 36.0 us with bf16
+// experts (111 MB, 17.7 us at the rate of a read probe), 30.2 with MXFP4 (39 MB,
+// 6.2); 16 tokens fp8 150 us (692 MB, 110).  One token is bound by the steps'
 // latency, in us of the MXFP4 call: router and the gap after it 6.5, top-k 4.4, list and
 // first loads 2.3, gate/up 7.4, the counters 3.9, down 5.7.  Sixteen waves of 128
 // registers instead of 8 of 256 spilled in the MXFP4 loop (43.9 us); two batches of
@@ -54,6 +54,20 @@ constexpr int kLogFW = 3, FW = 1 << kLogFW;  // of the experts kernel, one workg
 constexpr int kSlab = 16;                    // hidden columns per slab: a block of gate rows and one of up rows
 constexpr int kFewRows = kSmallBatch * 64;  // (token, expert) pairs at most
 static_assert(kSmallBatch == 16 && kMaxExperts < 2048, "a fragment row per token; packed list entries");
+
+// A hidden value of the shared expert as two bf16, its rounding and what that
+// left, together 16 bits of significand.  The shared expert outweighs the routed ones
+// (a gate of about 1/2 against weights of about 1 / k), so with its h rounded to
+// one bf16 the error of out against 64 bits is up to 1.56 times that of rounding
+// out alone.  The routed experts' h is one bf16, as in the other calls: in
+// two parts it took 159.5 against 150.5 us (16 tokens fp8) and 226 against 207 (4
+// tokens of the 2.4T shape).  An infinity or NaN has no second part.
+__device__ __forceinline__ uint32_t split(float v) {
+  const bf16 hi = f2bf(v);
+  const float rest = v - bf2f(hi);
+  const bf16 lo = f2bf(fabsf(bf2f(hi)) < __builtin_inff() ? rest : 0.f);
+  return (uint32_t)__builtin_bit_cast(uint16_t, hi) | (uint32_t)__builtin_bit_cast(uint16_t, lo) << 16;
+}
 
 // Workgroups [0, nr): 16 router rows each; workgroup nr (shared expert only):
 // its gate's logit; the rest: 8 of its hidden columns each (8 gate, 8 up rows).
@@ -121,7 +135,12 @@ __global__ __launch_bounds__(RW * 64) void few_router_kernel(const bf16* __restr
         if (tok < T && m < cols) logits[(int64_t)tok * N + col] = t[i];
       } else {
         const float up = __shfl_xor(t[i], 8, 64);  // the up row of lane m is lane m + 8's
-        if (tok < T && m < cols) h_sh[(int64_t)tok * Is + c0 + m] = f2bf(silu(t[i]) * up);
+        if (tok < T && m < cols) {
+          const uint32_t h = split(silu(t[i]) * up);
+          bf16* at = h_sh + (int64_t)(2 * tok) * Is + c0 + m;
+          at[0] = __builtin_bit_cast(bf16, (uint16_t)h);
+          at[Is] = __builtin_bit_cast(bf16, (uint16_t)(h >> 16));
+        }
       }
     }
   }
@@ -250,7 +269,7 @@ template <int WT>
 __global__ __launch_bounds__(FW * 64, 2) void few_experts_kernel(FfnArgs f, FewArgs a) {
   using F = fragdot::Form<WT>;
   // per wave: the logits' keys and candidates, later activations; picks and expert tables; the waves' blocks
-  __shared__ __attribute__((aligned(16))) char act[FW][fragdot::kLds];
+  __shared__ __attribute__((aligned(16))) char act[FW][fragdot::Form<kWtPlain, 2 * kSmallBatch>::LDS];
   __shared__ __attribute__((aligned(16))) uint64_t cand[FW][64];
   __shared__ int ids[kFewRows];
   __shared__ float wts[kFewRows];
@@ -564,16 +583,16 @@ __global__ __launch_bounds__(FW * 64, 2) void few_experts_kernel(FfnArgs f, FewA
     // which watches the counter, has none of it
     const int s_lo = lo > u_r ? (lo - u_r) / kWeigh : 0, s_hi = hi > u_r ? (hi - u_r) / kWeigh : 0;
     bool todo = s_lo < s_hi;
-    fragdot::run<kWtPlain, 1, 0>(  // (h_sh is the first kernel's)
-        f.h_sh, (uint32_t)T * (uint32_t)f.Is * 2u, f.Is, lane, act[wave], BaseRows{},
+    fragdot::run<kWtPlain, 1, 0, 2 * kSmallBatch, 4, true>(  // (h_sh is the first kernel's)
+        f.h_sh, (uint32_t)T * (uint32_t)f.Is * 4u, f.Is, lane, act[wave], BaseRows{},
         [&](auto& j) {
           if (!todo) return false;
           todo = false;
           j.w[0] = static_cast<const char*>(f.shd) + (int64_t)c0 * f.Is * 2;
           j.w[1] = j.w[0] + 16 * (int64_t)f.Is;
           rows_of(j);
-          j.rows = T;
-          j.ar = m < T ? m : 0;
+          j.rows = 2 * T;
+          j.ar = m < T ? 2 * m : 0;
           j.k0 = s_lo * kUnitK;
           j.kend = s_hi * kUnitK < f.Is ? s_hi * kUnitK : f.Is;
           return true;

@@ -101,7 +101,9 @@ struct Job {
 // a job's row r < rows.  k0 is a multiple of 128, K of 128 (fp8), 32 (MXFP4) or 8.
 // lds: the wave's Form::LDS bytes.  gate(): called once if there is a job, after
 // the first weights have been asked for and before any activation is.
-template <int WT, int NB, int AUXA, int AROWS = 0, int U_ = 4, class Rows, class Next, class After, class Gate>
+// PAIR: a product's activation row is the sum of the rows ar and ar + 1 (a value in two
+// bf16 parts).
+template <int WT, int NB, int AUXA, int AROWS = 0, int U_ = 4, bool PAIR = false, class Rows, class Next, class After, class Gate>
 __device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, int lane, char* lds, Rows row_of,
                                     Next next, After after, Gate gate) {
   using F = Form<WT, AROWS, U_>;
@@ -176,9 +178,9 @@ __device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, i
                                  : kNone;  // (some place or none: its results are not used)
         }
     };
-    // Before the weights where a row's index may come from memory: its wait is for
-    // every load before it.
-    if (AROWS && have && fresh) offsets();
+    // Before the weights where a row's index may come from memory (the callers with
+    // half runs): its wait is for every load before it.
+    if (U == 2 && have && fresh) offsets();
     int n_rows = 0, n_ar = 0, n_kb = 0, n_tag = 0;
     bool n_last = false;
     if (have) {
@@ -221,7 +223,7 @@ __device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, i
       }
       if (first) gate();
       first = false;
-      if (!AROWS && fresh) offsets();
+      if (U != 2 && fresh) offsets();
 #pragma unroll
       for (int i = 0; i < F::NL; ++i)
         if (i * F::RPL < job.rows)
@@ -234,15 +236,18 @@ __device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, i
     }
     if (pending) {
       const char* const arow = lds + 2 * (c_ar * F::KB + G * q);
-      auto act = [&](int k) { return frag(*reinterpret_cast<const u32x4*>(arow + 2 * k)); };
+      constexpr int NP = PAIR ? 2 : 1;
+      auto act = [&](int k, int p) { return frag(*reinterpret_cast<const u32x4*>(arow + 2 * (k + p * F::KB))); };
       if constexpr (WT == kWtPlain) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const bf16x8 x = act(4 * G * u);
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
-            acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, frag(wv[b][u]), acc[b], 0, 0, 0);
-        }
+          for (int p = 0; p < NP; ++p) {
+            const bf16x8 x = act(4 * G * u, p);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+              acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, frag(wv[b][u]), acc[b], 0, 0, 0);
+          }
       } else if constexpr (WT == kWtFp8) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -253,11 +258,17 @@ __device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, i
           for (int u = 2 * h; u < 2 * h + 2; ++u)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const bf16x8 x = act(4 * G * u + 8 * j);
+              bf16x8 w[NB];
 #pragma unroll
               for (int b = 0; b < NB; ++b)
-                part[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    x, frag(fp8x8_to_bf16x8_exact(u32x2{wv[b][u][2 * j], wv[b][u][2 * j + 1]})), part[b], 0, 0, 0);
+                w[b] = frag(fp8x8_to_bf16x8_exact(u32x2{wv[b][u][2 * j], wv[b][u][2 * j + 1]}));
+#pragma unroll
+              for (int p = 0; p < NP; ++p) {
+                const bf16x8 x = act(4 * G * u + 8 * j, p);
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                  part[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w[b], part[b], 0, 0, 0);
+              }
             }
 #pragma unroll
           for (int b = 0; b < NB; ++b) acc[b] += __uint_as_float(sv[b][h]) * part[b];
@@ -271,11 +282,15 @@ __device__ __forceinline__ void run(const void* abase, uint32_t abytes, int K, i
           for (int b = 0; b < NB; ++b) f[b] = e8m0(sv[b][u]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const bf16x8 x = act(4 * G * u + 8 * j);
+            bf16x8 w[NB];
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
-              acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, frag(mx8_to_bf16x8(wv[b][u][j], f[b])), acc[b], 0,
-                                                               0, 0);
+            for (int b = 0; b < NB; ++b) w[b] = frag(mx8_to_bf16x8(wv[b][u][j], f[b]));
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+              const bf16x8 x = act(4 * G * u + 8 * j, p);
+#pragma unroll
+              for (int b = 0; b < NB; ++b) acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w[b], acc[b], 0, 0, 0);
+            }
           }
         }
       }
