@@ -380,15 +380,15 @@ moe_status run_ffn(const moe_problem* p, FfnArgs& a, int phases, void* plan_ws, 
   // tiles.  (As ragged 256-row tiles they measured slower: the 2.4T fp8
   // layer 4.26 against 3.75 ms per step.)
   const int stream_rows = moe::kStreamMaxRows;
-  // A group holds at most T rows, so with T <= stream_rows no group can
-  // reach the GEMM path unless it is forced; with the GEMM path forced no
-  // group streams.  Launches that cannot have work are skipped.
+  // With T <= stream_rows every group streams unless the GEMM path is forced:
+  // it holds at most T rows, or some 16-row blocks where ids repeat an expert
+  // within a token.  With the GEMM path forced no group streams.  Launches
+  // that cannot have work are skipped.
   const bool any_gemm = (p->flags & MOE_FLAG_FORCE_GEMM) ||
                         (!(p->flags & MOE_FLAG_FORCE_STREAM) && p->T > stream_rows);
   const bool any_stream = !(p->flags & MOE_FLAG_FORCE_GEMM);
-  // Every group streaming as one m-block (T <= kStreamMaxRows): the
-  // streaming kernels list the groups themselves, with no plan kernel ahead
-  // of them in the chain.
+  // Every group streaming (T <= kStreamMaxRows): the streaming kernels list
+  // the groups themselves, with no plan kernel ahead of them in the chain.
   const bool self_plan = !any_gemm && p->T <= moe::kStreamMaxRows;
   if (!self_plan) {
     if (moe::launch_ffn_plan(a.offsets, a.sorted, a.T, a.E, a.k, a.Is > 0 ? 1 : 0, p->flags,

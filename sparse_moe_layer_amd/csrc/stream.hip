@@ -71,10 +71,15 @@ __device__ __forceinline__ void stream_dot(const bf16* a_row, const bf16* const*
 // flight per wave.  Down items are 32 output columns (2 blocks).
 //
 // SELF_PLAN (batches of at most kStreamMaxRows tokens, where every group
-// streams as one m-block): no plan kernel runs before the launch; each
-// workgroup lists the touched groups itself, in ascending order with the
-// shared expert last, from the expert offsets (the plan's stream list for
-// such a batch); the list bounds name plan positions as without it.
+// streams): no plan kernel runs before the launch; each workgroup lists the
+// touched groups itself, in ascending order with the shared expert last, from
+// the expert offsets (the plan's stream list for such a batch); the list
+// bounds name plan positions as without it.  A group of more than 16 rows,
+// which ids that repeat an expert within a token make, is one item per slab all
+// the same: the wave takes the item once per 16 rows (`begun`), for nothing in
+// the usual batch.  (Each block listed as an item of its own: 16-token fp8
+// layer 191 -> 196.7 us; a loop around the item's code, whose addresses the
+// compiler keeps: 16-token bf16 layer 249 -> 254.)
 // self_plan == 2 (route.ids non-null; bf16 gate/up split items, T <=
 // kSmallBatch): the dispatch is not in memory yet.  Each workgroup ORs every
 // assignment a = t*k + j into its expert's token mask in LDS (bit t; a
@@ -188,7 +193,8 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(FfnArgs f, int li
   const int n_slabs = (wide + cols_per_item - 1) / cols_per_item;
   const int total = (sb_end - sb_begin) * n_slabs;
 
-  for (int item = gw; item < total; item += nw) {
+  int begun = 0;  // rows of the item's group that are done
+  for (int item = gw; item < total;) {
     const int sb = sb_begin + item / n_slabs;
     const int slab = item % n_slabs;
     int g, r0, base, nrows;
@@ -212,9 +218,9 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(FfnArgs f, int li
       }
     } else if (self_plan) {
       g = glist[sb];
-      r0 = 0;
+      r0 = begun;
       base = g < f.E ? f.offsets[g] : 0;
-      nrows = g < f.E ? f.offsets[g + 1] - base : f.T;
+      nrows = g < f.E ? f.offsets[g + 1] - base - begun : f.T;
     } else {
       g = f.sb_group[sb];
       r0 = f.sb_row0[sb];
@@ -223,6 +229,9 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(FfnArgs f, int li
     }
     stream_item<PHASE, FP8, SPLIT>(f, g, r0, base, nrows, self_plan ? nullptr : f.sb_tok + sb * kStreamBM, slab,
                                    lane, stage + wave * STAGE_BYTES, mk);
+    const bool more = nrows > kStreamBM;  // the same item's next 16 rows
+    begun = more ? begun + kStreamBM : 0;
+    item += more ? 0 : nw;
   }
 }
 

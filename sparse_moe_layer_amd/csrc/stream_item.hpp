@@ -284,7 +284,7 @@ constexpr int item_lds_bytes() {
 }
 
 // One item: slab `slab` of group g (routed expert g < E, or the shared
-// expert g == E) for rows r0 .. r0+nrows-1 of the group (nrows <= 16), whose
+// expert g == E) for rows r0 .. r0+min(nrows, 16)-1 of the group, whose
 // dispatched rows start at `base`.  The gathered token of each row: tok_row
 // (the plan's list); else, when tok_mask is nonzero, the group's tokens as a
 // bit mask (row m is the token of its m-th set bit: a batch of at most 32
