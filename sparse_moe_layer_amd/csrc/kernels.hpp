@@ -190,6 +190,7 @@ struct FewArgs {
   void* out;             // [T, H] bf16
   int32_t* counters;     // few_counter_ints words, zeroed by the first kernel
   // sizes, filled in by the launcher
+  int owners;          // workgroups that the gate/up chunks are dealt to: the grid's, or more than it has (tests)
   Divisor slabs;       // slabs of 16 hidden columns per group
   Divisor down_units;  // units of K of a group's down rows
   int units, shared_units, cols;  // units of the gate/up K and of the shared expert's; output columns at a time
