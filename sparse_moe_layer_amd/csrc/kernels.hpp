@@ -55,7 +55,7 @@ struct FfnArgs {
   const float* scg; const float* scu; const float* scd;  // fp8: block scales; MXFP4: where the E8M0 bytes are
   const void* shg; const void* shu; const void* shd;     // shared expert (bf16) or null
   void* h;                    // [R, I]  bf16 hidden of routed rows
-  void* h_sh;                 // [T, Is] bf16 hidden of the shared expert
+  void* h_sh;                 // [T, Is] bf16 hidden of the shared expert (launch_layer_few: [2 T, Is])
   void* y;                    // [R, H]  bf16
   void* y_sh;                 // [T, H]  bf16 (may be null when Is == 0)
   // device-built work lists
@@ -198,7 +198,8 @@ struct FewArgs {
 constexpr int kFewDone = 16, kFewCounterStride = 64;  // done counters, ints apart
 constexpr int kFewMaxGrid = 512;
 size_t few_counter_ints(int64_t T, int64_t k, int64_t I);
-// f.h [T*k, I] and f.h_sh [T, Is] are scratch; f.offsets and f.sorted are not used.
+// f.h [T*k, I] and f.h_sh [2 T, Is] bf16 are scratch (of h_sh rows 2 t and 2 t + 1
+// are the two parts of token t's values); f.offsets and f.sorted are not used.
 hipError_t launch_layer_few(const FfnArgs& f, const void* w_router, const void* w_sg, FewArgs a, hipStream_t s);
 
 // MXFP4 weights: rows of K values (bf16, or fp32 with f32) to codes and E8M0
