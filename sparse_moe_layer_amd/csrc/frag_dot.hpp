@@ -98,7 +98,8 @@ struct Job {
 // Runs the jobs that next(Job&) gives until it returns false, and after(tag,
 // acc) with each one's products A [16 rows] x W [16 rows]^T, NB blocks.  abase: the
 // activation rows, K values each, `abytes` in all; row_of(job, r) is the index of
-// a job's row r < rows.  k0 is a multiple of 128, K of 128 (fp8), 32 (MXFP4) or 8.
+// a job's row r < rows.  k0 is a multiple of 128 (fp8, MXFP4: whole scale blocks and
+// aligned scale bytes) or of 8 (bf16), K of 128 (fp8), 32 (MXFP4) or 8.
 // lds: the wave's Form::LDS bytes.  gate(): called once if there is a job, after
 // the first weights have been asked for and before any activation is.
 // PAIR: a product's activation row is the sum of the rows ar and ar + 1 (a value in two

@@ -1,5 +1,7 @@
-// Top-k of one wave's keys (gfx950, 64 lanes): the ranking that every routing
-// kernel of the layer uses.
+// Order of logits (descending, equal ones by ascending expert id) as unsigned
+// keys, which every routing kernel uses, and the top-k of one wave's keys
+// (gfx950, 64 lanes).  The few-token layer picks from the same keys in a way of
+// its own (few.hip), which ranks only the logits that can be among the k.
 #pragma once
 #include "common.hpp"
 
