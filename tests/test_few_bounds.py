@@ -2,6 +2,7 @@
 import numpy as np
 import pytest
 
+import expert_bounds as eb
 import few_bounds as fb
 
 
@@ -39,3 +40,27 @@ def test_rms_limit(H, I):
     assert ratio(wd=twice) > 4 * fb.RMS  # a K unit counted twice
     assert ratio(x=x[::-1]) > 4 * fb.RMS  # another token's rows
     assert ratio(column=np.arange(512, 528)) > 4 * fb.RMS  # a block of output columns
+
+
+@pytest.mark.parametrize("T,H,Is", [(16, 64, 64), (4, 320, 640), (1, 32, 16)])
+def test_second_part_of_the_shared_hidden_values(T, H, Is):
+    x, sg, wg, wu, wd = fb.cancelling_shared(T, H, Is, Is)
+    ref, dy = fb.shared_parts(x, sg, wg, wu, wd)
+    s = 1 / (1 + np.exp(-(x @ sg)))[:, None]
+    h = fb.swiglu(x, wg, wu)
+    hi = fb.bf16(h)
+    lo = fb.bf16(h - hi)
+
+    def over(h):
+        return np.max(np.abs(fb.bf16(s * (h @ wd.T)) - ref) / eb.rounded(ref, dy), axis=1)
+
+    assert (over(hi + lo) <= 1).all()
+    assert (over(hi) > 2).all()  # not there
+    assert (over(hi - lo) > 2).all()  # subtracted
+    if T > 1:
+        assert (over(hi + np.roll(lo, 1, axis=0)) > 2).all()  # another token's
+    if Is > 128:  # missing in one K unit of 128
+        for k in range(0, Is, 128):
+            part = lo.copy()
+            part[:, k:k + 128] = 0
+            assert (over(hi + part) > 2).all()
