@@ -26,7 +26,8 @@
  *  - `stream` is a hipStream_t (NULL = the default stream).  All work is
  *    enqueued asynchronously and ordered after earlier work on it; no
  *    host<->device copy happens inside a call.  When an expert FFN call has
- *    both 256-row GEMM tiles and streamed groups, the streamed groups run on
+ *    both 256-row GEMM tiles and streamed groups, the streamed groups, and
+ *    when all routed MXFP4 groups run as tiles, the shared expert, run on
  *    a second stream of the library's (one per device, default priority,
  *    created with two events on the first such call): forked from `stream`
  *    after the call's first kernel and joined back into it before the call's
@@ -271,6 +272,13 @@ moe_status moe_layer_forward_noalloc(const moe_problem* p, const moe_weights* w,
  * router, then top-k, expert products, shared expert and combine in one grid.
  * bf16 activations with any routed weight type; T > MOE_FEW_MAX_TOKENS or
  * fp32 layers return MOE_ERR_UNSUPPORTED.
+ *   It saves launches, not bytes, so it is for batches that are short next to
+ * them.  Measured against moe_layer_forward (512 experts, 10 a token): fp8 and
+ * MXFP4 weights, faster at every T, by 3 % (2.4T shape, 16 tokens fp8) to more
+ * than half; bf16 weights, faster up to 0.74 GB of touched weights (Flash-Next,
+ * 8 tokens), up to 12 % slower from 1 GB on (12 tokens).  MXFP4 experts that
+ * many tokens share are read once per 4 of them: 16 tokens of 2 picks over 8
+ * experts of 4096 x 1024 take 40.6 us against 32.2.
  *   Routing as moe_route (MOE_FLAG_PAGE_ROUTING included; the other flags name
  *   kernels that this call does not use and change nothing).  The routed hidden
  *   h is rounded to bf16 as everywhere; the shared expert's keeps 16 significant

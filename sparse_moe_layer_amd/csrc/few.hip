@@ -30,9 +30,11 @@
 // its first down weights before it waits for h, so the memory stays busy
 // across the dependency.
 //
-// Measured (2560 x 640, 512 experts, 10 a token): one token 36.0 us with bf16
-// experts (111 MB, 17.7 us at the rate of a read probe), 30.2 with MXFP4 (39 MB,
-// 6.2); 16 tokens fp8 150 us (692 MB, 110).  One token is bound by the steps'
+// Measured (2560 x 640, 512 experts, 10 a token): one token 36 us with bf16
+// experts (111 MB, 17.7 us at the rate of a read probe), 30 with MXFP4 (39 MB,
+// 6.2); 16 tokens fp8 150 us (692 MB, 110).  bf16 at 12 tokens and more (1 GB)
+// streams slower than the kernels of moe_layer_forward: 16 tokens 257 us against
+// 249, the 2.4T shape 213 to 2202 against 202 to 2084 (1 to 16 tokens).  One token is bound by the steps'
 // latency, in us of the MXFP4 call: router and the gap after it 6.5, top-k 4.4, list and
 // first loads 2.3, gate/up 7.4, the counters 3.9, down 5.7.  Sixteen waves of 128
 // registers instead of 8 of 256 spilled in the MXFP4 loop (43.9 us); two batches of
@@ -300,7 +302,9 @@ __global__ __launch_bounds__(FW * 64, 2) void few_experts_kernel(FfnArgs f, FewA
   // Wave 0 groups the assignments i = t * k + j by expert: an expert's token
   // mask, its first assignment (its place in the list is by first use), its
   // first row of h and its groups.  (An expert with more than ROWS tokens is
-  // read once per group; with 512 experts and 16 tokens 2 in 1000 have that many.)
+  // read once per group: with MXFP4, 512 experts and 16 tokens 2 in 1000 have more
+  // than 4, but of 8 experts that 2 of are picked about half do: 40.6 us against
+  // 32.2 of the layer call's kernels, 4096 x 1024.)
   // LDS operations of one wave are executed in order.
   if (wave == 0) {
     for (int i = lane; i < R; i += 64) {
