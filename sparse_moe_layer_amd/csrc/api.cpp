@@ -311,6 +311,9 @@ constexpr int kStreamReserve = 32;
 // 16 rows run as m-tiles as well: two launches less, and their reading overlaps
 // the large groups' products (4096 tokens over 512 experts 649 against 675 us, a
 // skewed 1023 over 64 1251 against 1257; 24 tokens over 512 experts 198 against 128).
+// Just below the bound tiles alone would be up to 12 % faster (512 experts of 2560 x
+// 640, 819 tokens 420 against 370 us, 512 tokens 389 against 359; 256 tokens 320
+// against 355 the other way).
 constexpr int kMxTileRows = 16;
 
 // The FFN of an MXFP4 layer: its routed groups have kernels of their own, and the
@@ -327,7 +330,11 @@ moe_status run_ffn_mx(const moe_problem* p, FfnArgs& a, int phases, int32_t* pla
   // So do the few groups of a larger batch whose m-tiles would leave most compute
   // units idle: an m-tile's time is its K steps', however few they are, where the
   // streaming kernel splits K (a dense 8192 x 2048, streamed and as tiles: 64 tokens
-  // 46 and 115 us, 128 tokens 73 and 165, 256 tokens 128 and 172).
+  // 46 and 115 us, 128 tokens 73 and 165, 256 tokens 128 and 172).  The bounds are
+  // from that expert: with short rows tiles win earlier (4 experts of 1024 x 512,
+  // 128 tokens 31 and 36 us, 512 tokens 55 and 49, 1024 tokens 85 and 49), and
+  // 8 experts of 4096 x 1024 are past the bound where streaming wins (64 tokens
+  // of 2 picks 38 and 65).
   const int64_t R = p->T * p->k;
   const bool few_tiles = a.Is == 0 && R <= 256 * p->E &&
                          (R / moe::kGemmBM + (p->E < R ? p->E : R)) * ((p->I + 127) / 128) < 64;
