@@ -34,11 +34,12 @@
 // experts (111 MB, 17.7 us at the rate of a read probe), 30 with MXFP4 (39 MB,
 // 6.2); 16 tokens fp8 150 us (692 MB, 110).  bf16 at 12 tokens and more (1 GB)
 // streams slower than the kernels of moe_layer_forward: 16 tokens 257 us against
-// 249, the 2.4T shape 213 to 2202 against 202 to 2084 (1 to 16 tokens).  One token is bound by the steps'
-// latency, in us of the MXFP4 call: router and the gap after it 6.5, top-k 4.4, list and
-// first loads 2.3, gate/up 7.4, the counters 3.9, down 5.7.  Sixteen waves of 128
-// registers instead of 8 of 256 spilled in the MXFP4 loop (43.9 us); two batches of
-// down weights in flight were slower (31.8: the compiler waits for both).
+// 249, the 2.4T shape 213 to 2202 against 202 to 2084 (1 to 16 tokens).
+// One token is bound by the steps' latency, in us of the MXFP4 call: router and the
+// gap after it 6.5, top-k 4.7, list and first loads 2.6, gate/up 7.4, the counters
+// 3.9, down 5.3.  Sixteen waves of 128 registers instead of 8 of 256 spilled in the
+// MXFP4 loop (43.9 us); two batches of down weights in flight were slower (31.8: the
+// compiler waits for both).
 #include <atomic>
 
 #include "common.hpp"
@@ -303,8 +304,8 @@ __global__ __launch_bounds__(FW * 64, 2) void few_experts_kernel(FfnArgs f, FewA
   // mask, its first assignment (its place in the list is by first use), its
   // first row of h and its groups.  (An expert with more than ROWS tokens is
   // read once per group: with MXFP4, 512 experts and 16 tokens 2 in 1000 have more
-  // than 4, but of 8 experts that 2 of are picked about half do: 40.6 us against
-  // 32.2 of the layer call's kernels, 4096 x 1024.)
+  // than 4; with 8 experts and 2 picks a third do: 40.6 us against 32.2 of the
+  // layer call's kernels, 4096 x 1024.)
   // LDS operations of one wave are executed in order.
   if (wave == 0) {
     for (int i = lane; i < R; i += 64) {
