@@ -411,6 +411,156 @@ moe_status moe_mx_dequantize(const void* codes, const void* scales, int64_t rows
                              int64_t row_stride, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * A block around experts of the caller's own, and its gradients: the rows of
+ * the assignments to expert order and back (moe_dispatch's positions), the
+ * norms before and after a block with its gate and residual, and products over
+ * groups of rows with bias, activation, factor and residual in the epilogue.
+ * F32 or BF16 tensors throughout (one dtype per call); fp32 accumulation, sums
+ * and statistics, each output rounded once.  An infinity or NaN stays with the
+ * rows it belongs to and the sums over them.  Results are deterministic.
+ * Tensors of act dtype 16-byte aligned, fp32 vectors and int32 arrays 4-byte
+ * aligned (MOE_ERR_ALIGN).  No input may overlap an output, except where a
+ * call says so.
+ * --------------------------------------------------------------------------- */
+
+/* Rows to expert order: xs[assign_pos[t*k+j]] = topk_w[t,j] * x[t], or x[t]
+ * where topk_w is NULL (weights that moe_combine applies).
+ *   x [T,H] act; assign_pos [T,k] as moe_dispatch returns it; xs [T*k, H] act.
+ * The positions in [0, T*k) must differ; an assignment with a position outside
+ * has no row (dropped, or another GPU's), here and in the two calls below, and
+ * rows that no assignment names are left as they were.  Uses T, H, E, k and
+ * act_dtype of p.                                                           */
+moe_status moe_permute(const moe_problem* p, const void* x, const int32_t* assign_pos, const float* topk_w, void* xs,
+                       void* stream);
+
+/* Gradient of moe_permute for the gradient dxs [T*k, H] of xs:
+ *   dx[t] = sum_j topk_w[t,j] * dxs[assign_pos[t*k+j]]   (weight 1 where topk_w is NULL)
+ *   dtopk_w[t,j] = <x[t], dxs[assign_pos[t*k+j]]>        (0 for an assignment without a row)
+ * dx [T,H] act; dtopk_w [T,k] fp32 or NULL (x is read for it alone and may be
+ * NULL without it).  With weights and dtopk_w NULL it is also the way back
+ * from the experts without a shared one.                                   */
+moe_status moe_permute_backward(const moe_problem* p, const void* dxs, const int32_t* assign_pos, const float* topk_w,
+                                const void* x, void* dx, float* dtopk_w, void* stream);
+
+/* Gradient of moe_combine for the gradient dout [T,H] of out, s = shared_logit:
+ *   dy[assign_pos[t*k+j]] = topk_w[t,j] * dout[t]
+ *   dtopk_w[t,j]          = <dout[t], y[assign_pos[t*k+j]]>
+ *   dy_shared[t]          = sigmoid(s[t]) * dout[t]
+ *   dshared_logit[t]      = sigmoid(s[t]) (1 - sigmoid(s[t])) <dout[t], y_shared[t]>
+ * dy [T*k, H] act, may be y itself (in place); dtopk_w [T,k] fp32 or NULL (y is
+ * read for it alone and may be NULL without it); y_shared, shared_logit,
+ * dy_shared ([T,H] act, may be y_shared itself) and dshared_logit ([T] fp32)
+ * all NULL or all given.                                                    */
+moe_status moe_combine_backward(const moe_problem* p, const void* dout, const void* y, const int32_t* assign_pos,
+                                const float* topk_w, const void* y_shared, const float* shared_logit, void* dy,
+                                float* dtopk_w, void* dy_shared, float* dshared_logit, void* stream);
+
+/* Between two blocks of a model with one residual stream: the norm behind a
+ * block, its gate, the residual and the norm before the next block,
+ *   n         = f / rms(f) * g_post            (f itself where g_post is NULL)
+ *   resid_out = resid_scale * resid + gate * n
+ *   x         = resid_out / rms(resid_out) * g_pre,   rms(v) = sqrt(mean v^2 + eps)
+ * (x from the residual before its rounding).
+ * gate, by p->gate: NULL; [T] fp32; [H] dtype; [T,H] dtype.                 */
+typedef enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_TOKEN = 1,   /* one factor per token, fp32                        */
+  MOE_GATE_CHANNEL = 2, /* one per channel                                   */
+  MOE_GATE_FULL = 3     /* one per value                                     */
+} moe_gate;
+
+/* dtype MOE_F32 or MOE_BF16; H a multiple of 4 (F32) or 8 (BF16), at most
+ * MOE_NORM_MAX_H; T*H < 2^31; eps > 0 and resid_scale finite (MOE_ERR_SHAPE). */
+#define MOE_NORM_MAX_H 16384
+typedef struct {
+  int64_t T;          /* tokens                                              */
+  int64_t H;          /* width                                               */
+  int32_t dtype;      /* of f, resid, the gains, x and resid_out             */
+  int32_t gate;       /* moe_gate                                            */
+  float eps;          /* of both norms                                       */
+  float resid_scale;  /* factor of the residual                              */
+} moe_norm_problem;
+
+/* f, resid, resid_out, x [T,H]; g_post, g_pre [H].  f may be NULL (before the
+ * first block: resid_out = resid_scale * resid; g_post and gate then NULL and
+ * p->gate MOE_GATE_NONE).  g_pre and x both NULL: no norm behind.  resid_out may be
+ * NULL where x is given, and may be resid or f itself.                      */
+moe_status moe_block_norm(const moe_norm_problem* p, const void* f, const void* resid, const void* g_post,
+                          const void* gate, const void* g_pre, void* resid_out, void* x, void* stream);
+
+/* Scratch of moe_block_norm_backward: fp32 partial sums over the tokens of the
+ * gains' and the channel gate's gradients.  0 if p is invalid. */
+size_t moe_block_norm_workspace_bytes(const moe_norm_problem* p);
+
+/* Gradients for dresid_out and dx [T,H] of resid_out and x; either may be NULL
+ * (not used further), not both.  f and resid_out as the forward call read and
+ * wrote them (resid_out and g_pre are read for dx alone, NULL without it).
+ *   dresid [T,H] or NULL, may be dresid_out or dx itself; df [T,H], NULL iff f
+ *   is NULL; dg_post, dg_pre [H] fp32, or NULL; dgate: [T] fp32, [H] fp32 or
+ *   [T,H] dtype by p->gate, or NULL.
+ * dg_post needs g_post, dg_pre needs dx, dgate needs a gate (MOE_ERR_NULL).
+ * T == 0 launches nothing, so the sums are not written.  ws: 256-byte aligned,
+ * moe_block_norm_workspace_bytes(p) bytes; concurrent calls need distinct ones. */
+moe_status moe_block_norm_backward(const moe_norm_problem* p, const void* dresid_out, const void* dx, const void* f,
+                                   const void* resid_out, const void* g_post, const void* gate, const void* g_pre,
+                                   void* dresid, void* df, float* dg_post, void* dgate, float* dg_pre, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/* Product over groups of rows.  The rows of group g are [offsets[g],
+ * offsets[g+1]) (moe_dispatch's expert_offsets, or NULL for one group of every
+ * row); for each row r of group g
+ *   z[r] = x[r] W_g^T + bias_g
+ *   y[r] = resid[r] + act(z[r]) * mul[r]
+ * with bias, mul and resid each left out where NULL.  SiLU with mul = the up
+ * projection's output is a SwiGLU expert's hidden.  offsets must not decrease;
+ * values outside [0, rows] are taken as the nearer end.  Rows of no group are
+ * left as they were in every output.                                       */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_SILU = 1,    /* z * sigmoid(z)                                     */
+  MOE_ACT_GELU = 2     /* z * Phi(z), the normal distribution's exact Phi    */
+} moe_activation;
+
+/* dtype MOE_F32 or MOE_BF16; K, N multiples of 4 (F32) or 8 (BF16) in
+ * [1, 2^17], 1 <= groups <= 1024, 0 <= rows < 2^24, N*K < 2^30; w_stride 0
+ * (dense: N*K) or at least N*K and a multiple of 16 bytes (else MOE_ERR_SHAPE,
+ * MOE_ERR_ALIGN).  rows == 0 launches nothing (but see the backward's dw). */
+typedef struct {
+  int64_t rows;       /* rows of x                                           */
+  int64_t K;          /* width of x                                          */
+  int64_t N;          /* width of y                                          */
+  int64_t groups;     /* weight matrices                                     */
+  int64_t w_stride;   /* elements from one matrix to the next                */
+  int32_t dtype;      /* of x, w, bias, mul, resid, y, z                     */
+  int32_t act;        /* moe_activation                                      */
+} moe_linear_problem;
+
+/* x [rows,K]; w [groups][N,K] at w_stride; bias [groups,N]; offsets
+ * [groups+1] int32, NULL only if groups == 1; mul, resid, y [rows,N]; z [rows,N]
+ * receives the activation's argument for the backward call, or NULL.  y may be
+ * mul or resid itself.                                                      */
+moe_status moe_linear(const moe_linear_problem* p, const void* x, const void* w, const void* bias,
+                      const int32_t* offsets, const void* mul, const void* resid, void* y, void* z, void* stream);
+
+/* Scratch of moe_linear_backward: dz [rows,N] and partial sums of dbias.  0 if
+ * p is invalid. */
+size_t moe_linear_workspace_bytes(const moe_linear_problem* p);
+
+/* Gradients for dy [rows,N] of y (resid's gradient is dy itself):
+ *   dz = dy * mul * act'(z),  dmul = dy * act(z)
+ *   dx[r] = dz[r] W_g,  dw_g = sum_r dz[r]^T x[r],  dbias_g = sum_r dz[r]
+ * dx [rows,K], dw [groups][N,K] at w_stride, dmul [rows,N] (may be mul itself),
+ * dbias [groups,N] fp32: each may be NULL.  dw and dbias of a group without rows
+ * are zeros, rows == 0 included; what lies between the matrices of dw
+ * (w_stride > N*K) is left as it was.  z is needed with an activation and for
+ * dmul (MOE_ERR_NULL), w for dx, x for dw, mul for dmul.  BF16: dz is rounded to bf16 before the
+ * two products (dbias sums it unrounded).  ws: 256-byte aligned,
+ * moe_linear_workspace_bytes(p) bytes; concurrent calls need distinct ones. */
+moe_status moe_linear_backward(const moe_linear_problem* p, const void* dy, const void* x, const void* w,
+                               const int32_t* offsets, const void* mul, const void* z, void* dx, void* dw,
+                               float* dbias, void* dmul, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Measurement helper (not a step of the layer): reads `bytes` of device
  * memory at src once, 16 bytes per lane over contiguous runs with eight loads
  * in flight per lane, and writes nothing (sink: a device uint32, written only

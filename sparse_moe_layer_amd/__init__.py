@@ -16,7 +16,9 @@ from ._lib import (LIB, MOE_BF16, MOE_F32, MOE_FLAG_FORCE_GEMM, MOE_FLAG_FORCE_S
                    MOE_FLAG_GEMM_TILE_128, MOE_FLAG_GEMM_TILE_256, MOE_FLAG_PAGE_ROUTING, MOE_FP8_E4M3FN,
                    MOE_FEW_MAX_TOKENS, MOE_MXFP4, MOE_NOALLOC_SCRATCH_BYTES, MOE_OK, EXPORTS, moe_audit_stats,
                    moe_gr_weights, moe_problem,
-                   moe_weights)
+                   moe_weights,
+                   MOE_ACT_GELU, MOE_ACT_NONE, MOE_ACT_SILU, MOE_GATE_CHANNEL, MOE_GATE_FULL, MOE_GATE_NONE,
+                   MOE_GATE_TOKEN, MOE_NORM_MAX_H, moe_linear_problem, moe_norm_problem)
 
 _DT = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8": MOE_FP8_E4M3FN, "mxfp4": MOE_MXFP4}
 
@@ -280,6 +282,171 @@ def mx_quantize(w, stream=None):
     scales = torch.empty((*w.shape[:-1], w.shape[-1] // 32), dtype=torch.uint8, device=w.device)
     moe_mx_quantize(w, codes, scales, stream)
     return codes, scales
+
+
+# ---------------------------------------------------------------------------
+# a block around experts of the caller's own, and its gradients
+# ---------------------------------------------------------------------------
+_GATES = {"none": MOE_GATE_NONE, "token": MOE_GATE_TOKEN, "channel": MOE_GATE_CHANNEL, "full": MOE_GATE_FULL}
+_ACTS = {"none": MOE_ACT_NONE, "silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU}
+_TORCH_DT = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
+
+
+def norm_problem(T, H, dtype="bf16", gate="none", eps=1e-6, resid_scale=1.0) -> moe_norm_problem:
+    return moe_norm_problem(T, H, _DT[dtype], _GATES[gate], eps, resid_scale)
+
+
+def linear_problem(rows, K, N, groups=1, dtype="bf16", act="none", w_stride=0) -> moe_linear_problem:
+    return moe_linear_problem(rows, K, N, groups, w_stride, _DT[dtype], _ACTS[act])
+
+
+class _Args:
+    """Pointers of a call's tensors: contiguous, of the expected number of values and dtype, on the current device
+    (the library launches there), or None."""
+
+    __slots__ = ("where", "dev", "act")
+
+    def __init__(self, where: str, act: int):
+        self.where, self.dev = where, torch.cuda.current_device()
+        self.act = _TORCH_DT.get(act)  # None: the library refuses the dtype
+
+    def __call__(self, t, n: int, dtype=None):
+        if t is None:
+            return None
+        want = dtype or self.act
+        if (t.dtype is not want and want is not None) or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{self.where}: a contiguous tensor of {n} values of {want} is needed, not "
+                             f"{tuple(t.shape)} of {t.dtype}{'' if t.is_contiguous() else ', strided'}")
+        if t.get_device() != self.dev:
+            raise ValueError(f"{self.where}: tensors must be on the current CUDA device")
+        return t.data_ptr()
+
+    def ws(self, t):
+        if t is None:
+            return None, 0
+        n = t.numel() * t.element_size()
+        return self(t, t.numel(), t.dtype), n
+
+    def stream(self, stream):
+        if stream is None:
+            return _raw_stream(self.dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+        if getattr(stream, "device_index", self.dev) != self.dev:
+            raise ValueError(f"{self.where}: the stream must be one of the current CUDA device")
+        return _stream(stream)
+
+
+_I32, _F32 = torch.int32, torch.float32
+
+
+def moe_permute(p, x, assign_pos, topk_w, xs, stream=None):
+    """x [T, H] -> xs [T*k, H]: xs[assign_pos[t*k+j]] = topk_w[t, j] * x[t] (topk_w None: x[t])."""
+    a = _Args("moe_permute", p.act_dtype)
+    n, R = p.T * p.H, p.T * p.k
+    _check(LIB.moe_permute(ctypes.byref(p), a(x, n), a(assign_pos, R, _I32), a(topk_w, R, _F32), a(xs, R * p.H),
+                           a.stream(stream)), a.where)
+
+
+def moe_permute_backward(p, dxs, assign_pos, topk_w, x, dx, dtopk_w, stream=None):
+    """Gradients of moe_permute: dx [T, H], and dtopk_w [T, k] where it is not None (x is read for it alone)."""
+    a = _Args("moe_permute_backward", p.act_dtype)
+    n, R = p.T * p.H, p.T * p.k
+    _check(LIB.moe_permute_backward(ctypes.byref(p), a(dxs, R * p.H), a(assign_pos, R, _I32), a(topk_w, R, _F32),
+                                    a(x, n), a(dx, n), a(dtopk_w, R, _F32), a.stream(stream)), a.where)
+
+
+def moe_combine_backward(p, dout, y, assign_pos, topk_w, y_shared, shared_logit, dy, dtopk_w, dy_shared,
+                         dshared_logit, stream=None):
+    """Gradients of moe_combine: dy [T*k, H], dtopk_w [T, k] (or None), dy_shared [T, H], dshared_logit [T]."""
+    a = _Args("moe_combine_backward", p.act_dtype)
+    n, R = p.T * p.H, p.T * p.k
+    _check(LIB.moe_combine_backward(ctypes.byref(p), a(dout, n), a(y, R * p.H), a(assign_pos, R, _I32),
+                                    a(topk_w, R, _F32), a(y_shared, n), a(shared_logit, p.T, _F32), a(dy, R * p.H),
+                                    a(dtopk_w, R, _F32), a(dy_shared, n), a(dshared_logit, p.T, _F32),
+                                    a.stream(stream)), a.where)
+
+
+def _gate_arg(a, p, t, summed: bool):
+    """A gate ([T] fp32, [H], [T, H]), or its gradient, which is fp32 where it is summed over rows or columns."""
+    if p.gate == MOE_GATE_FULL:
+        return a(t, p.T * p.H)
+    if p.gate == MOE_GATE_CHANNEL:
+        return a(t, p.H, _F32 if summed else None)
+    return a(t, p.T, _F32)
+
+
+def moe_block_norm(p: moe_norm_problem, f, resid, g_post, gate, g_pre, resid_out, x, stream=None):
+    """resid_out = resid_scale * resid + gate * RMSNorm(f) g_post, x = RMSNorm(resid_out) g_pre (None: left out)."""
+    a = _Args("moe_block_norm", p.dtype)
+    n = p.T * p.H
+    _check(LIB.moe_block_norm(ctypes.byref(p), a(f, n), a(resid, n), a(g_post, p.H), _gate_arg(a, p, gate, False),
+                              a(g_pre, p.H), a(resid_out, n), a(x, n), a.stream(stream)), a.where)
+
+
+def moe_block_norm_workspace_bytes(p: moe_norm_problem) -> int:
+    return LIB.moe_block_norm_workspace_bytes(ctypes.byref(p))
+
+
+def norm_workspace(p: moe_norm_problem, device="cuda") -> torch.Tensor:
+    """A device buffer of moe_block_norm_workspace_bytes(p) bytes."""
+    n = moe_block_norm_workspace_bytes(p)
+    if n == 0:
+        raise MoEError(2, "moe_block_norm_workspace_bytes")  # 2: MOE_ERR_SHAPE
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_block_norm_backward(p: moe_norm_problem, dresid_out, dx, f, resid_out, g_post, gate, g_pre, dresid, df,
+                            dg_post, dgate, dg_pre, ws, stream=None):
+    """Gradients of moe_block_norm; dg_post, dg_pre [H] fp32, dgate [T] or [H] fp32 or [T, H]; ws: norm_workspace(p)."""
+    a = _Args("moe_block_norm_backward", p.dtype)
+    n = p.T * p.H
+    _check(LIB.moe_block_norm_backward(ctypes.byref(p), a(dresid_out, n), a(dx, n), a(f, n), a(resid_out, n),
+                                       a(g_post, p.H), _gate_arg(a, p, gate, False), a(g_pre, p.H), a(dresid, n),
+                                       a(df, n), a(dg_post, p.H, _F32), _gate_arg(a, p, dgate, True),
+                                       a(dg_pre, p.H, _F32), *a.ws(ws), a.stream(stream)), a.where)
+
+
+def _weights_arg(a, p, w):
+    """[groups, N, K] contiguous, or at p.w_stride from one contiguous matrix to the next (a slice of a fused
+    [groups, 2 N, K] tensor)."""
+    if w is None or p.w_stride in (0, p.N * p.K):
+        return a(w, p.groups * p.N * p.K)
+    want = (p.groups, p.N, p.K)
+    if tuple(w.shape) != want or (p.groups > 1 and w.stride(0) != p.w_stride) or not w[0].is_contiguous():
+        raise ValueError(f"{a.where}: weights must be {want} with {p.w_stride} values from one matrix to the next")
+    a(w[0], p.N * p.K)
+    return w.data_ptr()
+
+
+def moe_linear(p: moe_linear_problem, x, w, bias, offsets, mul, resid, y, z, stream=None):
+    """y[r] = resid[r] + act(x[r] W_g^T + bias_g) * mul[r] for the rows r of each group g (bias, mul, resid, z may be
+    None; offsets [groups + 1] int32, None for one group); z receives the activation's argument."""
+    a = _Args("moe_linear", p.dtype)
+    n = p.rows * p.N
+    _check(LIB.moe_linear(ctypes.byref(p), a(x, p.rows * p.K), _weights_arg(a, p, w), a(bias, p.groups * p.N),
+                          a(offsets, p.groups + 1, _I32), a(mul, n), a(resid, n), a(y, n), a(z, n),
+                          a.stream(stream)), a.where)
+
+
+def moe_linear_workspace_bytes(p: moe_linear_problem) -> int:
+    return LIB.moe_linear_workspace_bytes(ctypes.byref(p))
+
+
+def linear_workspace(p: moe_linear_problem, device="cuda") -> torch.Tensor:
+    """A device buffer of moe_linear_workspace_bytes(p) bytes."""
+    n = moe_linear_workspace_bytes(p)
+    if n == 0:
+        raise MoEError(2, "moe_linear_workspace_bytes")  # 2: MOE_ERR_SHAPE
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_linear_backward(p: moe_linear_problem, dy, x, w, offsets, mul, z, dx, dw, dbias, dmul, ws, stream=None):
+    """Gradients of moe_linear (each output may be None; dbias [groups, N] fp32); ws: linear_workspace(p)."""
+    a = _Args("moe_linear_backward", p.dtype)
+    n, m = p.rows * p.N, p.rows * p.K
+    _check(LIB.moe_linear_backward(ctypes.byref(p), a(dy, n), a(x, m), _weights_arg(a, p, w),
+                                   a(offsets, p.groups + 1, _I32), a(mul, n), a(z, n), a(dx, m),
+                                   _weights_arg(a, p, dw), a(dbias, p.groups * p.N, _F32), a(dmul, n), *a.ws(ws),
+                                   a.stream(stream)), a.where)
 
 
 _DT_OF_TORCH = {torch.float32: "f32", torch.bfloat16: "bf16", torch.uint8: "fp8"}

@@ -24,13 +24,18 @@ MOE_FLAG_GEMM_TILE_256 = 8
 MOE_FLAG_PAGE_ROUTING = 16
 MOE_NOALLOC_SCRATCH_BYTES = 32 << 20
 MOE_FEW_MAX_TOKENS = 16
+MOE_NORM_MAX_H = 16384
+MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_CHANNEL, MOE_GATE_FULL = range(4)
+MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU = range(3)
 
 EXPORTS = ["moe_abi_version", "moe_status_str", "moe_validate", "moe_workspace_bytes", "moe_route",
            "moe_dispatch", "moe_expert_ffn", "moe_expert_gate_up", "moe_expert_down", "moe_combine",
            "moe_layer_forward", "moe_gr_workspace_bytes", "moe_gr_read", "moe_gr_write", "moe_combine_gr_write",
            "moe_audit_workspace_bytes", "moe_weight_audit", "moe_layer_forward_noalloc",
            "moe_hbm_read_probe", "moe_mfma_pipe_probe", "moe_mx_quantize", "moe_mx_dequantize",
-           "moe_few_workspace_bytes", "moe_layer_forward_few"]
+           "moe_few_workspace_bytes", "moe_layer_forward_few", "moe_permute", "moe_permute_backward",
+           "moe_combine_backward", "moe_block_norm", "moe_block_norm_workspace_bytes", "moe_block_norm_backward",
+           "moe_linear", "moe_linear_workspace_bytes", "moe_linear_backward"]
 
 
 class moe_problem(ctypes.Structure):
@@ -57,6 +62,16 @@ class moe_audit_stats(ctypes.Structure):
                 ("median", ctypes.c_double), ("mad", ctypes.c_double), ("sigma_rob", ctypes.c_double)]
 
 
+class moe_norm_problem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("dtype", ctypes.c_int32), ("gate", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("resid_scale", ctypes.c_float)]
+
+
+class moe_linear_problem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("K", ctypes.c_int64), ("N", ctypes.c_int64), ("groups", ctypes.c_int64),
+                ("w_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python sparse_moe_layer_amd/build.py`")
@@ -64,6 +79,8 @@ def _load():
     P = ctypes.POINTER(moe_problem)
     W = ctypes.POINTER(moe_weights)
     G = ctypes.POINTER(moe_gr_weights)
+    N = ctypes.POINTER(moe_norm_problem)
+    L = ctypes.POINTER(moe_linear_problem)
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
     sig = {
         "moe_abi_version": (i32, []),
@@ -88,6 +105,15 @@ def _load():
         "moe_gr_read": (i32, [P, G, vp, vp, vp, vp, sz, vp]),
         "moe_gr_write": (i32, [P, vp, vp, vp, vp, vp]),
         "moe_combine_gr_write": (i32, [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "moe_permute": (i32, [P] + [vp] * 5),
+        "moe_permute_backward": (i32, [P] + [vp] * 7),
+        "moe_combine_backward": (i32, [P] + [vp] * 11),
+        "moe_block_norm": (i32, [N] + [vp] * 8),
+        "moe_block_norm_workspace_bytes": (sz, [N]),
+        "moe_block_norm_backward": (i32, [N] + [vp] * 13 + [sz, vp]),
+        "moe_linear": (i32, [L] + [vp] * 9),
+        "moe_linear_workspace_bytes": (sz, [L]),
+        "moe_linear_backward": (i32, [L] + [vp] * 11 + [sz, vp]),
         "moe_audit_workspace_bytes": (sz, [ctypes.c_int64]),
         "moe_weight_audit": (i32, [vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, vp, vp, sz,
                                    vp]),

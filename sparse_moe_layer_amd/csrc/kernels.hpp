@@ -209,6 +209,65 @@ hipError_t launch_mx_quantize(const void* w, bool f32, int64_t rows, int64_t K, 
 hipError_t launch_mx_dequantize(const void* codes, const void* scales, int64_t rows, int64_t K, void* w,
                                 int64_t row_stride, hipStream_t s);
 
+// Rows to expert order and the gradients of that and of the combine (w, dw,
+// y_sh .. dsl may be null as in the C ABI).
+hipError_t launch_permute(const void* x, const int32_t* pos, const float* w, void* xs, int T, int H, int k, int f32,
+                          hipStream_t s);
+hipError_t launch_permute_backward(const void* dxs, const int32_t* pos, const float* w, const void* x, void* dx,
+                                   float* dw, int T, int H, int k, int f32, hipStream_t s);
+hipError_t launch_combine_backward(const void* dout, const void* y, const int32_t* pos, const float* w,
+                                   const void* y_sh, const float* sl, void* dy, float* dw, void* dy_sh, float* dsl,
+                                   int T, int H, int k, int f32, hipStream_t s);
+
+// Block norms: pointers as in the C ABI, nch 16-byte chunks a row.
+struct NormArgs {
+  const void *f, *resid, *g_post, *gate, *g_pre;
+  void *resid_out, *x;
+  int nch, gate_kind;
+  float inv_h, eps, scale;
+};
+struct NormBackArgs {
+  const void *dresid_out, *dx, *f, *resid_out, *g_post, *gate, *g_pre;
+  void *dresid, *df;
+  float* dg_post;
+  void* dgate;
+  float* dg_pre;
+  float* partial;  // norm_partial_floats(T, H)
+  int T, nch, gate_kind;
+  float inv_h, eps, scale;
+  int sums;  // set by the launcher
+};
+size_t norm_partial_floats(int64_t T, int64_t H);
+hipError_t launch_norm(const NormArgs& a, int T, bool f32, hipStream_t s);
+hipError_t launch_norm_backward(NormBackArgs a, bool f32, hipStream_t s);
+
+// Products over groups of rows: pointers as in the C ABI.
+struct LinearArgs {
+  const void *x, *w, *bias;
+  const int32_t* offsets;  // null: one group of every row
+  const void *mul, *resid;
+  void *y, *z;
+  int rows, K, N, G;
+  int64_t w_stride;
+  int act;
+};
+hipError_t launch_linear(const LinearArgs& a, bool f32, hipStream_t s);
+struct LinearBackArgs {
+  const void *dy, *x, *w;
+  const int32_t* offsets;
+  const void *mul, *z;
+  void *dx, *dw;
+  float* dbias;
+  void* dmul;
+  void* dz;        // scratch [rows, N]
+  float* partial;  // scratch linear_partial_floats(..)
+  int rows, K, N, G;
+  int64_t w_stride;
+  int act;
+};
+size_t linear_partial_floats(int64_t rows, int64_t N, int64_t G);
+hipError_t launch_linear_backward(const LinearBackArgs& a, bool f32, hipStream_t s);
+
 // Gated residual read / write (bf16).
 // Expert-weight audit (bf16): histograms of the bit patterns per slice and
 // over the tensor, then the exact statistics of each.
