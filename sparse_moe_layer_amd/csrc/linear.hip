@@ -2,82 +2,10 @@
 //   forward  z = x W_g^T + b_g,  y = resid + act(z) mul
 //   backward dz = dy mul act'(z), dmul = dy act(z), db_g = sum dz;  dx = dz W_g;  dW_g = dz^T x
 // The rows of group g are [offsets[g], offsets[g+1]), known to the device only.
-#include "kernels.hpp"
-#include "vec.hpp"
+#include "linear.hpp"
 
 namespace moe {
 namespace {
-
-__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(-0.70710678f * z); }
-
-// act(z), and its derivative in d
-__device__ __forceinline__ float activate(int act, float z) {
-  if (act == MOE_ACT_SILU) return z / (1.f + expf(-z));
-  if (act == MOE_ACT_GELU) return z * normal_cdf(z);
-  return z;
-}
-__device__ __forceinline__ float activate_d(int act, float z, float& d) {
-  if (act == MOE_ACT_SILU) {
-    const float g = 1.f / (1.f + expf(-z));
-    d = g * fmaf(z, 1.f - g, 1.f);
-    return z * g;
-  }
-  if (act == MOE_ACT_GELU) {
-    const float c = normal_cdf(z);
-    d = fmaf(z * 0.39894228f, expf(-0.5f * z * z), c);
-    return z * c;
-  }
-  d = 1.f;
-  return z;
-}
-
-// First and last row of group g; offsets outside [0, rows] and decreasing ones
-// are brought into range, so that no access leaves the tensors.
-__device__ __forceinline__ int2 group_rows(const int32_t* offsets, int g, int rows) {
-  if (!offsets) return {0, rows};
-  const int lo = min(max(offsets[g], 0), rows);
-  return {lo, min(max(offsets[g + 1], lo), rows)};
-}
-
-// The m-tile of `bm` rows that comes `idx`-th when the groups' tiles are counted
-// in order: group, first row, end of the group.  g < 0 past the last tile.
-// Every thread of a 256-thread workgroup calls it; groups <= 1024.
-struct MTile {
-  int g, row, end;
-};
-__device__ __forceinline__ MTile find_tile(const int32_t* offsets, int G, int rows, int bm, int idx) {
-  if (!offsets) return {idx * bm < rows ? 0 : -1, idx * bm, rows};
-  __shared__ int wave_total[4];
-  __shared__ MTile found;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int2 rr[4];
-  int n[4], sum = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int g = tid * 4 + i;
-    rr[i] = g < G ? group_rows(offsets, g, rows) : int2{0, 0};
-    n[i] = (rr[i].y - rr[i].x + bm - 1) / bm;
-    sum += n[i];
-  }
-  int incl = sum;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int v = __shfl_up(incl, o, kWave);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 63) wave_total[wave] = incl;
-  if (tid == 0) found.g = -1;
-  __syncthreads();
-  int first = incl - sum;
-  for (int w = 0; w < wave; ++w) first += wave_total[w];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (idx >= first && idx < first + n[i]) found = {tid * 4 + i, rr[i].x + (idx - first) * bm, rr[i].y};
-    first += n[i];
-  }
-  __syncthreads();
-  return found;
-}
 
 // ---------------------------------------------------------------------------
 // fp32 matrix instructions on 64 x 64 tiles, any dtype
@@ -128,8 +56,9 @@ __global__ __launch_bounds__(256) void linear_simple_kernel(LinearArgs a, const 
     n0 = blockIdx.x * kSB;
     nn = a.K;
   } else {
-    const MTile t = find_tile(a.offsets, a.G, a.rows, kSB, blockIdx.x);
-    if (t.g < 0) return;
+    const TileMap map(a.offsets, a.G, a.rows, kSB);
+    if ((int)blockIdx.x >= map.total) return;
+    const MTile t = map.find(blockIdx.x);
     g = t.g;
     m0 = t.row;
     m1 = t.end;
@@ -254,9 +183,6 @@ __global__ __launch_bounds__(256) void linear_sums_kernel(const float* __restric
   out[i] = v;
 }
 
-// m-tiles of bm rows over all groups, at most
-int max_tiles(int rows, int G, int bm) { return rows / bm + (G < rows ? G : rows); }
-
 // Parts of each group's rows for the sums: about 64 rows each
 int sum_splits(int64_t rows, int64_t G) {
   const int64_t s = rows / G / 64;
@@ -271,9 +197,9 @@ size_t linear_partial_floats(int64_t rows, int64_t N, int64_t G) {
 }
 
 hipError_t launch_linear(const LinearArgs& a, bool f32, hipStream_t s) {
+  if (!f32) return launch_linear_tiles(kLinForward, a, a.x, a.w, a.y, s);
   const dim3 grid(max_tiles(a.rows, a.G, kSB), (a.N + kSB - 1) / kSB);
-  if (f32) linear_simple_kernel<true, 0><<<grid, 256, 0, s>>>(a, a.x, a.w, a.y);
-  else linear_simple_kernel<false, 0><<<grid, 256, 0, s>>>(a, a.x, a.w, a.y);
+  linear_simple_kernel<true, 0><<<grid, 256, 0, s>>>(a, a.x, a.w, a.y);
   return hipGetLastError();
 }
 
@@ -308,15 +234,19 @@ hipError_t launch_linear_backward(const LinearBackArgs& b, bool f32, hipStream_t
   l.N = a.N;
   l.G = a.G;
   l.w_stride = a.w_stride;
+  if (!f32) {
+    hipError_t e = hipSuccess;
+    if (a.dx && a.rows > 0) e = launch_linear_tiles(kLinDx, l, dz, a.w, a.dx, s);
+    if (a.dw && e == hipSuccess) e = launch_linear_tiles(kLinDw, l, dz, a.x, a.dw, s);
+    return e;
+  }
   if (a.dx && a.rows > 0) {
     const dim3 grid(max_tiles(a.rows, a.G, kSB), (a.K + kSB - 1) / kSB);
-    if (f32) linear_simple_kernel<true, 1><<<grid, 256, 0, s>>>(l, dz, a.w, a.dx);
-    else linear_simple_kernel<false, 1><<<grid, 256, 0, s>>>(l, dz, a.w, a.dx);
+    linear_simple_kernel<true, 1><<<grid, 256, 0, s>>>(l, dz, a.w, a.dx);
   }
   if (a.dw) {
     const dim3 grid((a.K + kSB - 1) / kSB, (a.N + kSB - 1) / kSB, a.G);
-    if (f32) linear_simple_kernel<true, 2><<<grid, 256, 0, s>>>(l, dz, a.x, a.dw);
-    else linear_simple_kernel<false, 2><<<grid, 256, 0, s>>>(l, dz, a.x, a.dw);
+    linear_simple_kernel<true, 2><<<grid, 256, 0, s>>>(l, dz, a.x, a.dw);
   }
   return hipGetLastError();
 }

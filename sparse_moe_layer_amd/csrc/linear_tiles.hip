@@ -1,0 +1,350 @@
+// bf16 products over groups of rows on v_mfma_f32_32x32x16_bf16 tiles:
+//   forward  z = x W_g^T     A = x  [r][k],  B = W [n][k]     (contracted along rows of both)
+//   dx       dz W_g          A = dz [r][n],  B = W [n][k]     (B contracted along its columns)
+//   dw       dz^T x          A = dz [r][n],  B = x [r][k]     (both contracted along their columns)
+#include "linear.hpp"
+
+namespace moe {
+namespace {
+
+template <int BM_, int BN_, int WM_, int WN_, int S_, int WG_PER_CU_>
+struct Tile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, BK = 32;
+  static constexpr int NW = WM * WN, NT = 64 * NW;
+  static constexpr int MI = BM / (32 * WM), NJ = BN / (32 * WN);  // 32 x 32 blocks of a wave
+  static constexpr int LA = BM / (16 * NW), LB = BN / (16 * NW);  // 1 KB direct loads a wave and stage
+  static constexpr int L = LA + LB;
+  static constexpr int STAGE = (BM + BN) * BK;  // elements
+  static constexpr int WG_PER_CU = WG_PER_CU_;
+  static_assert(NT == 256, "the search for tiles takes 256 threads");
+  static_assert(WM == 2 && BM == BN, "a stage holds 32 rows of the fp32 tile");
+  static_assert(MI >= 1 && NJ >= 1 && LA >= 1 && LB >= 1 && L * (S - 1) < 64, "tiling");
+  static_assert(S * STAGE * 2 * WG_PER_CU <= 160 * 1024, "LDS");
+  static_assert((BM / 32) % S == 0 && S % WM == 0, "the epilogue's passes");
+};
+
+constexpr int vmcnt_imm(int n) { return 0xF70 | (n & 15) | (((n >> 4) & 3) << 14); }
+constexpr int vmcnt_lgkm0_imm(int n) { return vmcnt_imm(n) & ~0xF00; }
+
+constexpr int kBufferFlags = 0x00020000;  // raw 32-bit buffer access
+constexpr uint32_t kNowhere = 0xFFFFFFF0u;  // past every buffer: the load writes zeros to LDS
+
+__device__ __forceinline__ void block_sync() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// A 16-byte direct load from base + voff + soff to LDS (voff the lane's, soff the
+// wave's); past `records` bytes it writes zeros.
+__device__ __forceinline__ void dma16(const char* base, uint32_t records, uint32_t voff, uint32_t soff, bf16* l) {
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, records, kBufferFlags);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)l, 16, voff, soff, 0, 0);
+}
+
+// One operand's tile of R rows (or, contracted along its columns, R columns) as
+// the direct loads see it.  T: contracted along its columns.
+//  !T: a stage holds [R][32], 64-byte rows, 16-byte chunk c of row r at
+//      c ^ ((r >> 2) & 3): 16 rows' fragment reads of one chunk cover all banks.
+//   T: a stage holds [32][R], the 64-byte block b of contraction row k at
+//      b ^ (k & 3): the transposing reads of four rows cover all banks.
+template <class C, int R, bool T>
+struct Operand {
+  const char* base;    // the tile's first element
+  int64_t bytes;       // from there to the tensor's (the contraction's) end
+  int64_t ld;          // bytes from row to row
+  uint32_t off[R / (16 * C::NW)];
+  int chunk;           // !T: the lane's first k within a stage
+
+  __device__ __forceinline__ Operand(const void* p, int64_t ld_elems, int64_t bytes_, int lane, int wave)
+      : base(static_cast<const char*>(p)), bytes(bytes_), ld(ld_elems * 2) {
+#pragma unroll
+    for (int i = 0; i < R / (16 * C::NW); ++i) {
+      const int q = C::NW * i + wave;  // the 1 KB piece of the stage
+      if constexpr (!T) {
+        const int row = q * 16 + (lane >> 2);
+        chunk = ((lane & 3) ^ ((row >> 2) & 3)) * 8;  // 16 rows a piece: the same for every i
+        off[i] = (uint32_t)(row * ld) + chunk * 2;
+      } else {
+        constexpr int LPR = R / 8;  // lanes a row
+        const int row = q * (64 / LPR) + lane / LPR, pos = lane % LPR;
+        off[i] = (uint32_t)(row * ld) + ((((pos >> 2) ^ (row & 3)) << 2) | (pos & 3)) * 16;
+      }
+    }
+  }
+
+  // The loads of the 32 contraction steps from k0 on; steps past kn give zeros.
+  __device__ __forceinline__ void issue(bf16* st, int k0, int kn, int wave) const {
+    const char* b = base;
+    int64_t left = bytes;
+    if constexpr (T) {
+      b += k0 * ld;
+      left -= k0 * ld;
+    }
+    const uint32_t records = left <= 0 ? 0u : left < (int64_t)kNowhere ? (uint32_t)left : kNowhere;
+    const bool none = !T && k0 + chunk >= kn;
+#pragma unroll
+    for (int i = 0; i < R / (16 * C::NW); ++i)
+      dma16(b, records, none ? kNowhere : off[i], T ? 0 : k0 * 2, st + (C::NW * i + wave) * 512);
+  }
+};
+
+// Within each 16 lanes, lane i gives the address of values 4 (i & 3) .. + 4 of row
+// i >> 2 and gets value i of the four rows.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ s16x4 read_tr(const bf16* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+}
+
+// A lane's fragment reads of one operand: block b (of 32 rows or columns), K
+// sub-step ks of 16.  first: the wave's first block; step: blocks apart.
+template <int R, bool T, int NB, int STEP>
+struct Frags {
+  int o[T ? NB : 2];
+  __device__ __forceinline__ Frags(int first, int lane) {
+    if constexpr (!T) {
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const int row = first * 32 + (lane & 31);
+        o[ks] = row * 32 + (((ks * 2 + (lane >> 5)) ^ ((row >> 2) & 3)) << 3);
+      }
+    } else {
+      const int k = 8 * (lane >> 5) + ((lane & 15) >> 2);
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+        o[i] = k * R + (((first + i * STEP) ^ (k & 3)) << 5) + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+    }
+  }
+  __device__ __forceinline__ void load(const bf16* st, int ks, bf16x8* f) const {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      if constexpr (!T) {
+        f[i] = *reinterpret_cast<const bf16x8*>(st + o[ks] + i * STEP * 32 * 32);
+      } else {
+        const bf16* p = st + o[i] + ks * 16 * R;
+        f[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(read_tr(p), read_tr(p + 4 * R), 0, 1, 2, 3, 4, 5, 6, 7));
+      }
+    }
+  }
+};
+
+template <class C>
+__device__ __forceinline__ void mfma_sub(f32x16 (&acc)[C::MI][C::NJ], const bf16x8* a, const bf16x8* b) {
+#pragma unroll
+  for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+    for (int j = 0; j < C::NJ; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+}
+
+template <int MODE, class C>
+__global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_kernel(LinearArgs a, const bf16* p,
+                                                                                       const bf16* q, bf16* out) {
+  constexpr bool TA = MODE == kLinDw, TB = MODE != kLinForward;
+  // separate arrays: a read of one stage does not wait for loads into another
+  __shared__ __attribute__((aligned(1024))) bf16 s0[C::STAGE];
+  __shared__ __attribute__((aligned(1024))) bf16 s1[C::STAGE];
+  __shared__ __attribute__((aligned(1024))) bf16 s2[C::S > 2 ? C::STAGE : 8];
+  __shared__ __attribute__((aligned(1024))) bf16 s3[C::S > 3 ? C::STAGE : 8];
+  bf16* stg[4];
+  stg[0] = s0, stg[1] = s1, stg[2] = s2, stg[3] = s3;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+
+  // ---- which tile: XCD x (workgroup i runs on XCD i % 8) takes a run of
+  // consecutive tiles, so that its L2 holds what they share ----
+  const int nn = MODE == kLinForward ? a.N : a.K;  // columns of the output
+  const int tn = (nn + C::BN - 1) / C::BN;
+  const TileMap map(MODE == kLinDw ? nullptr : a.offsets, a.G, a.rows, C::BM);
+  const int tm = MODE == kLinDw ? a.G * ((a.N + C::BM - 1) / C::BM) : map.total;
+  const int total = tm * tn;
+  const int bid = blockIdx.x;
+  if (bid >= total) return;
+  const int x = bid & 7, per = total >> 3, rem = total & 7;
+  const int t = x * per + min(x, rem) + (bid >> 3);
+  // runs of kSuper m-tiles by all n-tiles, m first
+  constexpr int kSuper = C::BM == 256 ? 4 : 1;
+  const int sb = t / (kSuper * tn) * kSuper, in = t - sb * tn;
+  const int deep = min(tm - sb, kSuper);
+  const int mt = sb + in % deep, nt = in / deep;
+
+  int g, m0, m1, kn;
+  int64_t r0 = 0;  // first row of the contraction (dw)
+  if constexpr (MODE == kLinDw) {
+    const int tg = (a.N + C::BM - 1) / C::BM;
+    g = mt / tg;
+    m0 = (mt - g * tg) * C::BM;
+    m1 = a.N;
+    const int2 rr = group_rows(a.offsets, g, a.rows);
+    r0 = rr.x;
+    kn = rr.y - rr.x;
+  } else {
+    const MTile m = map.find(mt);
+    g = m.g;
+    m0 = m.row;
+    m1 = m.end;
+    kn = MODE == kLinForward ? a.K : a.N;
+  }
+  const int n0 = nt * C::BN;
+
+  const int64_t K = a.K, N = a.N;
+  const bf16 *pa, *pb;
+  int64_t la, lb, ba, bb;  // row lengths, elements left
+  if constexpr (MODE == kLinForward) {
+    pa = p + m0 * K, la = K, ba = (m1 - m0) * K;
+    pb = q + g * a.w_stride + n0 * K, lb = K, bb = (N - n0) * K;
+  } else if constexpr (MODE == kLinDx) {
+    pa = p + m0 * N, la = N, ba = (m1 - m0) * N;
+    pb = q + g * a.w_stride + n0, lb = K, bb = N * K - n0;
+  } else {
+    pa = p + r0 * N + m0, la = N, ba = kn * N - m0;
+    pb = q + r0 * K + n0, lb = K, bb = kn * K - n0;
+  }
+  const Operand<C, C::BM, TA> oa(pa, la, ba * 2, lane, wave);
+  const Operand<C, C::BN, TB> ob(pb, lb, bb * 2, lane, wave);
+  const Frags<C::BM, TA, C::MI, C::WM> fa(wm, lane);  // M-blocks wm, wm + WM, ..
+  const Frags<C::BN, TB, C::NJ, 1> fb(wn * C::NJ, lane);
+  auto issue = [&](bf16* st, int step) {
+    oa.issue(st, step * C::BK, kn, wave);
+    ob.issue(st + C::BM * C::BK, step * C::BK, kn, wave);
+  };
+
+  f32x16 acc[C::MI][C::NJ];
+#pragma unroll
+  for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+    for (int j = 0; j < C::NJ; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+  bf16x8 ca[C::MI] = {}, cb[C::NJ] = {};  // the stage's second sub-step, multiplied after the next barrier
+
+  const int nk = (kn + C::BK - 1) / C::BK;
+#pragma unroll
+  for (int s = 0; s < C::S - 1; ++s) issue(stg[s], s);
+  auto step = [&](int s, const bf16* st, bf16* next) {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm((C::S - 2) * C::L));
+    block_sync();
+    __builtin_amdgcn_sched_barrier(0);
+    issue(next, s + C::S - 1);
+    bf16x8 af[C::MI], bf[C::NJ];
+    fa.load(st, 0, af);
+    fb.load(st + C::BM * C::BK, 0, bf);
+    mfma_sub<C>(acc, ca, cb);
+    mfma_sub<C>(acc, af, bf);
+    fa.load(st, 1, ca);
+    fb.load(st + C::BM * C::BK, 1, cb);
+    constexpr int NR = (TA ? 2 : 1) * C::MI + (TB ? 2 : 1) * C::NJ, NM = C::MI * C::NJ;
+    __builtin_amdgcn_sched_group_barrier(0x010, C::L, 0);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < NM; ++i) {
+        if (i < NR) __builtin_amdgcn_sched_group_barrier(0x100, NR > NM ? (NR + NM - 1) / NM : 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      }
+    }
+  };
+  int s = 0;
+  for (; s + C::S <= nk; s += C::S) {
+#pragma unroll
+    for (int b = 0; b < C::S; ++b) step(s + b, stg[b], stg[(b + C::S - 1) % C::S]);
+  }
+#pragma unroll
+  for (int b = 0; b < C::S - 1; ++b)
+    if (s + b < nk) step(s + b, stg[b], stg[(b + C::S - 1) % C::S]);
+  mfma_sub<C>(acc, ca, cb);
+  __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(0));  // loads past the end have landed
+  block_sync();
+
+  // ---- epilogue: S blocks of 32 rows at a time go through LDS as fp32, so that a
+  // thread has 8 values side by side.  Column c of row r sits at c ^ (32 * ((r >> 2) & 1)):
+  // the two half-waves write rows 4 apart. ----
+  constexpr int CPR = C::BN / 8;  // 16-byte chunks of a row
+#pragma unroll
+  for (int pass = 0; pass < C::BM / 32 / C::S; ++pass) {
+    if (pass) block_sync();
+#pragma unroll
+    for (int i = 0; i < C::S / C::WM; ++i) {
+      const int ii = pass * (C::S / C::WM) + i;
+      float* f = reinterpret_cast<float*>(wm ? stg[i * C::WM + 1] : stg[i * C::WM]);
+#pragma unroll
+      for (int j = 0; j < C::NJ; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int r = 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+          f[r * C::BN + (((wn * C::NJ + j) * 32 + (lane & 31)) ^ (((r >> 2) & 1) << 5))] = acc[ii][j][v];
+        }
+    }
+    block_sync();
+#pragma unroll
+    for (int b = 0; b < C::S; ++b) {
+      const float* f = reinterpret_cast<const float*>(stg[b]);
+      for (int e = tid; e < 32 * CPR; e += C::NT) {
+        const int r = e / CPR, c = e % CPR * 8;
+        const int row = m0 + (pass * C::S + b) * 32 + r, col = n0 + c;
+        if (row >= m1 || col >= nn) continue;
+        const float* fr = f + r * C::BN + (c ^ (((r >> 2) & 1) << 5));
+        const f32x4 v0 = *reinterpret_cast<const f32x4*>(fr), v1 = *reinterpret_cast<const f32x4*>(fr + 4);
+        float z[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+        using V = Vec<false>;
+        if constexpr (MODE == kLinDw) {
+          st16(out + g * a.w_stride + row * K + col, V::pack(z));
+        } else if constexpr (MODE == kLinDx) {
+          st16(out + row * K + col, V::pack(z));
+        } else {
+          const int64_t at = row * N + col;
+          float o[8];
+          if (a.bias) {
+            V::unpack(ld16(static_cast<const bf16*>(a.bias) + g * N + col), o);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) z[k] += o[k];
+          }
+          if (a.z) st16(static_cast<bf16*>(a.z) + at, V::pack(z));
+#pragma unroll
+          for (int k = 0; k < 8; ++k) z[k] = activate(a.act, z[k]);
+          if (a.mul) {
+            V::unpack(ld16(static_cast<const bf16*>(a.mul) + at), o);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) z[k] *= o[k];
+          }
+          if (a.resid) {
+            V::unpack(ld16(static_cast<const bf16*>(a.resid) + at), o);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) z[k] += o[k];
+          }
+          st16(out + at, V::pack(z));
+        }
+      }
+    }
+  }
+}
+
+using Big = Tile<256, 256, 2, 2, 4, 1>;
+using Mid = Tile<128, 128, 2, 2, 4, 2>;
+
+template <class C>
+hipError_t launch(LinearMode mode, const LinearArgs& a, const bf16* p, const bf16* q, bf16* out, hipStream_t s) {
+  const int64_t tn = ((mode == kLinForward ? a.N : a.K) + C::BN - 1) / C::BN;
+  const int64_t tm = mode == kLinDw ? (int64_t)a.G * ((a.N + C::BM - 1) / C::BM) : max_tiles(a.rows, a.G, C::BM);
+  const dim3 grid((uint32_t)(tm * tn));
+  if (mode == kLinForward) linear_tiles_kernel<kLinForward, C><<<grid, C::NT, 0, s>>>(a, p, q, out);
+  else if (mode == kLinDx) linear_tiles_kernel<kLinDx, C><<<grid, C::NT, 0, s>>>(a, p, q, out);
+  else linear_tiles_kernel<kLinDw, C><<<grid, C::NT, 0, s>>>(a, p, q, out);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_linear_tiles(LinearMode mode, const LinearArgs& a, const void* p, const void* q, void* out,
+                               hipStream_t s) {
+  const bf16 *pp = static_cast<const bf16*>(p), *qq = static_cast<const bf16*>(q);
+  bf16* o = static_cast<bf16*>(out);
+  const int64_t rows = mode == kLinDw ? a.N : a.rows / a.G, cols = mode == kLinForward ? a.N : a.K;
+  const int64_t big = (rows + 255) / 256 * ((cols + 255) / 256) * (mode == kLinDw ? a.G : a.G);
+  if (rows >= 192 && big >= 192) return launch<Big>(mode, a, pp, qq, o, s);
+  return launch<Mid>(mode, a, pp, qq, o, s);
+}
+
+}  // namespace moe
