@@ -113,7 +113,9 @@ __global__ __launch_bounds__(256) void linear_simple_kernel(LinearArgs a, const 
       float z = acc[v];
       if (a.bias) z += elem<F32>(a.bias, (int64_t)g * a.N + col);
       if (a.z) put<F32>(a.z, i, z);
-      float y = activate(a.act, z);
+      float v[1] = {z};
+      activate<false>(a.act, v);
+      float y = v[0];
       if (a.mul) y *= elem<F32>(a.mul, i);
       if (a.resid) y += elem<F32>(a.resid, i);
       put<F32>(out, i, y);
@@ -149,7 +151,7 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearBackArgs a, int sp
 #pragma unroll
         for (int e = 0; e < V::N; ++e) {
           float slope;
-          const float v = activate_d(a.act, z[e], slope);
+          const float v = activate_d<!F32>(a.act, z[e], slope);
           dm[e] = d[e] * v;
           d[e] = d[e] * (a.mul ? m[e] : 1.f) * slope;
         }

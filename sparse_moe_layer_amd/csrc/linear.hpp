@@ -6,23 +6,73 @@
 
 namespace moe {
 
-__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(-0.70710678f * z); }
-
-// act(z), and its derivative in d
-__device__ __forceinline__ float activate(int act, float z) {
-  if (act == MOE_ACT_SILU) return z / (1.f + expf(-z));
-  if (act == MOE_ACT_GELU) return z * normal_cdf(z);
-  return z;
+// (x + 3) erfcx(x) for x >= 0, erfcx(x) = e^(x^2) erfc(x), as a polynomial in
+// t = (x - 3) / (x + 3): a least-maximum fit over x in [0, 12], off by 4e-9.
+__device__ __forceinline__ float erfcx_poly(float t) {
+  float p = -3.14715813e-4f;
+  p = fmaf(p, t, -4.63499426e-4f);
+  p = fmaf(p, t, 3.08281556e-3f);
+  p = fmaf(p, t, -1.23808580e-3f);
+  p = fmaf(p, t, -2.68434100e-2f);
+  p = fmaf(p, t, 1.19531333e-1f);
+  p = fmaf(p, t, -3.10465366e-1f);
+  p = fmaf(p, t, 5.90228140e-1f);
+  p = fmaf(p, t, -8.83394539e-1f);
+  return fmaf(p, t, 1.07400692f);
 }
+
+// The activations.  FAST (bf16 tensors): e^x and 1/x by the hardware's, the normal
+// distribution's integral by the fit above, 2e-7 absolute and 2e-5 relative down to
+// z = -12 (8192 x 2048 outputs of GELU 252 -> 2xx us); else the exact functions.
+template <bool FAST>
+__device__ __forceinline__ float exp_of(float x) {
+  if constexpr (FAST) return __builtin_amdgcn_exp2f(x * 1.44269504f);
+  else return expf(x);
+}
+template <bool FAST>
+__device__ __forceinline__ float logistic(float z) {
+  if constexpr (FAST) return __builtin_amdgcn_rcpf(1.f + exp_of<true>(-z));
+  else return 1.f / (1.f + expf(-z));
+}
+// Phi(z); density: e^(-z^2 / 2)
+template <bool FAST>
+__device__ __forceinline__ float normal_cdf(float z, float& density) {
+  density = exp_of<FAST>(-0.5f * z * z);
+  if constexpr (FAST) {
+    const float x = fabsf(z) * 0.70710678f, r = __builtin_amdgcn_rcpf(x + 3.f);
+    const float h = 0.5f * density * r * erfcx_poly((x - 3.f) * r);
+    return z < 0.f ? h : 1.f - h;
+  } else {
+    return 0.5f * erfcf(-0.70710678f * z);
+  }
+}
+
+// n values through act
+template <bool FAST, int n>
+__device__ __forceinline__ void activate(int act, float (&z)[n]) {
+  if (act == MOE_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) z[i] *= logistic<FAST>(z[i]);
+  } else if (act == MOE_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      float e;
+      z[i] *= normal_cdf<FAST>(z[i], e);
+    }
+  }
+}
+// act(z) and its derivative
+template <bool FAST>
 __device__ __forceinline__ float activate_d(int act, float z, float& d) {
   if (act == MOE_ACT_SILU) {
-    const float g = 1.f / (1.f + expf(-z));
+    const float g = logistic<FAST>(z);
     d = g * fmaf(z, 1.f - g, 1.f);
     return z * g;
   }
   if (act == MOE_ACT_GELU) {
-    const float c = normal_cdf(z);
-    d = fmaf(z * 0.39894228f, expf(-0.5f * z * z), c);
+    float e;
+    const float c = normal_cdf<FAST>(z, e);
+    d = fmaf(z * 0.39894228f, e, c);
     return z * c;
   }
   d = 1.f;

@@ -7,20 +7,21 @@
 namespace moe {
 namespace {
 
-template <int BM_, int BN_, int WM_, int WN_, int S_, int WG_PER_CU_>
+template <int BM_, int BN_, int WM_, int WN_, int S_, int BK_, int WG_PER_CU_, bool W_ONCE_ = false>
 struct Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, BK = 32;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, BK = BK_;
+  static constexpr bool W_ONCE = W_ONCE_;  // each weight is read by one tile
+  static constexpr int KS = BK / 16;                              // matrix instructions deep
   static constexpr int NW = WM * WN, NT = 64 * NW;
   static constexpr int MI = BM / (32 * WM), NJ = BN / (32 * WN);  // 32 x 32 blocks of a wave
-  static constexpr int LA = BM / (16 * NW), LB = BN / (16 * NW);  // 1 KB direct loads a wave and stage
+  static constexpr int LA = BM * BK / 512 / NW, LB = BN * BK / 512 / NW;  // 1 KB direct loads a wave and stage
   static constexpr int L = LA + LB;
   static constexpr int STAGE = (BM + BN) * BK;  // elements
   static constexpr int WG_PER_CU = WG_PER_CU_;
   static_assert(NT == 256, "the search for tiles takes 256 threads");
-  static_assert(WM == 2 && BM == BN, "a stage holds 32 rows of the fp32 tile");
+  static_assert(WM == 2 && BM == BN && (BK == 32 || BK == 64), "tiling");
   static_assert(MI >= 1 && NJ >= 1 && LA >= 1 && LB >= 1 && L * (S - 1) < 64, "tiling");
   static_assert(S * STAGE * 2 * WG_PER_CU <= 160 * 1024, "LDS");
-  static_assert((BM / 32) % S == 0 && S % WM == 0, "the epilogue's passes");
 };
 
 constexpr int vmcnt_imm(int n) { return 0xF70 | (n & 15) | (((n >> 4) & 3) << 14); }
@@ -36,35 +37,44 @@ __device__ __forceinline__ void block_sync() {
 }
 
 // A 16-byte direct load from base + voff + soff to LDS (voff the lane's, soff the
-// wave's); past `records` bytes it writes zeros.
-__device__ __forceinline__ void dma16(const char* base, uint32_t records, uint32_t voff, uint32_t soff, bf16* l) {
+// wave's); past `records` bytes it writes zeros.  once: non-temporal.
+__device__ __forceinline__ void dma16(const char* base, uint32_t records, uint32_t voff, uint32_t soff, bf16* l,
+                                      bool once) {
   const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, records, kBufferFlags);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)l, 16, voff, soff, 0, 0);
+  if (once) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)l, 16, voff, soff, 0, 2);
+  else __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)l, 16, voff, soff, 0, 0);
 }
 
 // One operand's tile of R rows (or, contracted along its columns, R columns) as
 // the direct loads see it.  T: contracted along its columns.
-//  !T: a stage holds [R][32], 64-byte rows, 16-byte chunk c of row r at
-//      c ^ ((r >> 2) & 3): 16 rows' fragment reads of one chunk cover all banks.
-//   T: a stage holds [32][R], the 64-byte block b of contraction row k at
+//  !T: a stage holds [R][BK]; 16-byte chunk c of row r at c ^ ((r >> 2) & 3) for
+//      64-byte rows, c ^ ((r >> 1) & 7) for 128-byte rows: 16 rows' fragment reads
+//      of one chunk cover all banks.
+//   T: a stage holds [BK][R], the 64-byte block b of contraction row k at
 //      b ^ (k & 3): the transposing reads of four rows cover all banks.
+template <int BK>
+__device__ __forceinline__ int swz(int r) { return BK == 32 ? (r >> 2) & 3 : (r >> 1) & 7; }
+
 template <class C, int R, bool T>
 struct Operand {
+  static constexpr int LOADS = R * C::BK / 512 / C::NW;
   const char* base;    // the tile's first element
   int64_t bytes;       // from there to the tensor's (the contraction's) end
   int64_t ld;          // bytes from row to row
-  uint32_t off[R / (16 * C::NW)];
-  int chunk;           // !T: the lane's first k within a stage
+  uint32_t off[LOADS];
+  int chunk[2];        // !T: the lane's first k within a stage, of even and odd pieces
 
   __device__ __forceinline__ Operand(const void* p, int64_t ld_elems, int64_t bytes_, int lane, int wave)
       : base(static_cast<const char*>(p)), bytes(bytes_), ld(ld_elems * 2) {
 #pragma unroll
-    for (int i = 0; i < R / (16 * C::NW); ++i) {
+    for (int i = 0; i < LOADS; ++i) {
       const int q = C::NW * i + wave;  // the 1 KB piece of the stage
       if constexpr (!T) {
-        const int row = q * 16 + (lane >> 2);
-        chunk = ((lane & 3) ^ ((row >> 2) & 3)) * 8;  // 16 rows a piece: the same for every i
-        off[i] = (uint32_t)(row * ld) + chunk * 2;
+        constexpr int LPR = C::BK / 8;  // lanes a row
+        const int row = q * (64 / LPR) + lane / LPR;
+        const int k = ((lane % LPR) ^ swz<C::BK>(row)) * 8;
+        chunk[i & 1] = k;  // the swizzle repeats after 16 rows, which NW pieces make up
+        off[i] = (uint32_t)(row * ld) + k * 2;
       } else {
         constexpr int LPR = R / 8;  // lanes a row
         const int row = q * (64 / LPR) + lane / LPR, pos = lane % LPR;
@@ -73,8 +83,8 @@ struct Operand {
     }
   }
 
-  // The loads of the 32 contraction steps from k0 on; steps past kn give zeros.
-  __device__ __forceinline__ void issue(bf16* st, int k0, int kn, int wave) const {
+  // The loads of the BK contraction steps from k0 on; steps past kn give zeros.
+  __device__ __forceinline__ void issue(bf16* st, int k0, int kn, int wave, bool once = false) const {
     const char* b = base;
     int64_t left = bytes;
     if constexpr (T) {
@@ -82,10 +92,9 @@ struct Operand {
       left -= k0 * ld;
     }
     const uint32_t records = left <= 0 ? 0u : left < (int64_t)kNowhere ? (uint32_t)left : kNowhere;
-    const bool none = !T && k0 + chunk >= kn;
 #pragma unroll
-    for (int i = 0; i < R / (16 * C::NW); ++i)
-      dma16(b, records, none ? kNowhere : off[i], T ? 0 : k0 * 2, st + (C::NW * i + wave) * 512);
+    for (int i = 0; i < LOADS; ++i)
+      dma16(b, records, !T && k0 + chunk[i & 1] >= kn ? kNowhere : off[i], T ? 0 : k0 * 2, st + (C::NW * i + wave) * 512, once);
   }
 };
 
@@ -98,15 +107,15 @@ __device__ __forceinline__ s16x4 read_tr(const bf16* p) {
 
 // A lane's fragment reads of one operand: block b (of 32 rows or columns), K
 // sub-step ks of 16.  first: the wave's first block; step: blocks apart.
-template <int R, bool T, int NB, int STEP>
+template <int BK, int R, bool T, int NB, int STEP>
 struct Frags {
-  int o[T ? NB : 2];
+  int o[T ? NB : BK / 16];
   __device__ __forceinline__ Frags(int first, int lane) {
     if constexpr (!T) {
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
+      for (int ks = 0; ks < BK / 16; ++ks) {
         const int row = first * 32 + (lane & 31);
-        o[ks] = row * 32 + (((ks * 2 + (lane >> 5)) ^ ((row >> 2) & 3)) << 3);
+        o[ks] = row * BK + (((ks * 2 + (lane >> 5)) ^ swz<BK>(row)) << 3);
       }
     } else {
       const int k = 8 * (lane >> 5) + ((lane & 15) >> 2);
@@ -119,7 +128,7 @@ struct Frags {
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       if constexpr (!T) {
-        f[i] = *reinterpret_cast<const bf16x8*>(st + o[ks] + i * STEP * 32 * 32);
+        f[i] = *reinterpret_cast<const bf16x8*>(st + o[ks] + i * STEP * 32 * BK);
       } else {
         const bf16* p = st + o[i] + ks * 16 * R;
         f[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(read_tr(p), read_tr(p + 4 * R), 0, 1, 2, 3, 4, 5, 6, 7));
@@ -134,7 +143,23 @@ __device__ __forceinline__ void mfma_sub(f32x16 (&acc)[C::MI][C::NJ], const bf16
   for (int i = 0; i < C::MI; ++i)
 #pragma unroll
     for (int j = 0; j < C::NJ; ++j)
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[j], a[i], acc[i][j], 0, 0, 0);  // columns by rows
+}
+
+// The order of a stage's instructions, from matrix instruction I on: each comes
+// after its share of the next sub-step's NR fragment reads and of the direct
+// loads, which go out one by one (issued together they hold up the wave for as
+// long as the address unit takes for all of them).
+template <class C, int NR, int I>
+__device__ __forceinline__ void spread() {
+  constexpr int NM = C::MI * C::NJ, ALL = C::KS * NM / 2;
+  if constexpr (I < C::KS * NM) {
+    if constexpr (I % NM < NR) __builtin_amdgcn_sched_group_barrier(0x100, (NR + NM - 1) / NM, 0);
+    if constexpr (I < ALL && (I + 1) * C::L / ALL > I * C::L / ALL)
+      __builtin_amdgcn_sched_group_barrier(0x010, (I + 1) * C::L / ALL - I * C::L / ALL, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    spread<C, NR, I + 1>();
+  }
 }
 
 template <int MODE, class C>
@@ -203,11 +228,12 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
   }
   const Operand<C, C::BM, TA> oa(pa, la, ba * 2, lane, wave);
   const Operand<C, C::BN, TB> ob(pb, lb, bb * 2, lane, wave);
-  const Frags<C::BM, TA, C::MI, C::WM> fa(wm, lane);  // M-blocks wm, wm + WM, ..
-  const Frags<C::BN, TB, C::NJ, 1> fb(wn * C::NJ, lane);
+  const Frags<C::BK, C::BM, TA, C::MI, C::WM> fa(wm, lane);  // M-blocks wm, wm + WM, ..
+  const Frags<C::BK, C::BN, TB, C::NJ, 1> fb(wn * C::NJ, lane);
+  const int nk = (kn + C::BK - 1) / C::BK;
   auto issue = [&](bf16* st, int step) {
     oa.issue(st, step * C::BK, kn, wave);
-    ob.issue(st + C::BM * C::BK, step * C::BK, kn, wave);
+    ob.issue(st + C::BM * C::BK, step * C::BK, kn, wave, C::W_ONCE);
   };
 
   f32x16 acc[C::MI][C::NJ];
@@ -219,7 +245,6 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
   bf16x8 ca[C::MI] = {}, cb[C::NJ] = {};  // the stage's second sub-step, multiplied after the next barrier
 
-  const int nk = (kn + C::BK - 1) / C::BK;
 #pragma unroll
   for (int s = 0; s < C::S - 1; ++s) issue(stg[s], s);
   auto step = [&](int s, const bf16* st, bf16* next) {
@@ -228,23 +253,20 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
     block_sync();
     __builtin_amdgcn_sched_barrier(0);
     issue(next, s + C::S - 1);
-    bf16x8 af[C::MI], bf[C::NJ];
-    fa.load(st, 0, af);
-    fb.load(st + C::BM * C::BK, 0, bf);
-    mfma_sub<C>(acc, ca, cb);
-    mfma_sub<C>(acc, af, bf);
-    fa.load(st, 1, ca);
-    fb.load(st + C::BM * C::BK, 1, cb);
-    constexpr int NR = (TA ? 2 : 1) * C::MI + (TB ? 2 : 1) * C::NJ, NM = C::MI * C::NJ;
-    __builtin_amdgcn_sched_group_barrier(0x010, C::L, 0);
+    bf16x8 af[C::KS][C::MI], bf[C::KS][C::NJ];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int i = 0; i < NM; ++i) {
-        if (i < NR) __builtin_amdgcn_sched_group_barrier(0x100, NR > NM ? (NR + NM - 1) / NM : 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      }
+    for (int ks = 0; ks < C::KS; ++ks) {
+      fa.load(st, ks, af[ks]);
+      fb.load(st + C::BM * C::BK, ks, bf[ks]);
+      if (ks == 0) mfma_sub<C>(acc, ca, cb);
+      else mfma_sub<C>(acc, af[ks - 1], bf[ks - 1]);
     }
+#pragma unroll
+    for (int i = 0; i < C::MI; ++i) ca[i] = af[C::KS - 1][i];
+#pragma unroll
+    for (int j = 0; j < C::NJ; ++j) cb[j] = bf[C::KS - 1][j];
+    constexpr int NR = (TA ? 2 : 1) * C::MI + (TB ? 2 : 1) * C::NJ;
+    spread<C, NR, 0>();
   };
   int s = 0;
   for (; s + C::S <= nk; s += C::S) {
@@ -258,42 +280,56 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
   __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(0));  // loads past the end have landed
   block_sync();
 
-  // ---- epilogue: S blocks of 32 rows at a time go through LDS as fp32, so that a
-  // thread has 8 values side by side.  Column c of row r sits at c ^ (32 * ((r >> 2) & 1)):
-  // the two half-waves write rows 4 apart. ----
-  constexpr int CPR = C::BN / 8;  // 16-byte chunks of a row
+  // ---- epilogue: blocks of 32 rows go through LDS (forward: as fp32, so that z is
+  // rounded once; the gradients as bf16), so that a thread has 8 values side by side.
+  // A lane holds row lane % 32 of a block and columns 8 q + 4 (lane / 32) .. + 4; 16-byte
+  // chunk c of row r sits at c ^ (r & 15), so 16 rows' writes cover the banks. ----
+  constexpr bool F = MODE == kLinForward;
+  constexpr int ROW = C::BN * (F ? 4 : 2), PER = C::STAGE * 2 / (32 * ROW);  // bytes of a row, blocks a stage holds
+  constexpr int BPP = C::BM / 32 < C::S * PER ? C::BM / 32 : C::S * PER;     // blocks of a pass
+  static_assert(C::BM / 32 % BPP == 0 && BPP % C::WM == 0, "whole passes");
+  constexpr int CPR = C::BN / 8;  // threads a row
+  auto block = [&](int b) { return reinterpret_cast<char*>(stg[b / PER]) + b % PER * 32 * ROW; };
 #pragma unroll
-  for (int pass = 0; pass < C::BM / 32 / C::S; ++pass) {
+  for (int pass = 0; pass < C::BM / 32 / BPP; ++pass) {
     if (pass) block_sync();
 #pragma unroll
-    for (int i = 0; i < C::S / C::WM; ++i) {
-      const int ii = pass * (C::S / C::WM) + i;
-      float* f = reinterpret_cast<float*>(wm ? stg[i * C::WM + 1] : stg[i * C::WM]);
+    for (int i = 0; i < BPP / C::WM; ++i) {
+      const int ii = pass * (BPP / C::WM) + i, r = lane & 31;
+      char* f = (wm ? block(i * C::WM + 1) : block(i * C::WM)) + r * ROW;
 #pragma unroll
       for (int j = 0; j < C::NJ; ++j)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const int r = 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-          f[r * C::BN + (((wn * C::NJ + j) * 32 + (lane & 31)) ^ (((r >> 2) & 1) << 5))] = acc[ii][j][v];
+        for (int v = 0; v < 4; ++v) {
+          const f32x16& d = acc[ii][j];
+          const int u = (wn * C::NJ + j) * 8 + 2 * v + (lane >> 5);  // four columns
+          if constexpr (F) {
+            *reinterpret_cast<f32x4*>(f + ((u ^ (r & 15)) << 4)) =
+                f32x4{d[4 * v], d[4 * v + 1], d[4 * v + 2], d[4 * v + 3]};
+          } else {
+            *reinterpret_cast<bf16x4*>(f + (((u >> 1) ^ (r & 15)) << 4) + ((u & 1) << 3)) =
+                bf16x4{f2bf(d[4 * v]), f2bf(d[4 * v + 1]), f2bf(d[4 * v + 2]), f2bf(d[4 * v + 3])};
+          }
         }
     }
     block_sync();
 #pragma unroll
-    for (int b = 0; b < C::S; ++b) {
-      const float* f = reinterpret_cast<const float*>(stg[b]);
+    for (int b = 0; b < BPP; ++b) {
+      const char* f = block(b);
       for (int e = tid; e < 32 * CPR; e += C::NT) {
         const int r = e / CPR, c = e % CPR * 8;
-        const int row = m0 + (pass * C::S + b) * 32 + r, col = n0 + c;
+        const int row = m0 + (pass * BPP + b) * 32 + r, col = n0 + c;
         if (row >= m1 || col >= nn) continue;
-        const float* fr = f + r * C::BN + (c ^ (((r >> 2) & 1) << 5));
-        const f32x4 v0 = *reinterpret_cast<const f32x4*>(fr), v1 = *reinterpret_cast<const f32x4*>(fr + 4);
-        float z[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+        const char* fr = f + r * ROW;
         using V = Vec<false>;
         if constexpr (MODE == kLinDw) {
-          st16(out + g * a.w_stride + row * K + col, V::pack(z));
+          st16_nt(out + g * a.w_stride + row * K + col, ld16(fr + (((c >> 3) ^ (r & 15)) << 4)));
         } else if constexpr (MODE == kLinDx) {
-          st16(out + row * K + col, V::pack(z));
+          st16(out + row * K + col, ld16(fr + (((c >> 3) ^ (r & 15)) << 4)));
         } else {
+          const f32x4 v0 = *reinterpret_cast<const f32x4*>(fr + (((c >> 2) ^ (r & 15)) << 4));
+          const f32x4 v1 = *reinterpret_cast<const f32x4*>(fr + ((((c >> 2) + 1) ^ (r & 15)) << 4));
+          float z[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
           const int64_t at = row * N + col;
           float o[8];
           if (a.bias) {
@@ -302,8 +338,7 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
             for (int k = 0; k < 8; ++k) z[k] += o[k];
           }
           if (a.z) st16(static_cast<bf16*>(a.z) + at, V::pack(z));
-#pragma unroll
-          for (int k = 0; k < 8; ++k) z[k] = activate(a.act, z[k]);
+          activate<true>(a.act, z);
           if (a.mul) {
             V::unpack(ld16(static_cast<const bf16*>(a.mul) + at), o);
 #pragma unroll
@@ -321,8 +356,10 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
   }
 }
 
-using Big = Tile<256, 256, 2, 2, 4, 1>;
-using Mid = Tile<128, 128, 2, 2, 4, 2>;
+using Big = Tile<256, 256, 2, 2, 2, 64, 1>;
+using Mid = Tile<128, 128, 2, 2, 2, 64, 2>;
+using MidOnce = Tile<128, 128, 2, 2, 2, 64, 2, true>;
+using Short = Tile<128, 128, 2, 2, 2, 32, 4>;
 
 template <class C>
 hipError_t launch(LinearMode mode, const LinearArgs& a, const bf16* p, const bf16* q, bf16* out, hipStream_t s) {
@@ -341,9 +378,15 @@ hipError_t launch_linear_tiles(LinearMode mode, const LinearArgs& a, const void*
                                hipStream_t s) {
   const bf16 *pp = static_cast<const bf16*>(p), *qq = static_cast<const bf16*>(q);
   bf16* o = static_cast<bf16*>(out);
-  const int64_t rows = mode == kLinDw ? a.N : a.rows / a.G, cols = mode == kLinForward ? a.N : a.K;
-  const int64_t big = (rows + 255) / 256 * ((cols + 255) / 256) * (mode == kLinDw ? a.G : a.G);
-  if (rows >= 192 && big >= 192) return launch<Big>(mode, a, pp, qq, o, s);
+  if (mode == kLinDw) {
+    const int64_t tiles = (int64_t)((a.N + 255) / 256) * ((a.K + 255) / 256) * a.G;
+    if (tiles >= 192 && a.rows >= 1024 * a.G) return launch<Big>(mode, a, pp, qq, o, s);
+    return launch<Short>(mode, a, pp, qq, o, s);
+  }
+  const int64_t cols = mode == kLinForward ? a.N : a.K;
+  const int64_t tiles = (int64_t)((a.rows / a.G + 255) / 256) * a.G * ((cols + 255) / 256);
+  if (a.rows >= 192 * a.G && tiles >= 192) return launch<Big>(mode, a, pp, qq, o, s);
+  if (a.rows <= 128 * a.G) return launch<MidOnce>(mode, a, pp, qq, o, s);
   return launch<Mid>(mode, a, pp, qq, o, s);
 }
 
