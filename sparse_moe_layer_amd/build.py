@@ -17,7 +17,7 @@ OUT = os.path.join(PKG, "libmoe_mi355x.so")
 BUILD = os.path.join(PKG, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["api.cpp", "router.hip", "dispatch.hip", "gemm.hip", "gemm_dma.hip", "stream.hip", "combine.hip", "simt.hip", "gr.hip", "audit.hip", "mx.hip", "mx_experts.hip", "few.hip", "noalloc.hip", "probe.hip",
-           "api_block.cpp", "permute.hip", "norm.hip", "linear.hip", "linear_tiles.hip"]
+           "api_block.cpp", "permute.hip", "norm.hip", "linear.hip", "linear_few.hip", "linear_tiles.hip"]
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-result",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-I", os.path.join(ROOT, "include"), "-I", CSRC]

@@ -199,6 +199,8 @@ size_t linear_partial_floats(int64_t rows, int64_t N, int64_t G) {
 }
 
 hipError_t launch_linear(const LinearArgs& a, bool f32, hipStream_t s) {
+  const int64_t few = (int64_t)(a.G < a.rows ? a.G : a.rows) * ((a.N + 15) / 16);
+  if (!f32 && a.rows <= 16 * (int64_t)a.G && few <= 256) return launch_linear_few(a, s);
   if (!f32) return launch_linear_tiles(kLinForward, a, a.x, a.w, a.y, s);
   const dim3 grid(max_tiles(a.rows, a.G, kSB), (a.N + kSB - 1) / kSB);
   linear_simple_kernel<true, 0><<<grid, 256, 0, s>>>(a, a.x, a.w, a.y);

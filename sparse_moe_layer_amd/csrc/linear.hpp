@@ -92,8 +92,8 @@ struct MTile {
 };
 
 // The groups' rows cut into tiles of `bm` rows, counted in order.  Every thread
-// of a 256-thread workgroup builds it (groups <= 1024: four a thread), then
-// looks tiles up; without offsets there is nothing to search.
+// of a workgroup of 256 or 512 builds it (groups <= 1024: four a thread), then
+// looks a tile up; without offsets there is nothing to search.
 struct TileMap {
   const int32_t* offsets;
   int rows, bm, total;
@@ -105,7 +105,7 @@ struct TileMap {
       total = (rows + bm - 1) / bm;
       return;
     }
-    __shared__ int wave_total[4];
+    __shared__ int wave_total[16];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int sum = 0;
 #pragma unroll
@@ -126,7 +126,7 @@ struct TileMap {
     first = incl - sum;
     total = 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < 4; ++w) {  // the first 256 threads have all groups
       if (w < wave) first += wave_total[w];
       total += wave_total[w];
     }
@@ -150,6 +150,9 @@ struct TileMap {
 
 // m-tiles of bm rows over all groups, at most
 inline int max_tiles(int rows, int G, int bm) { return rows / bm + (G < rows ? G : rows); }
+
+// Forward for groups of at most 16 rows, bf16.
+hipError_t launch_linear_few(const LinearArgs& a, hipStream_t s);
 
 // The bf16 kernels: 1 forward, dx or dw by matrix-instruction tiles
 // (p, q: the operands; out: y, dx or dw).

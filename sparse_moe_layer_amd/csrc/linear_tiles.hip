@@ -51,9 +51,13 @@ __device__ __forceinline__ void dma16(const char* base, uint32_t records, uint32
 //      64-byte rows, c ^ ((r >> 1) & 7) for 128-byte rows: 16 rows' fragment reads
 //      of one chunk cover all banks.
 //   T: a stage holds [BK][R], the 64-byte block b of contraction row k at
-//      b ^ (k & 3): the transposing reads of four rows cover all banks.
+//      b ^ (k & 3), or b ^ ((k >> 1) & 1) for rows of two blocks: the transposing
+//      reads of four rows cover all banks.
 template <int BK>
 __device__ __forceinline__ int swz(int r) { return BK == 32 ? (r >> 2) & 3 : (r >> 1) & 7; }
+
+template <int R>
+__device__ __forceinline__ int swz_t(int k) { return R == 64 ? (k >> 1) & 1 : k & 3; }
 
 template <class C, int R, bool T>
 struct Operand {
@@ -78,7 +82,7 @@ struct Operand {
       } else {
         constexpr int LPR = R / 8;  // lanes a row
         const int row = q * (64 / LPR) + lane / LPR, pos = lane % LPR;
-        off[i] = (uint32_t)(row * ld) + ((((pos >> 2) ^ (row & 3)) << 2) | (pos & 3)) * 16;
+        off[i] = (uint32_t)(row * ld) + ((((pos >> 2) ^ swz_t<R>(row)) << 2) | (pos & 3)) * 16;
       }
     }
   }
@@ -121,7 +125,7 @@ struct Frags {
       const int k = 8 * (lane >> 5) + ((lane & 15) >> 2);
 #pragma unroll
       for (int i = 0; i < NB; ++i)
-        o[i] = k * R + (((first + i * STEP) ^ (k & 3)) << 5) + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+        o[i] = k * R + (((first + i * STEP) ^ swz_t<R>(k)) << 5) + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
     }
   }
   __device__ __forceinline__ void load(const bf16* st, int ks, bf16x8* f) const {
@@ -283,12 +287,14 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
   // ---- epilogue: blocks of 32 rows go through LDS (forward: as fp32, so that z is
   // rounded once; the gradients as bf16), so that a thread has 8 values side by side.
   // A lane holds row lane % 32 of a block and columns 8 q + 4 (lane / 32) .. + 4; 16-byte
-  // chunk c of row r sits at c ^ (r & 15), so 16 rows' writes cover the banks. ----
+  // chunk c of row r sits at c ^ (r & 15) (& 7 in a row of 8), so 16 rows' writes cover
+  // the banks. ----
   constexpr bool F = MODE == kLinForward;
   constexpr int ROW = C::BN * (F ? 4 : 2), PER = C::STAGE * 2 / (32 * ROW);  // bytes of a row, blocks a stage holds
   constexpr int BPP = C::BM / 32 < C::S * PER ? C::BM / 32 : C::S * PER;     // blocks of a pass
   static_assert(C::BM / 32 % BPP == 0 && BPP % C::WM == 0, "whole passes");
   constexpr int CPR = C::BN / 8;  // threads a row
+  constexpr int SWZ = ROW >= 256 ? 15 : 7;
   auto block = [&](int b) { return reinterpret_cast<char*>(stg[b / PER]) + b % PER * 32 * ROW; };
 #pragma unroll
   for (int pass = 0; pass < C::BM / 32 / BPP; ++pass) {
@@ -304,10 +310,10 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
           const f32x16& d = acc[ii][j];
           const int u = (wn * C::NJ + j) * 8 + 2 * v + (lane >> 5);  // four columns
           if constexpr (F) {
-            *reinterpret_cast<f32x4*>(f + ((u ^ (r & 15)) << 4)) =
+            *reinterpret_cast<f32x4*>(f + ((u ^ (r & SWZ)) << 4)) =
                 f32x4{d[4 * v], d[4 * v + 1], d[4 * v + 2], d[4 * v + 3]};
           } else {
-            *reinterpret_cast<bf16x4*>(f + (((u >> 1) ^ (r & 15)) << 4) + ((u & 1) << 3)) =
+            *reinterpret_cast<bf16x4*>(f + (((u >> 1) ^ (r & SWZ)) << 4) + ((u & 1) << 3)) =
                 bf16x4{f2bf(d[4 * v]), f2bf(d[4 * v + 1]), f2bf(d[4 * v + 2]), f2bf(d[4 * v + 3])};
           }
         }
@@ -323,12 +329,12 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
         const char* fr = f + r * ROW;
         using V = Vec<false>;
         if constexpr (MODE == kLinDw) {
-          st16_nt(out + g * a.w_stride + row * K + col, ld16(fr + (((c >> 3) ^ (r & 15)) << 4)));
+          st16_nt(out + g * a.w_stride + row * K + col, ld16(fr + (((c >> 3) ^ (r & SWZ)) << 4)));
         } else if constexpr (MODE == kLinDx) {
-          st16(out + row * K + col, ld16(fr + (((c >> 3) ^ (r & 15)) << 4)));
+          st16(out + row * K + col, ld16(fr + (((c >> 3) ^ (r & SWZ)) << 4)));
         } else {
-          const f32x4 v0 = *reinterpret_cast<const f32x4*>(fr + (((c >> 2) ^ (r & 15)) << 4));
-          const f32x4 v1 = *reinterpret_cast<const f32x4*>(fr + ((((c >> 2) + 1) ^ (r & 15)) << 4));
+          const f32x4 v0 = *reinterpret_cast<const f32x4*>(fr + (((c >> 2) ^ (r & SWZ)) << 4));
+          const f32x4 v1 = *reinterpret_cast<const f32x4*>(fr + ((((c >> 2) + 1) ^ (r & SWZ)) << 4));
           float z[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
           const int64_t at = row * N + col;
           float o[8];
@@ -359,7 +365,10 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
 using Big = Tile<256, 256, 2, 2, 2, 64, 1>;
 using Mid = Tile<128, 128, 2, 2, 2, 64, 2>;
 using MidOnce = Tile<128, 128, 2, 2, 2, 64, 2, true>;
+using Deep = Tile<128, 128, 2, 2, 4, 64, 1>;
 using Short = Tile<128, 128, 2, 2, 2, 32, 4>;
+using Small = Tile<64, 64, 2, 2, 4, 64, 2>;
+using SmallOnce = Tile<64, 64, 2, 2, 4, 64, 2, true>;
 
 template <class C>
 hipError_t launch(LinearMode mode, const LinearArgs& a, const bf16* p, const bf16* q, bf16* out, hipStream_t s) {
@@ -378,15 +387,31 @@ hipError_t launch_linear_tiles(LinearMode mode, const LinearArgs& a, const void*
                                hipStream_t s) {
   const bf16 *pp = static_cast<const bf16*>(p), *qq = static_cast<const bf16*>(q);
   bf16* o = static_cast<bf16*>(out);
-  if (mode == kLinDw) {
-    const int64_t tiles = (int64_t)((a.N + 255) / 256) * ((a.K + 255) / 256) * a.G;
-    if (tiles >= 192 && a.rows >= 1024 * a.G) return launch<Big>(mode, a, pp, qq, o, s);
-    return launch<Short>(mode, a, pp, qq, o, s);
-  }
+  const int64_t r = a.rows / a.G, touched = a.rows < a.G ? a.rows : a.G;
   const int64_t cols = mode == kLinForward ? a.N : a.K;
-  const int64_t tiles = (int64_t)((a.rows / a.G + 255) / 256) * a.G * ((cols + 255) / 256);
-  if (a.rows >= 192 * a.G && tiles >= 192) return launch<Big>(mode, a, pp, qq, o, s);
-  if (a.rows <= 128 * a.G) return launch<MidOnce>(mode, a, pp, qq, o, s);
+  auto tiles = [&](int b) {
+    const int64_t m = mode == kLinDw ? (int64_t)a.G * ((a.N + b - 1) / b) : touched * ((r + b - 1) / b > 1 ? (r + b - 1) / b : 1);
+    return m * ((cols + b - 1) / b);
+  };
+  // us, forward unless named, of one side and the other:
+  // 256-row tiles once they fill three quarters of the chip (8192 x 2560 x 8192: 283; 128-row 391), dw
+  // also with a contraction long enough for their pipeline (512 experts of 80 rows: 645, short 497);
+  if (r >= (mode == kLinDw ? 1024 : 192) && tiles(256) >= 192) return launch<Big>(mode, a, pp, qq, o, s);
+  // 64-row tiles where 128-row ones would leave most of the chip idle (256 x 4096 x 4096: 21.6; 25.7),
+  // or groups of a few rows, whose weights they stream in more and smaller pieces (512 groups of 4:
+  // 278; 291.  dx, whose rows of W they read in 128-byte pieces, only as long as there are few:
+  // 38 groups of a row 24.8; 28.3, 139 groups 100; 87), weights that no cache holds anyway
+  // non-temporally (365 groups of a row or two 185; 202, 38 groups 25.1; 21.7);
+  if (mode == kLinForward && r <= 64 && touched * a.N * a.K > 100000000) return launch<SmallOnce>(mode, a, pp, qq, o, s);
+  if (tiles(128) < 96 || (mode == kLinForward && r <= 64) || (mode == kLinDx && r <= 64 && tiles(128) <= 1024))
+    return launch<Small>(mode, a, pp, qq, o, s);
+  // a round of 128-row tiles with four stages (2000 x 2048 x 2048: 19.6; two workgroups of two stages 26.3);
+  if (tiles(128) <= 256) return launch<Deep>(mode, a, pp, qq, o, s);
+  // dw of short groups, which is loads, a few steps and stores: four workgroups a compute
+  // unit overlap them (512 groups of 80 rows 497; two 554);
+  if (mode == kLinDw && r <= 256) return launch<Short>(mode, a, pp, qq, o, s);
+  // groups of one tile read their weights once (512 groups of 80 rows 393; 404), others share them.
+  if (mode != kLinDw && r <= 128) return launch<MidOnce>(mode, a, pp, qq, o, s);
   return launch<Mid>(mode, a, pp, qq, o, s);
 }
 
