@@ -87,6 +87,8 @@ __device__ __forceinline__ int2 group_rows(const int32_t* offsets, int g, int ro
   return {lo, min(max(offsets[g + 1], lo), rows)};
 }
 
+enum LinearMode { kLinForward = 0, kLinDx = 1, kLinDw = 2 };
+
 struct MTile {
   int g, row, end;  // group, first row, end of the group
 };
@@ -154,10 +156,25 @@ inline int max_tiles(int rows, int G, int bm) { return rows / bm + (G < rows ? G
 // Forward for groups of at most 16 rows, bf16.
 hipError_t launch_linear_few(const LinearArgs& a, hipStream_t s);
 
-// The bf16 kernels: 1 forward, dx or dw by matrix-instruction tiles
-// (p, q: the operands; out: y, dx or dw).
-enum LinearMode { kLinForward = 0, kLinDx = 1, kLinDw = 2 };
-hipError_t launch_linear_tiles(LinearMode mode, const LinearArgs& a, const void* p, const void* q, void* out,
-                               hipStream_t s);
+// Sums of the dbias partials: n columns, `splits` each; n == 0: none.
+struct LinearSums {
+  const float* partial;
+  float* dbias;
+  int n, splits;
+};
+__device__ __forceinline__ void add_partials(const float* __restrict__ partial, float* __restrict__ out, int n,
+                                             int splits, int block) {
+  const int i = block * 256 + threadIdx.x;
+  if (i >= n) return;
+  float v = 0.f;
+  for (int s = 0; s < splits; ++s) v += partial[(int64_t)s * n + i];
+  out[i] = v;
+}
+
+// Products by matrix-instruction tiles: forward (a.x, a.w, a.y), or dx and dw (either may
+// be null) from dz, with the sums of the partials beside them.
+hipError_t launch_linear_tiles(const LinearArgs& a, bool f32, hipStream_t s);
+hipError_t launch_linear_back_tiles(const LinearArgs& a, bool f32, const void* dz, const void* w, const void* x,
+                                    void* dx, void* dw, const LinearSums& sums, hipStream_t s);
 
 }  // namespace moe

@@ -1,27 +1,37 @@
-// bf16 products over groups of rows on v_mfma_f32_32x32x16_bf16 tiles:
+// Products over groups of rows on matrix-instruction tiles (bf16: v_mfma_f32_32x32x16_bf16,
+// fp32: v_mfma_f32_32x32x2_f32, four of them with K 8 j + e and 8 j + 4 + e a sub-step, so
+// that a lane's operands are one 16-byte chunk of a row along K):
 //   forward  z = x W_g^T     A = x  [r][k],  B = W [n][k]     (contracted along rows of both)
 //   dx       dz W_g          A = dz [r][n],  B = W [n][k]     (B contracted along its columns)
 //   dw       dz^T x          A = dz [r][n],  B = x [r][k]     (both contracted along their columns)
 #include "linear.hpp"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
-template <int BM_, int BN_, int WM_, int WN_, int S_, int BK_, int WG_PER_CU_, bool W_ONCE_ = false>
+// F32_: fp32 tensors.  KB: bytes of a row's K step in a stage.
+template <bool F32_, int BM_, int BN_, int WM_, int WN_, int S_, int KB_, int WG_PER_CU_, bool W_ONCE_ = false>
 struct Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, BK = BK_;
-  static constexpr bool W_ONCE = W_ONCE_;  // each weight is read by one tile
-  static constexpr int KS = BK / 16;                              // matrix instructions deep
+  static constexpr bool F32 = F32_;
+  using T = typename std::conditional<F32, float, bf16>::type;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, KB = KB_;
+  static constexpr int BK = KB / (int)sizeof(T);                   // K step
+  static constexpr int CE = 16 / (int)sizeof(T);                   // values of a 16-byte chunk
+  static constexpr int KS = KB / 32;                               // sub-steps of two chunks a row
+  static constexpr int PER_SUB = F32 ? 4 : 1;                      // matrix instructions of a block and sub-step
+  static constexpr bool W_ONCE = W_ONCE_;                          // each weight is read by one tile
   static constexpr int NW = WM * WN, NT = 64 * NW;
-  static constexpr int MI = BM / (32 * WM), NJ = BN / (32 * WN);  // 32 x 32 blocks of a wave
-  static constexpr int LA = BM * BK / 512 / NW, LB = BN * BK / 512 / NW;  // 1 KB direct loads a wave and stage
+  static constexpr int MI = BM / (32 * WM), NJ = BN / (32 * WN);   // 32 x 32 blocks of a wave
+  static constexpr int LA = BM * KB / 1024 / NW, LB = BN * KB / 1024 / NW;  // 1 KB direct loads a wave and stage
   static constexpr int L = LA + LB;
-  static constexpr int STAGE = (BM + BN) * BK;  // elements
+  static constexpr int STAGE = (BM + BN) * KB;                     // bytes
   static constexpr int WG_PER_CU = WG_PER_CU_;
   static_assert(NT == 256, "the search for tiles takes 256 threads");
-  static_assert(WM == 2 && BM == BN && (BK == 32 || BK == 64), "tiling");
+  static_assert(WM == 2 && BM == BN && (KB == 64 || KB == 128), "tiling");
   static_assert(MI >= 1 && NJ >= 1 && LA >= 1 && LB >= 1 && L * (S - 1) < 64, "tiling");
-  static_assert(S * STAGE * 2 * WG_PER_CU <= 160 * 1024, "LDS");
+  static_assert(S * STAGE * WG_PER_CU <= 160 * 1024, "LDS");
 };
 
 constexpr int vmcnt_imm(int n) { return 0xF70 | (n & 15) | (((n >> 4) & 3) << 14); }
@@ -38,57 +48,51 @@ __device__ __forceinline__ void block_sync() {
 
 // A 16-byte direct load from base + voff + soff to LDS (voff the lane's, soff the
 // wave's); past `records` bytes it writes zeros.  once: non-temporal.
-__device__ __forceinline__ void dma16(const char* base, uint32_t records, uint32_t voff, uint32_t soff, bf16* l,
+__device__ __forceinline__ void dma16(const char* base, uint32_t records, uint32_t voff, uint32_t soff, char* l,
                                       bool once) {
   const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, records, kBufferFlags);
   if (once) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)l, 16, voff, soff, 0, 2);
   else __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)l, 16, voff, soff, 0, 0);
 }
 
+// Where 16-byte chunk c of an operand's row lies within the row of a stage: c ^ swz.
+//  Rows along K (KB bytes): 16 rows' fragment reads of one chunk cover all banks.
+template <int KB>
+__device__ __forceinline__ int swz(int r) { return KB == 64 ? (r >> 2) & 3 : (r >> 1) & 7; }
+//  Rows across K (R values): bf16, the transposing reads of four rows k .. k + 3 take 64
+//  bytes each; fp32, a wave reads 128 bytes of rows k and k + 4.
+template <bool F32, int R>
+__device__ __forceinline__ int swz_t(int k) {
+  return F32 ? (k & 4) << 1 : R == 64 ? (k & 2) << 1 : (k & 3) << 2;
+}
+
 // One operand's tile of R rows (or, contracted along its columns, R columns) as
-// the direct loads see it.  T: contracted along its columns.
-//  !T: a stage holds [R][BK]; 16-byte chunk c of row r at c ^ ((r >> 2) & 3) for
-//      64-byte rows, c ^ ((r >> 1) & 7) for 128-byte rows: 16 rows' fragment reads
-//      of one chunk cover all banks.
-//   T: a stage holds [BK][R], the 64-byte block b of contraction row k at
-//      b ^ (k & 3), or b ^ ((k >> 1) & 1) for rows of two blocks: the transposing
-//      reads of four rows cover all banks.
-template <int BK>
-__device__ __forceinline__ int swz(int r) { return BK == 32 ? (r >> 2) & 3 : (r >> 1) & 7; }
-
-template <int R>
-__device__ __forceinline__ int swz_t(int k) { return R == 64 ? (k >> 1) & 1 : k & 3; }
-
+// the direct loads see it.  T: contracted along its columns; a stage then holds
+// [BK][R] values, else [R][BK].
 template <class C, int R, bool T>
 struct Operand {
-  static constexpr int LOADS = R * C::BK / 512 / C::NW;
+  static constexpr int LOADS = R * C::KB / 1024 / C::NW;
   const char* base;    // the tile's first element
   int64_t bytes;       // from there to the tensor's (the contraction's) end
   int64_t ld;          // bytes from row to row
   uint32_t off[LOADS];
   int chunk[2];        // !T: the lane's first k within a stage, of even and odd pieces
 
-  __device__ __forceinline__ Operand(const void* p, int64_t ld_elems, int64_t bytes_, int lane, int wave)
-      : base(static_cast<const char*>(p)), bytes(bytes_), ld(ld_elems * 2) {
+  __device__ __forceinline__ Operand(const typename C::T* p, int64_t ld_, int64_t left, int lane, int wave)
+      : base(reinterpret_cast<const char*>(p)), bytes(left * (int)sizeof(*p)), ld(ld_ * (int)sizeof(*p)) {
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
       const int q = C::NW * i + wave;  // the 1 KB piece of the stage
-      if constexpr (!T) {
-        constexpr int LPR = C::BK / 8;  // lanes a row
-        const int row = q * (64 / LPR) + lane / LPR;
-        const int k = ((lane % LPR) ^ swz<C::BK>(row)) * 8;
-        chunk[i & 1] = k;  // the swizzle repeats after 16 rows, which NW pieces make up
-        off[i] = (uint32_t)(row * ld) + k * 2;
-      } else {
-        constexpr int LPR = R / 8;  // lanes a row
-        const int row = q * (64 / LPR) + lane / LPR, pos = lane % LPR;
-        off[i] = (uint32_t)(row * ld) + ((((pos >> 2) ^ swz_t<R>(row)) << 2) | (pos & 3)) * 16;
-      }
+      constexpr int LPR = T ? R / C::CE : C::KB / 16;  // lanes a row
+      const int row = q * (64 / LPR) + lane / LPR;
+      const int c = (lane % LPR) ^ (T ? swz_t<C::F32, R>(row) : swz<C::KB>(row));
+      if constexpr (!T) chunk[i & 1] = c * C::CE;  // the swizzle repeats after 16 rows, at most two pieces of NW
+      off[i] = (uint32_t)(row * ld) + c * 16;
     }
   }
 
   // The loads of the BK contraction steps from k0 on; steps past kn give zeros.
-  __device__ __forceinline__ void issue(bf16* st, int k0, int kn, int wave, bool once = false) const {
+  __device__ __forceinline__ void issue(char* st, int k0, int kn, int wave, bool once = false) const {
     const char* b = base;
     int64_t left = bytes;
     if constexpr (T) {
@@ -98,56 +102,74 @@ struct Operand {
     const uint32_t records = left <= 0 ? 0u : left < (int64_t)kNowhere ? (uint32_t)left : kNowhere;
 #pragma unroll
     for (int i = 0; i < LOADS; ++i)
-      dma16(b, records, !T && k0 + chunk[i & 1] >= kn ? kNowhere : off[i], T ? 0 : k0 * 2, st + (C::NW * i + wave) * 512, once);
+      dma16(b, records, !T && k0 + chunk[i & 1] >= kn ? kNowhere : off[i], T ? 0 : k0 * (16 / C::CE),
+            st + (C::NW * i + wave) * 1024, once);
   }
 };
 
 // Within each 16 lanes, lane i gives the address of values 4 (i & 3) .. + 4 of row
 // i >> 2 and gets value i of the four rows.
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ s16x4 read_tr(const bf16* p) {
+__device__ __forceinline__ s16x4 read_tr(const char* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
 }
 
-// A lane's fragment reads of one operand: block b (of 32 rows or columns), K
-// sub-step ks of 16.  first: the wave's first block; step: blocks apart.
-template <int BK, int R, bool T, int NB, int STEP>
+// A lane's fragments of one operand: block b (of 32 rows or columns), sub-step ks;
+// row lane % 32, chunk 2 ks + lane / 32 of the stage's K.  first: the wave's first
+// block; STEP: blocks apart.
+template <class C, int R, bool T, int NB, int STEP>
 struct Frags {
-  int o[T ? NB : BK / 16];
+  using F = typename std::conditional<C::F32, f32x4, bf16x8>::type;
+  int o[T ? NB : C::KS];
   __device__ __forceinline__ Frags(int first, int lane) {
     if constexpr (!T) {
 #pragma unroll
-      for (int ks = 0; ks < BK / 16; ++ks) {
+      for (int ks = 0; ks < C::KS; ++ks) {
         const int row = first * 32 + (lane & 31);
-        o[ks] = row * BK + (((ks * 2 + (lane >> 5)) ^ swz<BK>(row)) << 3);
+        o[ks] = row * C::KB + (((ks * 2 + (lane >> 5)) ^ swz<C::KB>(row)) << 4);
       }
-    } else {
-      const int k = 8 * (lane >> 5) + ((lane & 15) >> 2);
+    } else if constexpr (C::F32) {
+      const int k = 4 * (lane >> 5);
 #pragma unroll
       for (int i = 0; i < NB; ++i)
-        o[i] = k * R + (((first + i * STEP) ^ swz_t<R>(k)) << 5) + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+        o[i] = k * R * 4 + ((((first + i * STEP) * 8 + ((lane & 31) >> 2)) ^ swz_t<true, R>(k)) << 4) + 4 * (lane & 3);
+    } else {
+      const int k = 8 * (lane >> 5) + ((lane & 15) >> 2);  // and k + 4, of the same swizzle
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+        o[i] = k * R * 2 + ((((first + i * STEP) * 4 + ((lane & 31) >> 4) * 2 + ((lane & 3) >> 1)) ^ swz_t<false, R>(k)) << 4) +
+               8 * (lane & 1);
     }
   }
-  __device__ __forceinline__ void load(const bf16* st, int ks, bf16x8* f) const {
+  __device__ __forceinline__ void load(const char* st, int ks, F* f) const {
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       if constexpr (!T) {
-        f[i] = *reinterpret_cast<const bf16x8*>(st + o[ks] + i * STEP * 32 * BK);
+        f[i] = *reinterpret_cast<const F*>(st + o[ks] + i * STEP * 32 * C::KB);
+      } else if constexpr (C::F32) {
+        const char* p = st + o[i] + ks * 8 * R * 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[i][e] = *reinterpret_cast<const float*>(p + e * R * 4);
       } else {
-        const bf16* p = st + o[i] + ks * 16 * R;
-        f[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(read_tr(p), read_tr(p + 4 * R), 0, 1, 2, 3, 4, 5, 6, 7));
+        const char* p = st + o[i] + ks * 16 * R * 2;
+        f[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(read_tr(p), read_tr(p + 4 * R * 2), 0, 1, 2, 3, 4, 5, 6, 7));
       }
     }
   }
 };
 
-template <class C>
-__device__ __forceinline__ void mfma_sub(f32x16 (&acc)[C::MI][C::NJ], const bf16x8* a, const bf16x8* b) {
+// Columns by rows, so that a lane has four columns of a row side by side.
+template <class C, class F>
+__device__ __forceinline__ void mfma_sub(f32x16 (&acc)[C::MI][C::NJ], const F* a, const F* b) {
 #pragma unroll
-  for (int i = 0; i < C::MI; ++i)
+  for (int e = 0; e < C::PER_SUB; ++e)
 #pragma unroll
-    for (int j = 0; j < C::NJ; ++j)
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[j], a[i], acc[i][j], 0, 0, 0);  // columns by rows
+    for (int i = 0; i < C::MI; ++i)
+#pragma unroll
+      for (int j = 0; j < C::NJ; ++j) {
+        if constexpr (C::F32) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(b[j][e], a[i][e], acc[i][j], 0, 0, 0);
+        else acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
+      }
 }
 
 // The order of a stage's instructions, from matrix instruction I on: each comes
@@ -156,7 +178,7 @@ __device__ __forceinline__ void mfma_sub(f32x16 (&acc)[C::MI][C::NJ], const bf16
 // long as the address unit takes for all of them).
 template <class C, int NR, int I>
 __device__ __forceinline__ void spread() {
-  constexpr int NM = C::MI * C::NJ, ALL = C::KS * NM / 2;
+  constexpr int NM = C::MI * C::NJ * C::PER_SUB, ALL = C::KS * NM / 2;
   if constexpr (I < C::KS * NM) {
     if constexpr (I % NM < NR) __builtin_amdgcn_sched_group_barrier(0x100, (NR + NM - 1) / NM, 0);
     if constexpr (I < ALL && (I + 1) * C::L / ALL > I * C::L / ALL)
@@ -166,17 +188,12 @@ __device__ __forceinline__ void spread() {
   }
 }
 
+// One tile, the bid-th: stg the stages.
 template <int MODE, class C>
-__global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_kernel(LinearArgs a, const bf16* p,
-                                                                                       const bf16* q, bf16* out) {
+__device__ __forceinline__ void run_tile(const LinearArgs& a, const typename C::T* p, const typename C::T* q,
+                                         typename C::T* out, int super, int bid, char* const (&stg)[4]) {
+  using T = typename C::T;
   constexpr bool TA = MODE == kLinDw, TB = MODE != kLinForward;
-  // separate arrays: a read of one stage does not wait for loads into another
-  __shared__ __attribute__((aligned(1024))) bf16 s0[C::STAGE];
-  __shared__ __attribute__((aligned(1024))) bf16 s1[C::STAGE];
-  __shared__ __attribute__((aligned(1024))) bf16 s2[C::S > 2 ? C::STAGE : 8];
-  __shared__ __attribute__((aligned(1024))) bf16 s3[C::S > 3 ? C::STAGE : 8];
-  bf16* stg[4];
-  stg[0] = s0, stg[1] = s1, stg[2] = s2, stg[3] = s3;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / C::WN, wn = wave % C::WN;
@@ -188,14 +205,12 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
   const TileMap map(MODE == kLinDw ? nullptr : a.offsets, a.G, a.rows, C::BM);
   const int tm = MODE == kLinDw ? a.G * ((a.N + C::BM - 1) / C::BM) : map.total;
   const int total = tm * tn;
-  const int bid = blockIdx.x;
   if (bid >= total) return;
   const int x = bid & 7, per = total >> 3, rem = total & 7;
   const int t = x * per + min(x, rem) + (bid >> 3);
-  // runs of kSuper m-tiles by all n-tiles, m first
-  constexpr int kSuper = C::BM == 256 ? 4 : 1;
-  const int sb = t / (kSuper * tn) * kSuper, in = t - sb * tn;
-  const int deep = min(tm - sb, kSuper);
+  // runs of `super` m-tiles by all n-tiles, m first
+  const int sb = t / (super * tn) * super, in = t - sb * tn;
+  const int deep = min(tm - sb, super);
   const int mt = sb + in % deep, nt = in / deep;
 
   int g, m0, m1, kn;
@@ -218,7 +233,7 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
   const int n0 = nt * C::BN;
 
   const int64_t K = a.K, N = a.N;
-  const bf16 *pa, *pb;
+  const T *pa, *pb;
   int64_t la, lb, ba, bb;  // row lengths, elements left
   if constexpr (MODE == kLinForward) {
     pa = p + m0 * K, la = K, ba = (m1 - m0) * K;
@@ -230,14 +245,14 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
     pa = p + r0 * N + m0, la = N, ba = kn * N - m0;
     pb = q + r0 * K + n0, lb = K, bb = kn * K - n0;
   }
-  const Operand<C, C::BM, TA> oa(pa, la, ba * 2, lane, wave);
-  const Operand<C, C::BN, TB> ob(pb, lb, bb * 2, lane, wave);
-  const Frags<C::BK, C::BM, TA, C::MI, C::WM> fa(wm, lane);  // M-blocks wm, wm + WM, ..
-  const Frags<C::BK, C::BN, TB, C::NJ, 1> fb(wn * C::NJ, lane);
+  const Operand<C, C::BM, TA> oa(pa, la, ba, lane, wave);
+  const Operand<C, C::BN, TB> ob(pb, lb, bb, lane, wave);
+  const Frags<C, C::BM, TA, C::MI, C::WM> fa(wm, lane);  // M-blocks wm, wm + WM, ..
+  const Frags<C, C::BN, TB, C::NJ, 1> fb(wn * C::NJ, lane);
   const int nk = (kn + C::BK - 1) / C::BK;
-  auto issue = [&](bf16* st, int step) {
+  auto issue = [&](char* st, int step) {
     oa.issue(st, step * C::BK, kn, wave);
-    ob.issue(st + C::BM * C::BK, step * C::BK, kn, wave, C::W_ONCE);
+    ob.issue(st + C::BM * C::KB, step * C::BK, kn, wave, C::W_ONCE);
   };
 
   f32x16 acc[C::MI][C::NJ];
@@ -247,21 +262,22 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
     for (int j = 0; j < C::NJ; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-  bf16x8 ca[C::MI] = {}, cb[C::NJ] = {};  // the stage's second sub-step, multiplied after the next barrier
+  using F = typename std::conditional<C::F32, f32x4, bf16x8>::type;
+  F ca[C::MI] = {}, cb[C::NJ] = {};  // the stage's second sub-step, multiplied after the next barrier
 
 #pragma unroll
   for (int s = 0; s < C::S - 1; ++s) issue(stg[s], s);
-  auto step = [&](int s, const bf16* st, bf16* next) {
+  auto step = [&](int s, const char* st, char* next) {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm((C::S - 2) * C::L));
     block_sync();
     __builtin_amdgcn_sched_barrier(0);
     issue(next, s + C::S - 1);
-    bf16x8 af[C::KS][C::MI], bf[C::KS][C::NJ];
+    F af[C::KS][C::MI], bf[C::KS][C::NJ];
 #pragma unroll
     for (int ks = 0; ks < C::KS; ++ks) {
       fa.load(st, ks, af[ks]);
-      fb.load(st + C::BM * C::BK, ks, bf[ks]);
+      fb.load(st + C::BM * C::KB, ks, bf[ks]);
       if (ks == 0) mfma_sub<C>(acc, ca, cb);
       else mfma_sub<C>(acc, af[ks - 1], bf[ks - 1]);
     }
@@ -269,7 +285,7 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
     for (int i = 0; i < C::MI; ++i) ca[i] = af[C::KS - 1][i];
 #pragma unroll
     for (int j = 0; j < C::NJ; ++j) cb[j] = bf[C::KS - 1][j];
-    constexpr int NR = (TA ? 2 : 1) * C::MI + (TB ? 2 : 1) * C::NJ;
+    constexpr int TR = C::F32 ? 4 : 2, NR = (TA ? TR : 1) * C::MI + (TB ? TR : 1) * C::NJ;
     spread<C, NR, 0>();
   };
   int s = 0;
@@ -284,18 +300,17 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
   __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(0));  // loads past the end have landed
   block_sync();
 
-  // ---- epilogue: blocks of 32 rows go through LDS (forward: as fp32, so that z is
-  // rounded once; the gradients as bf16), so that a thread has 8 values side by side.
-  // A lane holds row lane % 32 of a block and columns 8 q + 4 (lane / 32) .. + 4; 16-byte
-  // chunk c of row r sits at c ^ (r & 15) (& 7 in a row of 8), so 16 rows' writes cover
-  // the banks. ----
-  constexpr bool F = MODE == kLinForward;
-  constexpr int ROW = C::BN * (F ? 4 : 2), PER = C::STAGE * 2 / (32 * ROW);  // bytes of a row, blocks a stage holds
-  constexpr int BPP = C::BM / 32 < C::S * PER ? C::BM / 32 : C::S * PER;     // blocks of a pass
+  // ---- epilogue: blocks of 32 rows go through LDS (bf16 gradients as bf16, the rest as
+  // fp32, so that z is rounded once), so that a thread has 8 values side by side.  A lane
+  // holds row lane % 32 of a block and columns 8 q + 4 (lane / 32) .. + 4; 16-byte chunk c
+  // of row r sits at c ^ (r & 15) (& 7 in a row of 8), so 16 rows' writes cover the banks. ----
+  constexpr bool WIDE = MODE == kLinForward || C::F32;
+  constexpr int ROW = C::BN * (WIDE ? 4 : 2), PER = C::STAGE / (32 * ROW);  // bytes of a row, blocks a stage holds
+  constexpr int BPP = C::BM / 32 < C::S * PER ? C::BM / 32 : C::S * PER;    // blocks of a pass
   static_assert(C::BM / 32 % BPP == 0 && BPP % C::WM == 0, "whole passes");
   constexpr int CPR = C::BN / 8;  // threads a row
   constexpr int SWZ = ROW >= 256 ? 15 : 7;
-  auto block = [&](int b) { return reinterpret_cast<char*>(stg[b / PER]) + b % PER * 32 * ROW; };
+  auto block = [&](int b) { return stg[b / PER] + b % PER * 32 * ROW; };
 #pragma unroll
   for (int pass = 0; pass < C::BM / 32 / BPP; ++pass) {
     if (pass) block_sync();
@@ -309,7 +324,7 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
         for (int v = 0; v < 4; ++v) {
           const f32x16& d = acc[ii][j];
           const int u = (wn * C::NJ + j) * 8 + 2 * v + (lane >> 5);  // four columns
-          if constexpr (F) {
+          if constexpr (WIDE) {
             *reinterpret_cast<f32x4*>(f + ((u ^ (r & SWZ)) << 4)) =
                 f32x4{d[4 * v], d[4 * v + 1], d[4 * v + 2], d[4 * v + 3]};
           } else {
@@ -327,92 +342,242 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
         const int row = m0 + (pass * BPP + b) * 32 + r, col = n0 + c;
         if (row >= m1 || col >= nn) continue;
         const char* fr = f + r * ROW;
-        using V = Vec<false>;
-        if constexpr (MODE == kLinDw) {
-          st16_nt(out + g * a.w_stride + row * K + col, ld16(fr + (((c >> 3) ^ (r & SWZ)) << 4)));
-        } else if constexpr (MODE == kLinDx) {
-          st16(out + row * K + col, ld16(fr + (((c >> 3) ^ (r & SWZ)) << 4)));
+        T* o = out + (MODE == kLinDw ? g * a.w_stride : 0) + (int64_t)row * nn + col;
+        if constexpr (!WIDE) {
+          const u32x4 v = ld16(fr + (((c >> 3) ^ (r & SWZ)) << 4));
+          if constexpr (MODE == kLinDw) st16_nt(o, v);
+          else st16(o, v);
         } else {
-          const f32x4 v0 = *reinterpret_cast<const f32x4*>(fr + (((c >> 2) ^ (r & SWZ)) << 4));
-          const f32x4 v1 = *reinterpret_cast<const f32x4*>(fr + ((((c >> 2) + 1) ^ (r & SWZ)) << 4));
-          float z[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
-          const int64_t at = row * N + col;
-          float o[8];
-          if (a.bias) {
-            V::unpack(ld16(static_cast<const bf16*>(a.bias) + g * N + col), o);
+          // fp32: the last four of the eight columns may be past the end
+          constexpr int H = C::F32 ? 2 : 1, W = 8 / H;
+          using V = Vec<C::F32>;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) z[k] += o[k];
-          }
-          if (a.z) st16(static_cast<bf16*>(a.z) + at, V::pack(z));
-          activate<true>(a.act, z);
-          if (a.mul) {
-            V::unpack(ld16(static_cast<const bf16*>(a.mul) + at), o);
+          for (int h = 0; h < H; ++h) {
+            if (h && col + W >= nn) continue;
+            float z[W];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) z[k] *= o[k];
-          }
-          if (a.resid) {
-            V::unpack(ld16(static_cast<const bf16*>(a.resid) + at), o);
+            for (int k = 0; k < W; k += 4) {
+              const f32x4 v = *reinterpret_cast<const f32x4*>(fr + ((((c >> 2) + h + k / 4) ^ (r & SWZ)) << 4));
 #pragma unroll
-            for (int k = 0; k < 8; ++k) z[k] += o[k];
+              for (int l = 0; l < 4; ++l) z[k + l] = v[l];
+            }
+            if constexpr (MODE == kLinForward) {
+              const int64_t at = (int64_t)row * nn + col + h * W;
+              float x[W];
+              if (a.bias) {
+                V::unpack(ld16(static_cast<const T*>(a.bias) + (int64_t)g * nn + col + h * W), x);
+#pragma unroll
+                for (int k = 0; k < W; ++k) z[k] += x[k];
+              }
+              if (a.z) st16(static_cast<T*>(a.z) + at, V::pack(z));
+              activate<!C::F32>(a.act, z);
+              if (a.mul) {
+                V::unpack(ld16(static_cast<const T*>(a.mul) + at), x);
+#pragma unroll
+                for (int k = 0; k < W; ++k) z[k] *= x[k];
+              }
+              if (a.resid) {
+                V::unpack(ld16(static_cast<const T*>(a.resid) + at), x);
+#pragma unroll
+                for (int k = 0; k < W; ++k) z[k] += x[k];
+              }
+            }
+            if constexpr (MODE == kLinDw) st16_nt(o + h * W, V::pack(z));
+            else st16(o + h * W, V::pack(z));
           }
-          st16(out + at, V::pack(z));
         }
       }
     }
   }
 }
 
-using Big = Tile<256, 256, 2, 2, 2, 64, 1>;
-using Mid = Tile<128, 128, 2, 2, 2, 64, 2>;
-using MidOnce = Tile<128, 128, 2, 2, 2, 64, 2, true>;
-using Deep = Tile<128, 128, 2, 2, 4, 64, 1>;
-using Short = Tile<128, 128, 2, 2, 2, 32, 4>;
-using Small = Tile<64, 64, 2, 2, 4, 64, 2>;
-using SmallOnce = Tile<64, 64, 2, 2, 4, 64, 2, true>;
+// A launch's work: sums of the dbias partials (workgroups [0, sums)), then the tiles
+// of one product, then those of another.
+struct Job {
+  LinearArgs a;
+  const void *p, *q[2];
+  void* out[2];
+  int super[2];
+  int sums, second;  // first workgroups of the first and the second product
+  const float* partial;
+  float* dbias;
+  int n, splits;
+};
 
-template <class C>
-hipError_t launch(LinearMode mode, const LinearArgs& a, const bf16* p, const bf16* q, bf16* out, hipStream_t s) {
-  const int64_t tn = ((mode == kLinForward ? a.N : a.K) + C::BN - 1) / C::BN;
-  const int64_t tm = mode == kLinDw ? (int64_t)a.G * ((a.N + C::BM - 1) / C::BM) : max_tiles(a.rows, a.G, C::BM);
-  const dim3 grid((uint32_t)(tm * tn));
-  if (mode == kLinForward) linear_tiles_kernel<kLinForward, C><<<grid, C::NT, 0, s>>>(a, p, q, out);
-  else if (mode == kLinDx) linear_tiles_kernel<kLinDx, C><<<grid, C::NT, 0, s>>>(a, p, q, out);
-  else linear_tiles_kernel<kLinDw, C><<<grid, C::NT, 0, s>>>(a, p, q, out);
-  return hipGetLastError();
+// M1, M2: the products' modes (M2 < 0: one product).
+template <int M1, int M2, class C>
+__global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_kernel(Job j) {
+  using T = typename C::T;
+  // separate arrays: a read of one stage does not wait for loads into another
+  __shared__ __attribute__((aligned(1024))) char s0[C::STAGE];
+  __shared__ __attribute__((aligned(1024))) char s1[C::STAGE];
+  __shared__ __attribute__((aligned(1024))) char s2[C::S > 2 ? C::STAGE : 16];
+  __shared__ __attribute__((aligned(1024))) char s3[C::S > 3 ? C::STAGE : 16];
+  char* stg[4];
+  stg[0] = s0, stg[1] = s1, stg[2] = s2, stg[3] = s3;
+  const int bid = blockIdx.x;
+  if (M1 != kLinForward && bid < j.sums) {
+    add_partials(j.partial, j.dbias, j.n, j.splits, bid);
+    return;
+  }
+  const T* p = static_cast<const T*>(j.p);
+  if (M2 < 0 || bid < j.second)
+    run_tile<M1, C>(j.a, p, static_cast<const T*>(j.q[0]), static_cast<T*>(j.out[0]), j.super[0], bid - j.sums, stg);
+  else if constexpr (M2 >= 0)
+    run_tile<M2, C>(j.a, p, static_cast<const T*>(j.q[1]), static_cast<T*>(j.out[1]), j.super[1], bid - j.second, stg);
 }
 
-}  // namespace
+template <bool F32>
+struct Tiles {
+  using Big = Tile<F32, 256, 256, 2, 2, 2, 128, 1>;
+  using Mid = Tile<F32, 128, 128, 2, 2, 2, 128, 2>;
+  using MidOnce = Tile<F32, 128, 128, 2, 2, 2, 128, 2, true>;
+  using Deep = Tile<F32, 128, 128, 2, 2, 4, 128, 1>;
+  using Short = Tile<F32, 128, 128, 2, 2, 2, 64, 4>;
+  using Small = Tile<F32, 64, 64, 2, 2, 4, 128, 2>;
+  using SmallOnce = Tile<F32, 64, 64, 2, 2, 4, 128, 2, true>;
+};
+enum Choice { kBig, kMid, kMidOnce, kDeep, kShort, kSmall, kSmallOnce };
 
-hipError_t launch_linear_tiles(LinearMode mode, const LinearArgs& a, const void* p, const void* q, void* out,
-                               hipStream_t s) {
-  const bf16 *pp = static_cast<const bf16*>(p), *qq = static_cast<const bf16*>(q);
-  bf16* o = static_cast<bf16*>(out);
-  const int64_t r = a.rows / a.G, touched = a.rows < a.G ? a.rows : a.G;
-  const int64_t cols = mode == kLinForward ? a.N : a.K;
-  auto tiles = [&](int b) {
-    const int64_t m = mode == kLinDw ? (int64_t)a.G * ((a.N + b - 1) / b) : touched * ((r + b - 1) / b > 1 ? (r + b - 1) / b : 1);
-    return m * ((cols + b - 1) / b);
-  };
+// Rows of a group on average, and the tiles of edge b that a product takes about.
+int64_t group_mean(const LinearArgs& a) { return a.rows / a.G; }
+int64_t tiles_about(LinearMode mode, const LinearArgs& a, int b) {
+  const int64_t touched = a.rows < a.G ? a.rows : a.G, deep = (group_mean(a) + b - 1) / b;
+  const int64_t m = mode == kLinDw ? (int64_t)a.G * ((a.N + b - 1) / b) : touched * (deep > 1 ? deep : 1);
+  return m * (((mode == kLinForward ? a.N : a.K) + b - 1) / b);
+}
+
+Choice choose(LinearMode mode, const LinearArgs& a, bool f32) {
+  const int64_t r = group_mean(a), touched = a.rows < a.G ? a.rows : a.G;
+  const int64_t t128 = tiles_about(mode, a, 128);
   // us, forward unless named, of one side and the other:
   // 256-row tiles once they fill three quarters of the chip (8192 x 2560 x 8192: 283; 128-row 391), dw
   // also with a contraction long enough for their pipeline (512 experts of 80 rows: 645, short 497);
-  if (r >= (mode == kLinDw ? 1024 : 192) && tiles(256) >= 192) return launch<Big>(mode, a, pp, qq, o, s);
+  if (r >= (mode == kLinDw ? 1024 : 192) && tiles_about(mode, a, 256) >= 192) return kBig;
   // 64-row tiles where 128-row ones would leave most of the chip idle (256 x 4096 x 4096: 21.6; 25.7),
   // or groups of a few rows, whose weights they stream in more and smaller pieces (512 groups of 4:
   // 278; 291.  dx, whose rows of W they read in 128-byte pieces, only as long as there are few:
   // 38 groups of a row 24.8; 28.3, 139 groups 100; 87), weights that no cache holds anyway
   // non-temporally (365 groups of a row or two 185; 202, 38 groups 25.1; 21.7);
-  if (mode == kLinForward && r <= 64 && touched * a.N * a.K > 100000000) return launch<SmallOnce>(mode, a, pp, qq, o, s);
-  if (tiles(128) < 96 || (mode == kLinForward && r <= 64) || (mode == kLinDx && r <= 64 && tiles(128) <= 1024))
-    return launch<Small>(mode, a, pp, qq, o, s);
+  if (mode == kLinForward && r <= 64 && touched * a.N * a.K > (f32 ? 50000000 : 100000000)) return kSmallOnce;
+  if (t128 < 96 || (mode == kLinForward && r <= 64) || (mode == kLinDx && r <= 64 && t128 <= 1024)) return kSmall;
   // a round of 128-row tiles with four stages (2000 x 2048 x 2048: 19.6; two workgroups of two stages 26.3);
-  if (tiles(128) <= 256) return launch<Deep>(mode, a, pp, qq, o, s);
+  if (t128 <= 256) return kDeep;
   // dw of short groups, which is loads, a few steps and stores: four workgroups a compute
   // unit overlap them (512 groups of 80 rows 497; two 554);
-  if (mode == kLinDw && r <= 256) return launch<Short>(mode, a, pp, qq, o, s);
+  if (mode == kLinDw && r <= 256) return kShort;
   // groups of one tile read their weights once (512 groups of 80 rows 393; 404), others share them.
-  if (mode != kLinDw && r <= 128) return launch<MidOnce>(mode, a, pp, qq, o, s);
-  return launch<Mid>(mode, a, pp, qq, o, s);
+  return mode != kLinDw && r <= 128 ? kMidOnce : kMid;
+}
+
+// Workgroups of a product and, an XCD's share of the tiles that run at a time being
+// `super` m-tiles deep, as square as it goes, so that its L2 takes in the fewest rows of
+// both operands (256 x 4096 x 4096 21.8 -> 14.3 us against rows of tiles), 4 at most
+// (8192^3: 5 822-869, 4 784-824); groups do not share their weights, and dw of
+// short groups is all stores, of whole rows (512 groups of 80 rows: 5 567, 1 542).
+template <class C>
+int64_t grid_of(LinearMode mode, const LinearArgs& a, int& super) {
+  const int64_t tn = ((mode == kLinForward ? a.N : a.K) + C::BN - 1) / C::BN;
+  const int64_t tm = mode == kLinDw ? (int64_t)a.G * ((a.N + C::BM - 1) / C::BM) : max_tiles(a.rows, a.G, C::BM);
+  const int64_t at_once = tm * tn < 256 * C::WG_PER_CU ? tm * tn : 256 * C::WG_PER_CU;
+  const int64_t of_group = mode == kLinDw ? (a.N + C::BM - 1) / C::BM : (group_mean(a) + C::BM - 1) / C::BM;
+  super = 1;
+  while (super < 4 && super < of_group && 8 * (super + 1) * (super + 1) <= at_once) ++super;
+  if (mode == kLinDw && group_mean(a) <= 256 && a.G > 1) super = 1;
+  return tm * tn;
+}
+
+template <class C>
+hipError_t launch(LinearMode mode, Job j, hipStream_t s) {
+  const dim3 grid((uint32_t)(j.sums + grid_of<C>(mode, j.a, j.super[0])));
+  if (mode == kLinForward) linear_tiles_kernel<kLinForward, -1, C><<<grid, C::NT, 0, s>>>(j);
+  else if (mode == kLinDx) linear_tiles_kernel<kLinDx, -1, C><<<grid, C::NT, 0, s>>>(j);
+  else linear_tiles_kernel<kLinDw, -1, C><<<grid, C::NT, 0, s>>>(j);
+  return hipGetLastError();
+}
+
+// dx and dw of a small product side by side, `first` first.
+template <class C>
+hipError_t launch_both(LinearMode first, Job j, hipStream_t s) {
+  const int64_t n = j.sums + grid_of<C>(first, j.a, j.super[0]);
+  j.second = (int)((n + 7) / 8 * 8);  // its first workgroup on XCD 0 too
+  const LinearMode other = first == kLinDx ? kLinDw : kLinDx;
+  const dim3 grid((uint32_t)(j.second + grid_of<C>(other, j.a, j.super[1])));
+  if (first == kLinDx) linear_tiles_kernel<kLinDx, kLinDw, C><<<grid, C::NT, 0, s>>>(j);
+  else linear_tiles_kernel<kLinDw, kLinDx, C><<<grid, C::NT, 0, s>>>(j);
+  return hipGetLastError();
+}
+
+template <bool F32>
+hipError_t launch_one(LinearMode mode, const Job& j, hipStream_t s) {
+  using X = Tiles<F32>;
+  switch (choose(mode, j.a, F32)) {
+    case kBig: return launch<typename X::Big>(mode, j, s);
+    case kMid: return launch<typename X::Mid>(mode, j, s);
+    case kMidOnce: return launch<typename X::MidOnce>(mode, j, s);
+    case kDeep: return launch<typename X::Deep>(mode, j, s);
+    case kShort: return launch<typename X::Short>(mode, j, s);
+    case kSmallOnce: return launch<typename X::SmallOnce>(mode, j, s);
+    default: return launch<typename X::Small>(mode, j, s);
+  }
+}
+
+template <bool F32>
+hipError_t launch_back(const LinearArgs& a, const void* dz, const void* w, const void* x, void* dx, void* dw,
+                       const LinearSums& sums, hipStream_t s) {
+  Job j{};
+  j.a = a;
+  j.p = dz;
+  j.partial = sums.partial;
+  j.dbias = sums.dbias;
+  j.n = sums.n;
+  j.splits = sums.splits;
+  j.sums = (sums.n + 255) / 256;
+  j.sums = (j.sums + 7) / 8 * 8;  // the first tile on XCD 0
+  // Small products side by side in one launch (1000 x 1416 x 2056 with its dz: 54.0 -> 34.5 us).
+  if (dx && dw) {
+    const Choice cx = choose(kLinDx, a, F32), cw = choose(kLinDw, a, F32);
+    if ((cx == kSmall || cx == kDeep) && (cw == kSmall || cw == kDeep)) {
+      // the longer contraction first
+      const bool x_first = a.N >= group_mean(a);
+      j.q[0] = x_first ? w : x;
+      j.q[1] = x_first ? x : w;
+      j.out[0] = x_first ? dx : dw;
+      j.out[1] = x_first ? dw : dx;
+      const LinearMode first = x_first ? kLinDx : kLinDw;
+      if (cx == kSmall && cw == kSmall) return launch_both<typename Tiles<F32>::Small>(first, j, s);
+      return launch_both<typename Tiles<F32>::Deep>(first, j, s);
+    }
+  }
+  hipError_t e = hipSuccess;
+  if (dx) {
+    j.q[0] = w;
+    j.out[0] = dx;
+    e = launch_one<F32>(kLinDx, j, s);
+    j.sums = 0;
+  }
+  if (dw && e == hipSuccess) {
+    j.q[0] = x;
+    j.out[0] = dw;
+    e = launch_one<F32>(kLinDw, j, s);
+  }
+  return e;
+}
+
+}  // namespace
+
+hipError_t launch_linear_tiles(const LinearArgs& a, bool f32, hipStream_t s) {
+  Job j{};
+  j.a = a;
+  j.p = a.x;
+  j.q[0] = a.w;
+  j.out[0] = a.y;
+  return f32 ? launch_one<true>(kLinForward, j, s) : launch_one<false>(kLinForward, j, s);
+}
+
+hipError_t launch_linear_back_tiles(const LinearArgs& a, bool f32, const void* dz, const void* w, const void* x,
+                                    void* dx, void* dw, const LinearSums& sums, hipStream_t s) {
+  return f32 ? launch_back<true>(a, dz, w, x, dx, dw, sums, s) : launch_back<false>(a, dz, w, x, dx, dw, sums, s);
 }
 
 }  // namespace moe
