@@ -97,7 +97,7 @@ hipError_t launch_linear(const LinearArgs& a, bool f32, hipStream_t s) {
   // (a row of 8192 x 2048: 7.9 us, 64-row tiles 20.1); more of them keep the chip busy in
   // tiles, which read whole 64-row pieces (ten groups of 2560 x 640: 10.2; 13.5).
   const int64_t few = (int64_t)(a.G < a.rows ? a.G : a.rows) * ((a.N + 15) / 16);
-  if (!f32 && a.rows <= 16 * (int64_t)a.G && few <= 256) return launch_linear_few(a, s);
+  if (a.rows <= 16 * (int64_t)a.G && few <= 256) return launch_linear_few(a, f32, s);
   return launch_linear_tiles(a, f32, s);
 }
 

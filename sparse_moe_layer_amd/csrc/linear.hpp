@@ -153,8 +153,8 @@ struct TileMap {
 // m-tiles of bm rows over all groups, at most
 inline int max_tiles(int rows, int G, int bm) { return rows / bm + (G < rows ? G : rows); }
 
-// Forward for groups of at most 16 rows, bf16.
-hipError_t launch_linear_few(const LinearArgs& a, hipStream_t s);
+// Forward for groups of at most 16 rows.
+hipError_t launch_linear_few(const LinearArgs& a, bool f32, hipStream_t s);
 
 // Sums of the dbias partials: n columns, `splits` each; n == 0: none.
 struct LinearSums {

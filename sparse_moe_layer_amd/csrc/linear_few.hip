@@ -1,11 +1,13 @@
 // The forward product for groups of at most 16 rows (single tokens, decode batches):
 //   z[r][n] = sum_k x[r][k] W_g[n][k]
 // bound by reading W_g once.  A workgroup has 16 rows of W (columns of y) and up to
-// 16 rows of x; its waves take every kWaves-th 64 values of K, so that all of them
+// 16 rows of x; its waves take every kWaves-th 128 bytes of K, so that all of them
 // stream, and add their sums through LDS.  Both operands come by direct loads (8 rows
 // x 128 bytes each: whole lines, where fragments loaded straight into registers take
 // 16 half lines a load) into LDS that only the wave itself uses, kAhead pieces in flight.
 #include "linear.hpp"
+
+#include <type_traits>
 
 namespace moe {
 namespace {
@@ -13,20 +15,23 @@ namespace {
 constexpr int kWaves = 8, kAhead = 4;
 constexpr int kFlags = 0x00020000;          // raw 32-bit buffer access
 constexpr uint32_t kNowhere = 0xFFFFFFF0u;  // past every buffer: a load writes zeros
-constexpr int kPiece = 16 * 64;             // values of an operand's piece
+constexpr int kPiece = 16 * 128;            // bytes of an operand's piece
 
 template <bool ONCE>
-__device__ __forceinline__ void dma16(const void* base, uint32_t records, uint32_t off, bf16* l) {
+__device__ __forceinline__ void dma16(const void* base, uint32_t records, uint32_t off, char* l) {
   const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, records, kFlags);
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)l, 16, off, 0, 0, ONCE ? 2 : 0);
 }
 
+template <bool F32>
 __global__ __launch_bounds__(kWaves * 64, 2) void linear_few_kernel(LinearArgs a) {
+  using T = typename std::conditional<F32, float, bf16>::type;
+  constexpr int ESZ = sizeof(T), CE = 16 / ESZ, BK = 128 / ESZ;  // values of a chunk, of a row's piece
   // separate arrays: a read of one does not wait for loads into another
-  __shared__ __attribute__((aligned(1024))) bf16 r0[kWaves * 2 * kPiece];
-  __shared__ __attribute__((aligned(1024))) bf16 r1[kWaves * 2 * kPiece];
-  __shared__ __attribute__((aligned(1024))) bf16 r2[kWaves * 2 * kPiece];
-  __shared__ __attribute__((aligned(1024))) bf16 r3[kWaves * 2 * kPiece];
+  __shared__ __attribute__((aligned(1024))) char r0[kWaves * 2 * kPiece];
+  __shared__ __attribute__((aligned(1024))) char r1[kWaves * 2 * kPiece];
+  __shared__ __attribute__((aligned(1024))) char r2[kWaves * 2 * kPiece];
+  __shared__ __attribute__((aligned(1024))) char r3[kWaves * 2 * kPiece];
   static_assert(kAhead == 4, "four arrays");
   __shared__ float red[kWaves][16][17];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -37,44 +42,52 @@ __global__ __launch_bounds__(kWaves * 64, 2) void linear_few_kernel(LinearArgs a
   const MTile t = map.find(mt);
   const int64_t K = a.K;
   const int rows = min(t.end - t.row, 16), cols = min(a.N - n0, 16);
-  const bf16* w = static_cast<const bf16*>(a.w) + t.g * a.w_stride + n0 * K;
-  const bf16* x = static_cast<const bf16*>(a.x) + t.row * K;
-  const uint32_t wb = (uint32_t)(cols * K * 2), xb = (uint32_t)(rows * K * 2);  // K <= 2^17
+  const T* w = static_cast<const T*>(a.w) + t.g * a.w_stride + n0 * K;
+  const T* x = static_cast<const T*>(a.x) + t.row * K;
+  const uint32_t wb = (uint32_t)(cols * K * ESZ), xb = (uint32_t)(rows * K * ESZ);  // K <= 2^17
   // load h of a piece: rows 8 h .. + 8, chunk c of row r at c ^ ((r >> 1) & 7)
   int kc[2];
   uint32_t at[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int r = 8 * h + (lane >> 3);
-    kc[h] = ((lane & 7) ^ ((r >> 1) & 7)) * 8;
-    at[h] = (uint32_t)(r * K + kc[h]) * 2;
+    kc[h] = ((lane & 7) ^ ((r >> 1) & 7)) * CE;
+    at[h] = (uint32_t)(r * K + kc[h]) * ESZ;
   }
-  auto load = [&](bf16* l, int p) {
+  auto load = [&](char* l, int p) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t off = p * 64 + kc[h] < a.K ? at[h] + p * 128 : kNowhere;
-      dma16<true>(w, wb, off, l + h * 512);
-      dma16<false>(x, xb, off, l + kPiece + h * 512);
+      const uint32_t off = p * BK + kc[h] < a.K ? at[h] + p * 128 : kNowhere;
+      dma16<true>(w, wb, off, l + h * 1024);
+      dma16<false>(x, xb, off, l + kPiece + h * 1024);
     }
   };
   const int fr = lane & 15;
-  const int o0 = fr * 64 + (((lane >> 4) ^ ((fr >> 1) & 7)) << 3), o1 = fr * 64 + (((4 + (lane >> 4)) ^ ((fr >> 1) & 7)) << 3);
+  const int o0 = fr * 128 + (((lane >> 4) ^ ((fr >> 1) & 7)) << 4), o1 = fr * 128 + (((4 + (lane >> 4)) ^ ((fr >> 1) & 7)) << 4);
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  const int mine = wave * 2 * kPiece, pieces = (a.K + 63) / 64;
+  const int mine = wave * 2 * kPiece, pieces = (a.K + BK - 1) / BK;
   load(r0 + mine, wave);
   load(r1 + mine, wave + kWaves);
   load(r2 + mine, wave + 2 * kWaves);
   load(r3 + mine, wave + 3 * kWaves);
-  auto step = [&](bf16* l, int next) {
+  auto step = [&](char* l, int next) {
     __builtin_amdgcn_s_waitcnt(0xF70 | 4 * (kAhead - 1));  // this piece's four loads have landed
     asm volatile("" ::: "memory");
-    const bf16x8 f0 = *reinterpret_cast<const bf16x8*>(l + o0), g0 = *reinterpret_cast<const bf16x8*>(l + kPiece + o0);
-    const bf16x8 f1 = *reinterpret_cast<const bf16x8*>(l + o1), g1 = *reinterpret_cast<const bf16x8*>(l + kPiece + o1);
+    using F = typename std::conditional<F32, f32x4, bf16x8>::type;
+    const F f0 = *reinterpret_cast<const F*>(l + o0), g0 = *reinterpret_cast<const F*>(l + kPiece + o0);
+    const F f1 = *reinterpret_cast<const F*>(l + o1), g1 = *reinterpret_cast<const F*>(l + kPiece + o1);
     __builtin_amdgcn_s_waitcnt(0xC07F);  // and are read, before the next ones overwrite them
     asm volatile("" ::: "memory");
     load(l, next);
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f0, g0, acc, 0, 0, 0);
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f1, g1, acc, 0, 0, 0);
+    if constexpr (F32) {  // K 16 j + 4 h + e over the four h of a wave, for e in 0 .. 3
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(f0[e], g0[e], acc, 0, 0, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(f1[e], g1[e], acc, 0, 0, 0);
+    } else {
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f0, g0, acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f1, g1, acc, 0, 0, 0);
+    }
   };
   for (int p = wave; p < pieces; p += kAhead * kWaves) {
     step(r0 + mine, p + kAhead * kWaves);
@@ -93,20 +106,21 @@ __global__ __launch_bounds__(kWaves * 64, 2) void linear_few_kernel(LinearArgs a
 #pragma unroll
   for (int i = 0; i < kWaves; ++i) z += red[i][r][c];
   const int64_t i = (int64_t)(t.row + r) * a.N + n0 + c;
-  if (a.bias) z += bf2f(static_cast<const bf16*>(a.bias)[(int64_t)t.g * a.N + n0 + c]);
-  if (a.z) static_cast<bf16*>(a.z)[i] = f2bf(z);
+  if (a.bias) z += (float)static_cast<const T*>(a.bias)[(int64_t)t.g * a.N + n0 + c];
+  if (a.z) static_cast<T*>(a.z)[i] = (T)z;
   float y[1] = {z};
-  activate<true>(a.act, y);
-  if (a.mul) y[0] *= bf2f(static_cast<const bf16*>(a.mul)[i]);
-  if (a.resid) y[0] += bf2f(static_cast<const bf16*>(a.resid)[i]);
-  static_cast<bf16*>(a.y)[i] = f2bf(y[0]);
+  activate<!F32>(a.act, y);
+  if (a.mul) y[0] *= (float)static_cast<const T*>(a.mul)[i];
+  if (a.resid) y[0] += (float)static_cast<const T*>(a.resid)[i];
+  static_cast<T*>(a.y)[i] = (T)y[0];
 }
 
 }  // namespace
 
-hipError_t launch_linear_few(const LinearArgs& a, hipStream_t s) {
+hipError_t launch_linear_few(const LinearArgs& a, bool f32, hipStream_t s) {
   const int64_t grid = (int64_t)max_tiles(a.rows, a.G, 16) * ((a.N + 15) / 16);
-  linear_few_kernel<<<dim3((uint32_t)grid), kWaves * 64, 0, s>>>(a);
+  if (f32) linear_few_kernel<true><<<dim3((uint32_t)grid), kWaves * 64, 0, s>>>(a);
+  else linear_few_kernel<false><<<dim3((uint32_t)grid), kWaves * 64, 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -11,25 +11,29 @@
 namespace moe {
 namespace {
 
-// F32_: fp32 tensors.  KB: bytes of a row's K step in a stage.
-template <bool F32_, int BM_, int BN_, int WM_, int WN_, int S_, int KB_, int WG_PER_CU_, bool W_ONCE_ = false>
+// F32_: fp32 tensors.  KB: bytes of a row's K step in a stage.  WK: waves that share
+// a step's sub-steps (each has a sum of the whole tile) instead of the tile.
+template <bool F32_, int BM_, int BN_, int WM_, int WN_, int S_, int KB_, int WG_PER_CU_, bool W_ONCE_ = false,
+          int WK_ = 1>
 struct Tile {
+  static constexpr int WK = WK_;
   static constexpr bool F32 = F32_;
   using T = typename std::conditional<F32, float, bf16>::type;
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, KB = KB_;
   static constexpr int BK = KB / (int)sizeof(T);                   // K step
   static constexpr int CE = 16 / (int)sizeof(T);                   // values of a 16-byte chunk
-  static constexpr int KS = KB / 32;                               // sub-steps of two chunks a row
+  static constexpr int KS = KB / 32 / WK;                          // a wave's sub-steps, of two chunks a row
   static constexpr int PER_SUB = F32 ? 4 : 1;                      // matrix instructions of a block and sub-step
   static constexpr bool W_ONCE = W_ONCE_;                          // each weight is read by one tile
-  static constexpr int NW = WM * WN, NT = 64 * NW;
+  static constexpr int NW = WM * WN * WK, NT = 64 * NW;
   static constexpr int MI = BM / (32 * WM), NJ = BN / (32 * WN);   // 32 x 32 blocks of a wave
   static constexpr int LA = BM * KB / 1024 / NW, LB = BN * KB / 1024 / NW;  // 1 KB direct loads a wave and stage
   static constexpr int L = LA + LB;
   static constexpr int STAGE = (BM + BN) * KB;                     // bytes
   static constexpr int WG_PER_CU = WG_PER_CU_;
   static_assert(NT == 256, "the search for tiles takes 256 threads");
-  static_assert(WM == 2 && BM == BN && (KB == 64 || KB == 128), "tiling");
+  static_assert((WM == 2 || WM == 1) && BM == BN && (KB == 64 || KB == 128), "tiling");
+  static_assert(WK == 1 || (WM * WN == 1 && MI * NJ == 1 && KS == 1), "K over the waves: one block");
   static_assert(MI >= 1 && NJ >= 1 && LA >= 1 && LB >= 1 && L * (S - 1) < 64, "tiling");
   static_assert(S * STAGE * WG_PER_CU <= 160 * 1024, "LDS");
 };
@@ -46,6 +50,13 @@ __device__ __forceinline__ void block_sync() {
   asm volatile("" ::: "memory");
 }
 
+// The same after this wave's LDS accesses are done (the barrier alone does not wait for
+// them).
+__device__ __forceinline__ void lds_sync() {
+  __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(63));
+  block_sync();
+}
+
 // A 16-byte direct load from base + voff + soff to LDS (voff the lane's, soff the
 // wave's); past `records` bytes it writes zeros.  once: non-temporal.
 __device__ __forceinline__ void dma16(const char* base, uint32_t records, uint32_t voff, uint32_t soff, char* l,
@@ -60,10 +71,11 @@ __device__ __forceinline__ void dma16(const char* base, uint32_t records, uint32
 template <int KB>
 __device__ __forceinline__ int swz(int r) { return KB == 64 ? (r >> 2) & 3 : (r >> 1) & 7; }
 //  Rows across K (R values): bf16, the transposing reads of four rows k .. k + 3 take 64
-//  bytes each; fp32, a wave reads 128 bytes of rows k and k + 4.
+//  bytes each; fp32, a wave reads 128 bytes of rows k and k + 4.  (A row of 32 values
+//  has no other place for them.)
 template <bool F32, int R>
 __device__ __forceinline__ int swz_t(int k) {
-  return F32 ? (k & 4) << 1 : R == 64 ? (k & 2) << 1 : (k & 3) << 2;
+  return R == 32 ? 0 : F32 ? (k & 4) << 1 : R == 64 ? (k & 2) << 1 : (k & 3) << 2;
 }
 
 // One operand's tile of R rows (or, contracted along its columns, R columns) as
@@ -121,20 +133,21 @@ template <class C, int R, bool T, int NB, int STEP>
 struct Frags {
   using F = typename std::conditional<C::F32, f32x4, bf16x8>::type;
   int o[T ? NB : C::KS];
-  __device__ __forceinline__ Frags(int first, int lane) {
+  // ks0: the wave's first sub-step
+  __device__ __forceinline__ Frags(int first, int ks0, int lane) {
     if constexpr (!T) {
 #pragma unroll
       for (int ks = 0; ks < C::KS; ++ks) {
         const int row = first * 32 + (lane & 31);
-        o[ks] = row * C::KB + (((ks * 2 + (lane >> 5)) ^ swz<C::KB>(row)) << 4);
+        o[ks] = row * C::KB + ((((ks0 + ks) * 2 + (lane >> 5)) ^ swz<C::KB>(row)) << 4);
       }
     } else if constexpr (C::F32) {
-      const int k = 4 * (lane >> 5);
+      const int k = 8 * ks0 + 4 * (lane >> 5);  // the swizzle is that of k & 7
 #pragma unroll
       for (int i = 0; i < NB; ++i)
         o[i] = k * R * 4 + ((((first + i * STEP) * 8 + ((lane & 31) >> 2)) ^ swz_t<true, R>(k)) << 4) + 4 * (lane & 3);
     } else {
-      const int k = 8 * (lane >> 5) + ((lane & 15) >> 2);  // and k + 4, of the same swizzle
+      const int k = 16 * ks0 + 8 * (lane >> 5) + ((lane & 15) >> 2);  // and k + 4, of the same swizzle
 #pragma unroll
       for (int i = 0; i < NB; ++i)
         o[i] = k * R * 2 + ((((first + i * STEP) * 4 + ((lane & 31) >> 4) * 2 + ((lane & 3) >> 1)) ^ swz_t<false, R>(k)) << 4) +
@@ -196,7 +209,7 @@ __device__ __forceinline__ void run_tile(const LinearArgs& a, const typename C::
   constexpr bool TA = MODE == kLinDw, TB = MODE != kLinForward;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / C::WN, wn = wave % C::WN;
+  const int wk = C::WK > 1 ? wave : 0, wm = C::WK > 1 ? 0 : wave / C::WN, wn = C::WK > 1 ? 0 : wave % C::WN;
 
   // ---- which tile: XCD x (workgroup i runs on XCD i % 8) takes a run of
   // consecutive tiles, so that its L2 holds what they share ----
@@ -247,8 +260,8 @@ __device__ __forceinline__ void run_tile(const LinearArgs& a, const typename C::
   }
   const Operand<C, C::BM, TA> oa(pa, la, ba, lane, wave);
   const Operand<C, C::BN, TB> ob(pb, lb, bb, lane, wave);
-  const Frags<C, C::BM, TA, C::MI, C::WM> fa(wm, lane);  // M-blocks wm, wm + WM, ..
-  const Frags<C, C::BN, TB, C::NJ, 1> fb(wn * C::NJ, lane);
+  const Frags<C, C::BM, TA, C::MI, C::WM> fa(wm, wk * C::KS, lane);  // M-blocks wm, wm + WM, ..
+  const Frags<C, C::BN, TB, C::NJ, 1> fb(wn * C::NJ, wk * C::KS, lane);
   const int nk = (kn + C::BK - 1) / C::BK;
   auto issue = [&](char* st, int step) {
     oa.issue(st, step * C::BK, kn, wave);
@@ -304,20 +317,20 @@ __device__ __forceinline__ void run_tile(const LinearArgs& a, const typename C::
   // fp32, so that z is rounded once), so that a thread has 8 values side by side.  A lane
   // holds row lane % 32 of a block and columns 8 q + 4 (lane / 32) .. + 4; 16-byte chunk c
   // of row r sits at c ^ (r & 15) (& 7 in a row of 8), so 16 rows' writes cover the banks. ----
-  constexpr bool WIDE = MODE == kLinForward || C::F32;
+  constexpr bool WIDE = MODE == kLinForward || C::F32 || C::WK > 1;
   constexpr int ROW = C::BN * (WIDE ? 4 : 2), PER = C::STAGE / (32 * ROW);  // bytes of a row, blocks a stage holds
   constexpr int BPP = C::BM / 32 < C::S * PER ? C::BM / 32 : C::S * PER;    // blocks of a pass
-  static_assert(C::BM / 32 % BPP == 0 && BPP % C::WM == 0, "whole passes");
+  static_assert(C::BM / 32 % BPP == 0 && BPP % C::WM == 0 && C::WK <= 2 * PER, "whole passes");
   constexpr int CPR = C::BN / 8;  // threads a row
   constexpr int SWZ = ROW >= 256 ? 15 : 7;
   auto block = [&](int b) { return stg[b / PER] + b % PER * 32 * ROW; };
 #pragma unroll
   for (int pass = 0; pass < C::BM / 32 / BPP; ++pass) {
-    if (pass) block_sync();
+    if (pass) lds_sync();
 #pragma unroll
     for (int i = 0; i < BPP / C::WM; ++i) {
       const int ii = pass * (BPP / C::WM) + i, r = lane & 31;
-      char* f = (wm ? block(i * C::WM + 1) : block(i * C::WM)) + r * ROW;
+      char* f = (C::WK > 1 ? (wk < PER ? stg[0] : stg[1]) + wk % PER * 32 * ROW : wm ? block(i * C::WM + C::WM - 1) : block(i * C::WM)) + r * ROW;
 #pragma unroll
       for (int j = 0; j < C::NJ; ++j)
 #pragma unroll
@@ -333,7 +346,7 @@ __device__ __forceinline__ void run_tile(const LinearArgs& a, const typename C::
           }
         }
     }
-    block_sync();
+    lds_sync();
 #pragma unroll
     for (int b = 0; b < BPP; ++b) {
       const char* f = block(b);
@@ -357,7 +370,10 @@ __device__ __forceinline__ void run_tile(const LinearArgs& a, const typename C::
             float z[W];
 #pragma unroll
             for (int k = 0; k < W; k += 4) {
-              const f32x4 v = *reinterpret_cast<const f32x4*>(fr + ((((c >> 2) + h + k / 4) ^ (r & SWZ)) << 4));
+              f32x4 v = *reinterpret_cast<const f32x4*>(fr + ((((c >> 2) + h + k / 4) ^ (r & SWZ)) << 4));
+#pragma unroll
+              for (int w = 1; w < C::WK; ++w)
+                v += *reinterpret_cast<const f32x4*>(block(w) + r * ROW + ((((c >> 2) + h + k / 4) ^ (r & SWZ)) << 4));
 #pragma unroll
               for (int l = 0; l < 4; ++l) z[k + l] = v[l];
             }
@@ -436,8 +452,9 @@ struct Tiles {
   using Short = Tile<F32, 128, 128, 2, 2, 2, 64, 4>;
   using Small = Tile<F32, 64, 64, 2, 2, 4, 128, 2>;
   using SmallOnce = Tile<F32, 64, 64, 2, 2, 4, 128, 2, true>;
+  using Tiny = Tile<F32, 32, 32, 1, 1, 4, 128, 4, false, 4>;
 };
-enum Choice { kBig, kMid, kMidOnce, kDeep, kShort, kSmall, kSmallOnce };
+enum Choice { kBig, kMid, kMidOnce, kDeep, kShort, kSmall, kSmallOnce, kTiny };
 
 // Rows of a group on average, and the tiles of edge b that a product takes about.
 int64_t group_mean(const LinearArgs& a) { return a.rows / a.G; }
@@ -450,16 +467,37 @@ int64_t tiles_about(LinearMode mode, const LinearArgs& a, int b) {
 Choice choose(LinearMode mode, const LinearArgs& a, bool f32) {
   const int64_t r = group_mean(a), touched = a.rows < a.G ? a.rows : a.G;
   const int64_t t128 = tiles_about(mode, a, 128);
+  if (f32) {
+    // The matrix rate bounds every size of tile, so the least work of the busiest compute
+    // unit decides, the smaller tiles' overhead counted in (forward, us, tiles of 32, 64 and
+    // 128 rows: 300 x 1024 x 1024 12.2, 18.9, 45; 2000 x 2048 x 1024 76.7, 65.5, 118;
+    // 8000 x 512 x 1024 85.2, 71.7, 68.6; the library's product 20.5, 64.2, 66.6).
+    struct Size {
+      int b;
+      double cost;
+      Choice c;
+    };
+    const Size sizes[] = {{32, 1.2, kTiny}, {64, 1.05, kSmall}, {128, 1.0, kMid}, {256, 1.0, kBig}};
+    Choice best = kTiny;
+    double least = 1e30;
+    for (const Size& z : sizes) {
+      const double work = (double)((tiles_about(mode, a, z.b) + 255) / 256) * z.b * z.b * z.cost;
+      if (work < least) least = work, best = z.c;
+    }
+    return best;
+  }
   // us, forward unless named, of one side and the other:
   // 256-row tiles once they fill three quarters of the chip (8192 x 2560 x 8192: 283; 128-row 391), dw
   // also with a contraction long enough for their pipeline (512 experts of 80 rows: 645, short 497);
   if (r >= (mode == kLinDw ? 1024 : 192) && tiles_about(mode, a, 256) >= 192) return kBig;
+  // 32-row tiles with K over the waves where even 64-row ones are few (100 x 8192 x 512: 11.9; 19.7);
   // 64-row tiles where 128-row ones would leave most of the chip idle (256 x 4096 x 4096: 21.6; 25.7),
   // or groups of a few rows, whose weights they stream in more and smaller pieces (512 groups of 4:
   // 278; 291.  dx, whose rows of W they read in 128-byte pieces, only as long as there are few:
   // 38 groups of a row 24.8; 28.3, 139 groups 100; 87), weights that no cache holds anyway
   // non-temporally (365 groups of a row or two 185; 202, 38 groups 25.1; 21.7);
-  if (mode == kLinForward && r <= 64 && touched * a.N * a.K > (f32 ? 50000000 : 100000000)) return kSmallOnce;
+  if (tiles_about(mode, a, 64) <= 64) return kTiny;
+  if (mode == kLinForward && r <= 64 && touched * a.N * a.K > 100000000) return kSmallOnce;
   if (t128 < 96 || (mode == kLinForward && r <= 64) || (mode == kLinDx && r <= 64 && t128 <= 1024)) return kSmall;
   // a round of 128-row tiles with four stages (2000 x 2048 x 2048: 19.6; two workgroups of two stages 26.3);
   if (t128 <= 256) return kDeep;
@@ -511,15 +549,17 @@ hipError_t launch_both(LinearMode first, Job j, hipStream_t s) {
 template <bool F32>
 hipError_t launch_one(LinearMode mode, const Job& j, hipStream_t s) {
   using X = Tiles<F32>;
-  switch (choose(mode, j.a, F32)) {
-    case kBig: return launch<typename X::Big>(mode, j, s);
-    case kMid: return launch<typename X::Mid>(mode, j, s);
-    case kMidOnce: return launch<typename X::MidOnce>(mode, j, s);
-    case kDeep: return launch<typename X::Deep>(mode, j, s);
-    case kShort: return launch<typename X::Short>(mode, j, s);
-    case kSmallOnce: return launch<typename X::SmallOnce>(mode, j, s);
-    default: return launch<typename X::Small>(mode, j, s);
+  const Choice c = choose(mode, j.a, F32);
+  if constexpr (!F32) {  // fp32 takes the others alone
+    if (c == kMidOnce) return launch<typename X::MidOnce>(mode, j, s);
+    if (c == kDeep) return launch<typename X::Deep>(mode, j, s);
+    if (c == kShort) return launch<typename X::Short>(mode, j, s);
+    if (c == kSmallOnce) return launch<typename X::SmallOnce>(mode, j, s);
   }
+  if (c == kBig) return launch<typename X::Big>(mode, j, s);
+  if (c == kMid) return launch<typename X::Mid>(mode, j, s);
+  if (c == kSmall) return launch<typename X::Small>(mode, j, s);
+  return launch<typename X::Tiny>(mode, j, s);
 }
 
 template <bool F32>
@@ -536,8 +576,8 @@ hipError_t launch_back(const LinearArgs& a, const void* dz, const void* w, const
   j.sums = (j.sums + 7) / 8 * 8;  // the first tile on XCD 0
   // Small products side by side in one launch (1000 x 1416 x 2056 with its dz: 54.0 -> 34.5 us).
   if (dx && dw) {
-    const Choice cx = choose(kLinDx, a, F32), cw = choose(kLinDw, a, F32);
-    if ((cx == kSmall || cx == kDeep) && (cw == kSmall || cw == kDeep)) {
+    const Choice c = choose(kLinDx, a, F32);
+    if ((c == kTiny || c == kSmall || c == kDeep) && choose(kLinDw, a, F32) == c) {
       // the longer contraction first
       const bool x_first = a.N >= group_mean(a);
       j.q[0] = x_first ? w : x;
@@ -545,8 +585,10 @@ hipError_t launch_back(const LinearArgs& a, const void* dz, const void* w, const
       j.out[0] = x_first ? dx : dw;
       j.out[1] = x_first ? dw : dx;
       const LinearMode first = x_first ? kLinDx : kLinDw;
-      if (cx == kSmall && cw == kSmall) return launch_both<typename Tiles<F32>::Small>(first, j, s);
-      return launch_both<typename Tiles<F32>::Deep>(first, j, s);
+      if (c == kTiny) return launch_both<typename Tiles<F32>::Tiny>(first, j, s);
+      if constexpr (!F32)
+        if (c == kDeep) return launch_both<typename Tiles<F32>::Deep>(first, j, s);
+      return launch_both<typename Tiles<F32>::Small>(first, j, s);
     }
   }
   hipError_t e = hipSuccess;
