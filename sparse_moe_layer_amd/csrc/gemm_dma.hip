@@ -97,6 +97,13 @@ __device__ __forceinline__ void block_sync() {
   asm volatile("" ::: "memory");
 }
 
+// The same once this wave's LDS accesses are done: where other waves read what it
+// wrote (the barrier alone does not wait for them).
+__device__ __forceinline__ void lds_sync() {
+  __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(63));
+  block_sync();
+}
+
 // Chunk c of row r: 4 chunks per 64-byte row XOR (r >> 2) & 3, or 8 per
 // 128-byte row XOR (r >> 1) & 7 (16 rows of one chunk hit 16 bank groups).
 template <int BK>
@@ -391,8 +398,9 @@ __device__ __forceinline__ void mainloop(f32x16 (&acc)[C::MI][C::NJ], bf16* cons
 #pragma unroll
   for (int j = 0; j < C::NJ; ++j) cy.b[j] = bf16x8{};
   // every wave's loads (vmcnt(0) before the call) and LDS reads of the
-  // previous tile are finished before its buffers are refilled
-  block_sync();
+  // previous tile are finished before its buffers are refilled, and its part
+  // of the fp8 scale table is written before any wave reads it
+  lds_sync();
 #pragma unroll
   for (int st = 0; st < C::S - 1; ++st) {
     const uint32_t k0 = (uint32_t)st * C::BK;
@@ -610,7 +618,7 @@ __device__ __forceinline__ void run_tile(const FfnArgs& f, int mt, int nt, bf16*
       }
     }
   }
-  block_sync();
+  lds_sync();
   bf16* obase;
   int ld;
   if (MODE == 1) {
