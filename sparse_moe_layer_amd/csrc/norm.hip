@@ -19,19 +19,25 @@ namespace {
 
 constexpr int kMaxWaves = 16;
 
-// Sums of P values over the workgroup, in every thread.  red: [kMaxWaves][P]
-// (one use per barrier interval: callers alternate two).
+// Sums of P values over the waves [first, first + nw) of the workgroup, in each of their
+// threads.  red: [kMaxWaves][P] (one use per barrier interval: callers alternate two).
 template <int P>
-__device__ __forceinline__ void block_sums(float (&a)[P], float* red, int lane, int wave, int nw) {
+__device__ __forceinline__ void block_sums(float (&a)[P], float* red, int lane, int wave, int first, int nw) {
   const float s = wave_sums<P>(a, lane);
   constexpr int kStep = 64 / P;
   if (lane % kStep == 0) red[wave * P + lane / kStep] = s;
   __syncthreads();
+  // lane l takes value l % P of the waves l / P, l / P + kStep ..; then over the lanes
+  float v = 0.f;
 #pragma unroll
-  for (int i = 0; i < P; ++i) a[i] = 0.f;
-  for (int w = 0; w < nw; ++w)
+  for (int w = 0; w < kMaxWaves; w += kStep) {
+    const int at = w + lane / P;
+    if (w < nw) v += at < nw ? red[(first + at) * P + lane % P] : 0.f;
+  }
 #pragma unroll
-    for (int i = 0; i < P; ++i) a[i] += red[w * P + i];
+  for (int o = P; o < 64; o <<= 1) v += __shfl_xor(v, o, kWave);
+#pragma unroll
+  for (int i = 0; i < P; ++i) a[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), i));
 }
 
 template <bool F32, int NCH>
@@ -65,7 +71,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a) {
 #pragma unroll
       for (int e = 0; e < V::N; ++e) ss[0] = fmaf(v[e], v[e], ss[0]);
     }
-    block_sums<1>(ss, red[0], lane, wave, nw);
+    block_sums<1>(ss, red[0], lane, wave, 0, nw);
     rf = 1.f / sqrtf(ss[0] * a.inv_h + a.eps);
   }
   const float gt = a.gate_kind == MOE_GATE_TOKEN ? static_cast<const float*>(a.gate)[t] : 1.f;
@@ -95,7 +101,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a) {
     if (a.resid_out && c < a.nch) st16(static_cast<u32x4*>(a.resid_out) + base + c, V::pack(r[i]));
   }
   if (!a.x) return;
-  block_sums<1>(ss, red[1], lane, wave, nw);
+  block_sums<1>(ss, red[1], lane, wave, 0, nw);
   const float rr = 1.f / sqrtf(ss[0] * a.inv_h + a.eps);
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
@@ -109,169 +115,236 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a) {
   }
 }
 
-// Rows blockIdx.x, blockIdx.x + gridDim.x, ...: NCH chunks a thread as above.
-template <bool F32, int NCH>
-__global__ __launch_bounds__(1024) void norm_backward_kernel(NormBackArgs a) {
+// A workgroup has blockDim.x / tpr rows at a time, tpr threads (whole waves) a row with
+// NCH chunks each; the next rows' loads go out before the present ones' sums.
+// GATE: MOE_GATE_NONE stands for the token's gate too (a factor that is 1 without one).
+template <bool F32, int NCH, int NT, bool POST, int GATE>
+__global__ __launch_bounds__(NT) void norm_backward_kernel(NormBackArgs a, int tpr) {
   using V = Vec<F32>;
-  __shared__ float red[2][kMaxWaves * 4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nw = blockDim.x >> 6;
+  __shared__ float red[2][kMaxWaves * 8];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wpr = tpr >> 6, group = wave / wpr, groups = blockDim.x / tpr;
+  const int me = tid - group * tpr;  // thread of the row
   const u32x4* f = static_cast<const u32x4*>(a.f);
   const u32x4* gate = static_cast<const u32x4*>(a.gate);
   const u32x4* g_post = static_cast<const u32x4*>(a.g_post);
   const u32x4* g_pre = static_cast<const u32x4*>(a.g_pre);
-  float s_post[NCH][V::N] = {}, s_pre[NCH][V::N] = {}, s_gate[NCH][V::N] = {};
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const int64_t base = (int64_t)t * a.nch;
-    u32x4 vd[NCH] = {}, vx[NCH] = {}, vf[NCH] = {}, vr[NCH] = {}, vg[NCH] = {};
+  // sums over a row's P values, in each of its threads
+  auto row_sums = [&](auto& v, float* r) {
+    constexpr int P = sizeof(v) / 4;
+    if (wpr == 1) {
+      const float s = wave_sums<P>(v, lane);
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int c = tid + i * blockDim.x;
-      if (c >= a.nch) continue;
-      if (a.dresid_out) vd[i] = ld16_nt(static_cast<const u32x4*>(a.dresid_out) + base + c);
-      if (a.dx) {
-        vx[i] = ld16_nt(static_cast<const u32x4*>(a.dx) + base + c);
-        vr[i] = ld16_nt(static_cast<const u32x4*>(a.resid_out) + base + c);
-      }
-      if (f) vf[i] = ld16_nt(f + base + c);
-      if (a.gate_kind == MOE_GATE_FULL) vg[i] = ld16_nt(gate + base + c);
-      if (a.gate_kind == MOE_GATE_CHANNEL) vg[i] = ld16(gate + c);
+      for (int i = 0; i < P; ++i) v[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s), i * (64 / P)));
+    } else {
+      block_sums<P>(v, r, lane, wave, group * wpr, wpr);
     }
-    // sums over the row: r'^2, g_pre dx r', f^2
-    float ss[4] = {};
+  };
+  struct Row {
+    u32x4 d[NCH], x[NCH], f[NCH], r[NCH], g[GATE == MOE_GATE_FULL ? NCH : 1];
+    float gt;  // the token's gate
+  };
+  auto load = [&](Row& v, int t) {
+    v.gt = GATE == MOE_GATE_NONE && a.gate && t < a.T ? static_cast<const float*>(a.gate)[t] : 1.f;
+    const int64_t base = (int64_t)t * a.nch;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int c = tid + i * blockDim.x;
-      float x[V::N], r[V::N], fv[V::N], g[V::N] = {};
-      V::unpack(vx[i], x);
-      V::unpack(vr[i], r);
-      V::unpack(vf[i], fv);
-      if (a.dx && c < a.nch) V::unpack(ld16(g_pre + c), g);
+      const int c = me + i * tpr;
+      v.d[i] = v.x[i] = v.f[i] = v.r[i] = u32x4{};
+      if constexpr (GATE == MOE_GATE_FULL) v.g[i] = u32x4{};
+      if (t >= a.T || c >= a.nch) continue;
+      if (a.dresid_out) v.d[i] = ld16_nt(static_cast<const u32x4*>(a.dresid_out) + base + c);
+      if (a.dx) {
+        v.x[i] = ld16_nt(static_cast<const u32x4*>(a.dx) + base + c);
+        v.r[i] = ld16_nt(static_cast<const u32x4*>(a.resid_out) + base + c);
+      }
+      if (f) v.f[i] = ld16_nt(f + base + c);
+      if constexpr (GATE == MOE_GATE_FULL) v.g[i] = ld16_nt(gate + base + c);
+    }
+  };
+  float s_post[POST ? NCH : 1][V::N] = {}, s_pre[NCH][V::N] = {}, s_gate[GATE == MOE_GATE_CHANNEL ? NCH : 1][V::N] = {};
+  // the columns' gains and gate stay in registers: a load of theirs in the loop would wait
+  // for the next rows' ahead of it
+  u32x4 k_pre[NCH], k_post[POST ? NCH : 1], k_gate[GATE == MOE_GATE_CHANNEL ? NCH : 1];
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int c = me + i * tpr;
+    k_pre[i] = a.dx && c < a.nch ? ld16(g_pre + c) : u32x4{};
+    if constexpr (POST) k_post[i] = c < a.nch ? ld16(g_post + c) : u32x4{};
+    if constexpr (GATE == MOE_GATE_CHANNEL) k_gate[i] = c < a.nch ? ld16(gate + c) : u32x4{};
+  }
+  const int step = gridDim.x * groups;
+  constexpr bool AHEAD = NCH < 4;  // registers for two rows
+  Row v;
+  if constexpr (AHEAD) load(v, blockIdx.x * groups + group);
+  // every group runs the same number of rounds: the sums have barriers
+  int round = 0;  // two places for the sums, in turn
+  for (int t0 = blockIdx.x * groups; t0 < a.T; t0 += step, ++round) {
+    const int t = t0 + group;
+    const bool live = t < a.T;
+    const int64_t base = (int64_t)t * a.nch;
+    Row next;
+    if constexpr (AHEAD) load(next, t0 + step + group);
+    else load(v, t);
+    // Sums over the row: r'^2, u r' with u = g_pre dx, f^2, and with q = gate g_post f
+    // (the token's gate left out) q dresid_out, q u, q r': the last three give
+    // sum q dr = s3 + rr s4 - rr mr s5, so one round of sums serves both norms.
+    float ss[8] = {};
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int c = me + i * tpr;
+      float d[V::N], x[V::N], r[V::N], q[V::N], g[V::N];
+      V::unpack(v.x[i], x);
+      V::unpack(v.r[i], r);
+      V::unpack(v.f[i], q);
+      V::unpack(v.d[i], d);
+      V::unpack(k_pre[i], g);
 #pragma unroll
       for (int e = 0; e < V::N; ++e) {
+        x[e] *= g[e];
         ss[0] = fmaf(r[e], r[e], ss[0]);
-        ss[1] = fmaf(g[e] * x[e], r[e], ss[1]);
-        ss[2] = fmaf(fv[e], fv[e], ss[2]);
+        ss[1] = fmaf(x[e], r[e], ss[1]);
+        if constexpr (POST) ss[2] = fmaf(q[e], q[e], ss[2]);
+      }
+      if constexpr (POST) {
+        V::unpack(k_post[i], g);
+#pragma unroll
+        for (int e = 0; e < V::N; ++e) q[e] *= g[e];
+      }
+      if constexpr (GATE != MOE_GATE_NONE && POST) {
+        if constexpr (GATE == MOE_GATE_FULL) V::unpack(v.g[i], g);
+        else V::unpack(k_gate[i], g);
+#pragma unroll
+        for (int e = 0; e < V::N; ++e) q[e] *= g[e];
+      }
+#pragma unroll
+      for (int e = 0; e < V::N; ++e) {
+        if constexpr (POST || GATE == MOE_GATE_NONE) {
+          ss[3] = fmaf(q[e], d[e], ss[3]);
+          ss[4] = fmaf(q[e], x[e], ss[4]);
+          ss[5] = fmaf(q[e], r[e], ss[5]);
+        }
       }
     }
-    block_sums<4>(ss, red[0], lane, wave, nw);
+    row_sums(ss, red[round & 1]);
     const float rr = 1.f / sqrtf(ss[0] * a.inv_h + a.eps);
     const float mr = ss[1] * a.inv_h * rr * rr;
-    const float rf = g_post ? 1.f / sqrtf(ss[2] * a.inv_h + a.eps) : 1.f;
-    const float gt = a.gate_kind == MOE_GATE_TOKEN ? static_cast<const float*>(a.gate)[t] : 1.f;
-    // dr, and the sums g_post dn f and n dr
-    float dn[NCH][V::N];
-    float s2[2] = {};
+    const float rf = POST ? 1.f / sqrtf(ss[2] * a.inv_h + a.eps) : 1.f;
+    const float gt = v.gt;
+    const float sq = fmaf(rr, fmaf(-mr, ss[5], ss[4]), ss[3]);
+    const float mf = gt * sq * a.inv_h * rf * rf;
+    if (GATE == MOE_GATE_NONE && a.dgate && live && me == 0) static_cast<float*>(a.dgate)[t] = rf * sq;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int c = tid + i * blockDim.x;
-      float dr[V::N], x[V::N], r[V::N], g[V::N] = {}, fv[V::N], gp[V::N];
-      V::unpack(vd[i], dr);
+      const int c = me + i * tpr;
+      const bool in = live && c < a.nch;
+      float dr[V::N], fv[V::N], g[V::N], o[V::N];
+      V::unpack(v.d[i], dr);
+      V::unpack(v.f[i], fv);
       if (a.dx) {
-        V::unpack(vx[i], x);
-        V::unpack(vr[i], r);
-        if (c < a.nch) V::unpack(ld16(g_pre + c), g);
+        float x[V::N], r[V::N];
+        V::unpack(v.x[i], x);
+        V::unpack(v.r[i], r);
+        V::unpack(k_pre[i], g);
 #pragma unroll
         for (int e = 0; e < V::N; ++e) {
           dr[e] = fmaf(rr, fmaf(-r[e], mr, g[e] * x[e]), dr[e]);
           s_pre[i][e] = fmaf(x[e] * rr, r[e], s_pre[i][e]);
         }
       }
-      if (a.dresid && c < a.nch) {
-        float o[V::N];
+      if (a.dresid && in) {
 #pragma unroll
         for (int e = 0; e < V::N; ++e) o[e] = a.scale * dr[e];
         st16(static_cast<u32x4*>(a.dresid) + base + c, V::pack(o));
       }
       if (!f) continue;
-      V::unpack(vf[i], fv);
-#pragma unroll
-      for (int e = 0; e < V::N; ++e) gp[e] = 1.f;
-      if (g_post && c < a.nch) V::unpack(ld16(g_post + c), gp);
-      float n_dr[V::N];  // n dr: the gate's gradient
+      float dn[V::N], gp[V::N];
 #pragma unroll
       for (int e = 0; e < V::N; ++e) {
-        n_dr[e] = fv[e] * rf * gp[e] * dr[e];
-        s2[1] += n_dr[e];
-        dn[i][e] = gt * dr[e];
+        dn[e] = gt * dr[e];
+        gp[e] = 1.f;
       }
-      if (a.gate_kind >= MOE_GATE_CHANNEL) {
-        V::unpack(vg[i], g);
-#pragma unroll
-        for (int e = 0; e < V::N; ++e) dn[i][e] *= g[e];
-        if (a.gate_kind == MOE_GATE_FULL) {
-          if (a.dgate && c < a.nch) st16(static_cast<u32x4*>(a.dgate) + base + c, V::pack(n_dr));
-        } else {
-#pragma unroll
-          for (int e = 0; e < V::N; ++e) s_gate[i][e] += n_dr[e];
-        }
-      }
-      if (g_post) {
+      if constexpr (POST) V::unpack(k_post[i], gp);
+      if constexpr (GATE != MOE_GATE_NONE) {
+        if constexpr (GATE == MOE_GATE_FULL) V::unpack(v.g[i], g);
+        else V::unpack(k_gate[i], g);
 #pragma unroll
         for (int e = 0; e < V::N; ++e) {
-          s_post[i][e] = fmaf(dn[i][e] * rf, fv[e], s_post[i][e]);
-          dn[i][e] *= gp[e];
-          s2[0] = fmaf(dn[i][e], fv[e], s2[0]);
+          dn[e] *= g[e];
+          o[e] = fv[e] * rf * gp[e] * dr[e];  // n dr: the gate's gradient
+          if constexpr (GATE == MOE_GATE_CHANNEL) s_gate[i][e] += o[e];
+        }
+        if (GATE == MOE_GATE_FULL && a.dgate && in) st16(static_cast<u32x4*>(a.dgate) + base + c, V::pack(o));
+      }
+      if constexpr (POST) {
+#pragma unroll
+        for (int e = 0; e < V::N; ++e) {
+          s_post[i][e] = fmaf(dn[e] * rf, fv[e], s_post[i][e]);
+          dn[e] = rf * fmaf(-fv[e], mf, dn[e] * gp[e]);
         }
       }
+      if (in) st16(static_cast<u32x4*>(a.df) + base + c, V::pack(dn));
     }
-    if (!f) {
-      __syncthreads();  // red[0] is read before the next row's sums
-      continue;
-    }
-    float mf = 0.f;
-    if (g_post || (a.gate_kind == MOE_GATE_TOKEN && a.dgate)) {
-      block_sums<2>(s2, red[1], lane, wave, nw);
-      mf = s2[0] * a.inv_h * rf * rf;
-      if (a.gate_kind == MOE_GATE_TOKEN && a.dgate && tid == 0) static_cast<float*>(a.dgate)[t] = s2[1];
-    } else {
-      __syncthreads();  // red[0] is read before the next row's sums
-    }
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int c = tid + i * blockDim.x;
-      if (c >= a.nch) continue;
-      if (g_post) {
-        float fv[V::N];
-        V::unpack(vf[i], fv);
-#pragma unroll
-        for (int e = 0; e < V::N; ++e) dn[i][e] = rf * fmaf(-fv[e], mf, dn[i][e]);
-      }
-      st16(static_cast<u32x4*>(a.df) + base + c, V::pack(dn[i]));
-    }
+    if constexpr (AHEAD) v = next;
   }
-  // partial sums [gridDim.x][sums][H]: dg_post, dg_pre, dgate, as far as wanted
+  // partial sums [gridDim.x][sums][H]: dg_post, dg_pre, dgate, as far as wanted; the
+  // workgroup's groups are added first
   const int H = a.nch * V::N;
   float* p = a.partial + (int64_t)blockIdx.x * a.sums * H;
-  auto put = [&](const float (&s)[NCH][V::N]) {
+  __shared__ __attribute__((aligned(16))) float other[NCH == 1 ? NT * V::N : 4];
+  auto put = [&](float (&s)[NCH][V::N]) {
+    if constexpr (NCH == 1) {
+      if (groups > 1) {
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int c = tid + i * blockDim.x;
-      if (c >= a.nch) continue;
+        for (int e = 0; e < V::N; ++e) other[tid * V::N + e] = s[0][e];
+        __syncthreads();
+        if (group == 0)
+          for (int q = 1; q < groups; ++q)
 #pragma unroll
-      for (int e = 0; e < V::N; e += 4)
-        *reinterpret_cast<f32x4*>(p + c * V::N + e) = f32x4{s[i][e], s[i][e + 1], s[i][e + 2], s[i][e + 3]};
+            for (int e = 0; e < V::N; ++e) s[0][e] += other[(q * tpr + tid) * V::N + e];
+      }
+    }
+    if (group == 0) {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        const int c = me + i * tpr;
+        if (c >= a.nch) continue;
+#pragma unroll
+        for (int e = 0; e < V::N; e += 4)
+          *reinterpret_cast<f32x4*>(p + c * V::N + e) = f32x4{s[i][e], s[i][e + 1], s[i][e + 2], s[i][e + 3]};
+      }
     }
     p += H;
   };
-  if (a.dg_post) put(s_post);
+  if constexpr (POST) {
+    if (a.dg_post) put(s_post);
+  }
   if (a.dg_pre) put(s_pre);
-  if (a.gate_kind == MOE_GATE_CHANNEL && a.dgate) put(s_gate);
+  if constexpr (GATE == MOE_GATE_CHANNEL) {
+    if (a.dgate) put(s_gate);
+  }
 }
 
-// One thread per column of the sums: the workgroups' partial sums in order.
-__global__ __launch_bounds__(256) void norm_sums_kernel(const float* __restrict__ partial, float* o0, float* o1,
-                                                        float* o2, int wgs, int H, int sums) {
-  __shared__ float red[16][17];
-  const int col = blockIdx.x * 16 + (threadIdx.x & 15), part = threadIdx.x >> 4;
+// The workgroups' partial sums in order: 32 columns a workgroup, 32 parts of the partials.
+__global__ __launch_bounds__(1024) void norm_sums_kernel(const float* __restrict__ partial, float* o0, float* o1,
+                                                         float* o2, int wgs, int H, int sums) {
+  __shared__ float red[32][33];
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   const int n = sums * H;
   float v = 0.f;
-  if (col < n)
-    for (int i = part; i < wgs; i += 16) v += partial[(int64_t)i * n + col];
-  red[part][threadIdx.x & 15] = v;
+  if (col < n) {
+    const float* p = partial + col;
+#pragma unroll 8
+    for (int i = part; i < wgs; i += 32) v += p[(int64_t)i * n];
+  }
+  red[part][lane] = v;
   __syncthreads();
   if (part == 0 && col < n) {
     v = 0.f;
-    for (int i = 0; i < 16; ++i) v += red[i][threadIdx.x & 15];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v += red[i][lane];
     const int which = col / H;
     (which == 0 ? o0 : which == 1 ? o1 : o2)[col - which * H] = v;
   }
@@ -282,7 +355,7 @@ int threads_of(int nch, int per) { return ((nch + per - 1) / per + 63) / 64 * 64
 
 }  // namespace
 
-constexpr int kNormMaxPartials = 512;
+constexpr int kNormMaxPartials = 256;  // workgroups: one a compute unit, fewer sums to add
 
 size_t norm_partial_floats(int64_t T, int64_t H) {
   return (size_t)(T < kNormMaxPartials ? T : kNormMaxPartials) * 3 * (size_t)H;
@@ -301,19 +374,39 @@ hipError_t launch_norm(const NormArgs& a, int T, bool f32, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <bool F32, int NCH, int NT, bool POST>
+static void back_kernel(const NormBackArgs& a, int grid, int threads, int tpr, hipStream_t s) {
+  if (a.gate_kind == MOE_GATE_FULL) norm_backward_kernel<F32, NCH, NT, POST, MOE_GATE_FULL><<<grid, threads, 0, s>>>(a, tpr);
+  else if (a.gate_kind == MOE_GATE_CHANNEL)
+    norm_backward_kernel<F32, NCH, NT, POST, MOE_GATE_CHANNEL><<<grid, threads, 0, s>>>(a, tpr);
+  else norm_backward_kernel<F32, NCH, NT, POST, MOE_GATE_NONE><<<grid, threads, 0, s>>>(a, tpr);
+}
+template <bool F32, int NCH, int NT>
+static void back_kernel(const NormBackArgs& a, int& grid, hipStream_t s) {
+  // short rows: several at a time
+  const int tpr = threads_of(a.nch, NCH), groups = NCH == 1 && tpr < NT ? NT / tpr : 1;
+  grid = (a.T + groups - 1) / groups;
+  grid = grid < kNormMaxPartials ? grid : kNormMaxPartials;
+  if (a.g_post) back_kernel<F32, NCH, NT, true>(a, grid, groups * tpr, tpr, s);
+  else back_kernel<F32, NCH, NT, false>(a, grid, groups * tpr, tpr, s);
+}
+
 hipError_t launch_norm_backward(NormBackArgs a, bool f32, hipStream_t s) {
   const int H = a.nch * (f32 ? 4 : 8);
   a.sums = (a.dg_post != nullptr) + (a.dg_pre != nullptr) + (a.gate_kind == MOE_GATE_CHANNEL && a.dgate);
-  const int grid = a.T < kNormMaxPartials ? a.T : kNormMaxPartials;
-#define MOE_NORM(NCH)                                                                              \
-  do {                                                                                             \
-    if (f32) norm_backward_kernel<true, NCH><<<grid, threads_of(a.nch, NCH), 0, s>>>(a);           \
-    else norm_backward_kernel<false, NCH><<<grid, threads_of(a.nch, NCH), 0, s>>>(a);              \
-  } while (0)
-  if (a.nch <= 512) MOE_NORM(1);
-  else if (a.nch <= 1024) MOE_NORM(2);
-  else MOE_NORM(4);
-#undef MOE_NORM
+  int grid = 0;
+  if (f32) {
+    if (a.nch <= 448) back_kernel<true, 1, 1024>(a, grid, s);
+    else if (a.nch <= 512) back_kernel<true, 1, 512>(a, grid, s);
+    else if (a.nch <= 1024) back_kernel<true, 2, 512>(a, grid, s);
+    else if (a.nch <= 2048) back_kernel<true, 4, 512>(a, grid, s);
+    else back_kernel<true, 4, 1024>(a, grid, s);
+  } else {
+    if (a.nch <= 448) back_kernel<false, 1, 1024>(a, grid, s);
+    else if (a.nch <= 512) back_kernel<false, 1, 512>(a, grid, s);
+    else if (a.nch <= 1024) back_kernel<false, 2, 512>(a, grid, s);
+    else back_kernel<false, 4, 512>(a, grid, s);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.sums == 0) return e;
   float* out[3] = {};
@@ -321,7 +414,7 @@ hipError_t launch_norm_backward(NormBackArgs a, bool f32, hipStream_t s) {
   if (a.dg_post) out[n++] = a.dg_post;
   if (a.dg_pre) out[n++] = a.dg_pre;
   if (a.gate_kind == MOE_GATE_CHANNEL && a.dgate) out[n++] = static_cast<float*>(a.dgate);
-  norm_sums_kernel<<<(a.sums * H + 15) / 16, 256, 0, s>>>(a.partial, out[0], out[1], out[2], grid, H, a.sums);
+  norm_sums_kernel<<<(a.sums * H + 31) / 32, 1024, 0, s>>>(a.partial, out[0], out[1], out[2], grid, H, a.sums);
   return hipGetLastError();
 }
 

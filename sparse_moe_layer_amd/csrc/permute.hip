@@ -79,130 +79,185 @@ __global__ __launch_bounds__(256) void unpermute_kernel(const char* __restrict__
 // 1 / (1 + e^-z) to fp32's precision (a scalar per token, on fp32 outputs)
 __device__ __forceinline__ float sigmoid_f32(float z) { return 1.f / (1.f + expf(-z)); }
 
-// With products over H: one workgroup per token, its threads over the row's
-// 16-byte chunks, KB assignments at a time, each with a sum in a register.
-// GRAD_Y: combine_backward, else permute_backward.
-struct TokenArgs {
-  const char* own;    // dout, or x
-  const char* rows;   // y, or dxs (y may be null)
+// The combine's gradient, a row per assignment and, with a shared expert, one more per
+// token: out = w * dout[t], dot = <dout[t], in>.  A wave has ROWS rows (short ones several
+// at a time).  A token's rows follow each other, so dout comes from the caches for all
+// but the first; nothing is shared between waves (4096 x 2560 x 10: 80 us; a workgroup per
+// token with its rows in registers 146).  Without dy only the products (x and dxs of
+// permute's gradient).
+struct RowArgs {
+  const char *dout, *y;
   const int32_t* pos;
-  const float* w;     // null: 1
+  const float* w;
   const char* y_sh;
   const float* sl;
-  char* out;          // dy, or dx (null, or k <= KB: a thread has all of a token's rows)
+  char* dy;
   float* dw;
   char* dy_sh;
   float* dsl;
-  int nch, k, R;      // 16-byte chunks of a row
+  int nch, k, R;  // 16-byte chunks of a row
+  int64_t n;      // rows in all
+  int per;        // rows a token
+  int first;      // k: the shared expert's rows alone
+};
+
+template <bool F32, int ROWS>
+__global__ __launch_bounds__(256) void rows_kernel(RowArgs a) {
+  using V = Vec<F32>;
+  constexpr int U = 4 / ROWS;  // 16-byte pieces of a row that a lane has in flight, each with a sum of its own
+  const int lane = threadIdx.x & 63;
+  const int64_t i0 = ((int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * ROWS;
+  const int64_t row = (int64_t)a.nch * 16;
+  const char *d[ROWS], *in[ROWS];
+  char* out[ROWS];
+  float w[ROWS], dot[4] = {};
+  bool ok[ROWS], shared[ROWS];
+  int64_t at[ROWS];
+#pragma unroll
+  for (int q = 0; q < ROWS; ++q) {
+    const int64_t i = i0 + q < a.n ? i0 + q : a.n - 1;
+    const int t = (int)(i / a.per), j = (int)(i - (int64_t)t * a.per) + a.first;
+    shared[q] = j == a.k;
+    at[q] = shared[q] ? t : (int64_t)t * a.k + j;
+    int p = shared[q] ? t : a.pos[at[q]];
+    ok[q] = shared[q] || (unsigned)p < (unsigned)a.R;
+    if (!ok[q]) p = 0;
+    w[q] = shared[q] ? sigmoid_f32(a.sl[t]) : a.w ? a.w[at[q]] : 1.f;
+    d[q] = a.dout + t * row;
+    in[q] = (shared[q] ? a.y_sh : a.y) + p * row;
+    out[q] = (shared[q] ? a.dy_sh : a.dy) + p * row;
+    ok[q] = ok[q] && i0 + q < a.n;
+  }
+  for (int c0 = lane; c0 < a.nch; c0 += 64 * U) {
+    u32x4 vd[4], vi[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int q = u / U, c = c0 + 64 * (u % U) < a.nch ? c0 + 64 * (u % U) : c0;
+      vd[u] = ld16(d[q] + (int64_t)c * 16);
+      vi[u] = ld16_nt(in[q] + (int64_t)c * 16);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int q = u / U, c = c0 + 64 * (u % U);
+      if (!ok[q] || c >= a.nch) continue;
+      float x[V::N], y[V::N];
+      V::unpack(vd[u], x);
+      V::unpack(vi[u], y);
+#pragma unroll
+      for (int e = 0; e < V::N; ++e) {
+        dot[u] = fmaf(x[e], y[e], dot[u]);
+        x[e] *= w[q];
+      }
+      if (a.dy) st16(out[q] + (int64_t)c * 16, V::pack(x));
+    }
+  }
+  const float s = wave_sums<4>(dot, lane);
+#pragma unroll
+  for (int q = 0; q < ROWS; ++q) {
+    float v = __shfl(s, q * U * 16, kWave);
+#pragma unroll
+    for (int u = 1; u < U; ++u) v += __shfl(s, (q * U + u) * 16, kWave);
+    if (lane || i0 + q >= a.n) continue;
+    if (shared[q]) a.dsl[at[q]] = w[q] * sigmoid_f32(-a.sl[at[q]]) * v;
+    else a.dw[at[q]] = ok[q] ? v : 0.f;
+  }
+}
+
+hipError_t launch_rows(RowArgs a, int T, int per, bool f32, hipStream_t s) {
+  a.n = (int64_t)T * per;
+  a.per = per;
+  const bool many = a.nch <= 64;  // rows of one piece a lane
+  const int64_t waves = many ? (a.n + 3) / 4 : a.n;
+  const dim3 grid((uint32_t)((waves + 3) / 4));
+  if (f32 && many) rows_kernel<true, 4><<<grid, 256, 0, s>>>(a);
+  else if (f32) rows_kernel<true, 1><<<grid, 256, 0, s>>>(a);
+  else if (many) rows_kernel<false, 4><<<grid, 256, 0, s>>>(a);
+  else rows_kernel<false, 1><<<grid, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// permute's gradient with dw for at most KB assignments a token: the token's waves over
+// the row's 16-byte chunks, a sum in a register for each assignment.
+struct TokenArgs {
+  const char* x;
+  const char* dxs;
+  const int32_t* pos;
+  const float* w;  // null: 1
+  char* dx;
+  float* dw;
+  int T, nch, k, R;  // nch: 16-byte chunks of a row
 };
 
 constexpr int kTokenThreads = 512;
 
-template <bool F32, bool GRAD_Y, int KB>
-__global__ __launch_bounds__(kTokenThreads) void token_kernel(TokenArgs a) {
+template <bool F32, int KB>
+__global__ __launch_bounds__(kTokenThreads, 2) void token_kernel(TokenArgs a) {
   using V = Vec<F32>;
   constexpr int P = KB <= 4 ? 4 : KB <= 8 ? 8 : 16;
   __shared__ float red[kTokenThreads / 64][P];
-  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nw = blockDim.x >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nw = blockDim.x >> 6;
   const int nch = a.nch;
-  const int64_t a0 = (int64_t)t * a.k;
-  const char* own = a.own + (int64_t)t * nch * 16;
-  const bool sums = a.dw != nullptr;
-  const bool shared = GRAD_Y && a.y_sh != nullptr;
-  const float g = shared ? sigmoid_f32(a.sl[t]) : 0.f;
-  float dots = 0.f;
-  for (int j0 = 0; j0 < a.k; j0 += KB) {
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const int64_t a0 = (int64_t)t * a.k;
+    const char* x = a.x + (int64_t)t * nch * 16;
     float acc[P] = {};
     int64_t row[KB];
     bool ok[KB];
     float wj[KB];
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
-      const int j = j0 + b < a.k ? j0 + b : a.k - 1;
+      const int j = b < a.k ? b : a.k - 1;
       const int p = a.pos[a0 + j];
-      ok[b] = j0 + b < a.k && (unsigned)p < (unsigned)a.R;
+      ok[b] = b < a.k && (unsigned)p < (unsigned)a.R;
       row[b] = (int64_t)(ok[b] ? p : 0) * nch * 16;
       wj[b] = a.w ? a.w[a0 + j] : 1.f;
     }
     for (int c = tid; c < nch; c += blockDim.x) {
-      u32x4 v[KB], vs = {};
-      const u32x4 vo = ld16(own + (int64_t)c * 16);
-      if (!GRAD_Y || sums) {
+      u32x4 v[KB];
+      const u32x4 vx = ld16(x + (int64_t)c * 16);
 #pragma unroll
-        for (int b = 0; b < KB; ++b) v[b] = ld16_nt(a.rows + row[b] + (int64_t)c * 16);
-      }
-      const bool sh = shared && j0 == 0;
-      if (sh) vs = ld16_nt(a.y_sh + ((int64_t)t * nch + c) * 16);
+      for (int b = 0; b < KB; ++b) v[b] = ld16_nt(a.dxs + row[b] + (int64_t)c * 16);
       float d[V::N], dx[V::N] = {};
-      V::unpack(vo, d);
+      V::unpack(vx, d);
 #pragma unroll
       for (int b = 0; b < KB; ++b) {
         float f[V::N];
-        if (!GRAD_Y || sums) {
-          V::unpack(v[b], f);
-#pragma unroll
-          for (int e = 0; e < V::N; ++e) acc[b] = fmaf(d[e], f[e], acc[b]);
-        }
-        if constexpr (GRAD_Y) {
-          if (ok[b]) {
-#pragma unroll
-            for (int e = 0; e < V::N; ++e) f[e] = wj[b] * d[e];
-            st16(a.out + row[b] + (int64_t)c * 16, V::pack(f));
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < V::N; ++e) dx[e] = ok[b] ? fmaf(wj[b], f[e], dx[e]) : dx[e];
-        }
-      }
-      if constexpr (!GRAD_Y) {
-        if (a.out) st16(a.out + ((int64_t)t * nch + c) * 16, V::pack(dx));
-      }
-      if (sh) {
-        float f[V::N];
-        V::unpack(vs, f);
+        V::unpack(v[b], f);
+        float s[2] = {};
 #pragma unroll
         for (int e = 0; e < V::N; ++e) {
-          dots = fmaf(d[e], f[e], dots);
-          f[e] = g * d[e];
+          s[e & 1] = fmaf(d[e], f[e], s[e & 1]);
+          dx[e] = ok[b] ? fmaf(wj[b], f[e], dx[e]) : dx[e];
         }
-        st16(a.dy_sh + ((int64_t)t * nch + c) * 16, V::pack(f));
+        acc[b] += s[0] + s[1];
       }
+      st16(a.dx + ((int64_t)t * nch + c) * 16, V::pack(dx));
     }
-    if (sums) {
-      const float s = wave_sums<P>(acc, lane);
-      constexpr int kStep = 64 / P;
-      __syncthreads();  // the values of the batch before are read
-      if (lane % kStep == 0) red[wave][lane / kStep] = s;
-      __syncthreads();
-      if (tid < KB && j0 + tid < a.k) {
-        float v = 0.f;
-        for (int i = 0; i < nw; ++i) v += red[i][tid];
-        const int p = a.pos[a0 + j0 + tid];
-        a.dw[a0 + j0 + tid] = (unsigned)p < (unsigned)a.R ? v : 0.f;
-      }
-    }
-  }
-  if (shared) {
-    dots = wave_sum(dots);
+    const float s = wave_sums<P>(acc, lane);
+    constexpr int kStep = 64 / P;
+    __syncthreads();  // the token before has read its sums
+    if (lane % kStep == 0) red[wave][lane / kStep] = s;
     __syncthreads();
-    if (lane == 0) red[wave][0] = dots;
-    __syncthreads();
-    if (tid == 0) {
+    if (tid < KB && tid < a.k) {
       float v = 0.f;
-      for (int i = 0; i < nw; ++i) v += red[i][0];
-      a.dsl[t] = g * sigmoid_f32(-a.sl[t]) * v;
+      for (int i = 0; i < nw; ++i) v += red[i][tid];
+      const int p = a.pos[a0 + tid];
+      a.dw[a0 + tid] = (unsigned)p < (unsigned)a.R ? v : 0.f;
     }
   }
 }
 
-template <bool F32, bool GRAD_Y>
-hipError_t launch_token(const TokenArgs& a, int T, hipStream_t s) {
-  const int rounds = (a.nch + kTokenThreads - 1) / kTokenThreads;
-  const int nt = ((a.nch + rounds - 1) / rounds + 63) / 64 * 64;
-  if (a.k <= 4) token_kernel<F32, GRAD_Y, 4><<<T, nt, 0, s>>>(a);
-  else if (a.k <= 8) token_kernel<F32, GRAD_Y, 8><<<T, nt, 0, s>>>(a);
-  else if (a.k <= 10) token_kernel<F32, GRAD_Y, 10><<<T, nt, 0, s>>>(a);
-  else token_kernel<F32, GRAD_Y, 16><<<T, nt, 0, s>>>(a);
+template <bool F32>
+hipError_t launch_token(const TokenArgs& a, hipStream_t s) {
+  // Waves a token: one, or as many as it takes to have about 16 a compute unit, but no
+  // more than the row has work for (4096 x 2560 x 10: 58 us; five waves a token 138).
+  int nw = 1;
+  while (nw < kTokenThreads / 64 && (int64_t)a.T * nw < 4096 && nw * 64 < a.nch) nw *= 2;
+  const int nt = nw * 64, grid = a.T < (1 << 22) ? a.T : 1 << 22;
+  if (a.k <= 4) token_kernel<F32, 4><<<grid, nt, 0, s>>>(a);
+  else if (a.k <= 8) token_kernel<F32, 8><<<grid, nt, 0, s>>>(a);
+  else if (a.k <= 10) token_kernel<F32, 10><<<grid, nt, 0, s>>>(a);
+  else token_kernel<F32, 16><<<grid, nt, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -225,11 +280,21 @@ hipError_t launch_permute_backward(const void* dxs, const int32_t* pos, const fl
   const Divisor chunks(H / (f32 ? 4 : 8));
   const char* d = static_cast<const char*>(dxs);
   char* o = static_cast<char*>(dx);
-  if (dw) {
-    const TokenArgs a{static_cast<const char*>(x), d, pos, w, nullptr, nullptr, k <= 16 ? o : nullptr, dw, nullptr,
-                      nullptr, chunks.d, k, T * k};
-    const hipError_t e = f32 ? launch_token<true, false>(a, T, s) : launch_token<false, false>(a, T, s);
-    if (a.out || e != hipSuccess) return e;  // more than 16 a token: dx by the kernel below
+  if (dw && k <= 16) {
+    const TokenArgs a{static_cast<const char*>(x), d, pos, w, o, dw, T, chunks.d, k, T * k};
+    return f32 ? launch_token<true>(a, s) : launch_token<false>(a, s);
+  }
+  if (dw) {  // more rows than registers hold: the products, then dx
+    RowArgs a{};
+    a.dout = static_cast<const char*>(x);
+    a.y = d;
+    a.pos = pos;
+    a.dw = dw;
+    a.nch = chunks.d;
+    a.k = k;
+    a.R = T * k;
+    const hipError_t e = launch_rows(a, T, k, f32, s);
+    if (e != hipSuccess) return e;
   }
   const int n = T * chunks.d, grid = (n + 255) / 256;
 #define MOE_UNPERMUTE(F32, W)                                                                               \
@@ -249,10 +314,14 @@ hipError_t launch_permute_backward(const void* dxs, const int32_t* pos, const fl
 hipError_t launch_combine_backward(const void* dout, const void* y, const int32_t* pos, const float* w,
                                    const void* y_sh, const float* sl, void* dy, float* dw, void* dy_sh, float* dsl,
                                    int T, int H, int k, int f32, hipStream_t s) {
-  const TokenArgs a{static_cast<const char*>(dout), static_cast<const char*>(y), pos, w,
-                    static_cast<const char*>(y_sh), sl, static_cast<char*>(dy), dw, static_cast<char*>(dy_sh), dsl,
-                    H / (f32 ? 4 : 8), k, T * k};
-  return f32 ? launch_token<true, true>(a, T, s) : launch_token<false, true>(a, T, s);
+  RowArgs a{static_cast<const char*>(dout), static_cast<const char*>(y), pos, w, static_cast<const char*>(y_sh), sl,
+            static_cast<char*>(dy), dw, static_cast<char*>(dy_sh), dsl, H / (f32 ? 4 : 8), k, T * k};
+  if (dw) return launch_rows(a, T, k + (y_sh ? 1 : 0), f32, s);
+  // without the weights' gradient dy is dout permuted
+  const hipError_t e = launch_permute(dout, pos, w, dy, T, H, k, f32, s);
+  if (e != hipSuccess || !y_sh) return e;
+  a.first = k;
+  return launch_rows(a, T, 1, f32, s);
 }
 
 }  // namespace moe

@@ -44,11 +44,12 @@ __device__ __forceinline__ float wave_sums(float (&a)[P], int lane) {
   int o = 32;
 #pragma unroll
   for (int n = P; n > 1; n >>= 1, o >>= 1) {
-    const bool up = lane & o;
+    // (masks, not selects: those of two array elements become a run-time index)
+    const uint32_t up = lane & o ? 0xFFFFFFFFu : 0u;
 #pragma unroll
     for (int i = 0; i < n / 2; ++i) {
-      const float send = up ? a[i] : a[i + n / 2];
-      const float keep = up ? a[i + n / 2] : a[i];
+      const uint32_t lo = __float_as_uint(a[i]), hi = __float_as_uint(a[i + n / 2]);
+      const float send = __uint_as_float((lo & up) | (hi & ~up)), keep = __uint_as_float((hi & up) | (lo & ~up));
       a[i] = keep + __shfl_xor(send, o, kWave);
     }
   }
