@@ -300,39 +300,40 @@ def linear_problem(rows, K, N, groups=1, dtype="bf16", act="none", w_stride=0) -
     return moe_linear_problem(rows, K, N, groups, w_stride, _DT[dtype], _ACTS[act])
 
 
-class _Args:
-    """Pointers of a call's tensors: contiguous, of the expected number of values and dtype, on the current device
-    (the library launches there), or None."""
+def _bad(where: str, t, n: int, dtype, dev: int):
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{where}: a contiguous tensor of {n} values of {dtype} is needed, not {tuple(t.shape)} of "
+                         f"{t.dtype}{'' if t.is_contiguous() else ', strided'}")
+    raise ValueError(f"{where}: tensors must be on the current CUDA device")
 
-    __slots__ = ("where", "dev", "act")
 
-    def __init__(self, where: str, act: int):
-        self.where, self.dev = where, torch.cuda.current_device()
-        self.act = _TORCH_DT.get(act)  # None: the library refuses the dtype
-
-    def __call__(self, t, n: int, dtype=None):
-        if t is None:
-            return None
-        want = dtype or self.act
-        if (t.dtype is not want and want is not None) or t.numel() != n or not t.is_contiguous():
-            raise ValueError(f"{self.where}: a contiguous tensor of {n} values of {want} is needed, not "
-                             f"{tuple(t.shape)} of {t.dtype}{'' if t.is_contiguous() else ', strided'}")
-        if t.get_device() != self.dev:
-            raise ValueError(f"{self.where}: tensors must be on the current CUDA device")
+def _arg(where: str, t, n: int, dtype, dev: int):
+    """Pointer of a call's tensor (or None): contiguous, n values of dtype, on the current device, where the library
+    launches."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.numel() == n and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
+    return _bad(where, t, n, dtype, dev)
 
-    def ws(self, t):
-        if t is None:
-            return None, 0
-        n = t.numel() * t.element_size()
-        return self(t, t.numel(), t.dtype), n
 
-    def stream(self, stream):
-        if stream is None:
-            return _raw_stream(self.dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
-        if getattr(stream, "device_index", self.dev) != self.dev:
-            raise ValueError(f"{self.where}: the stream must be one of the current CUDA device")
-        return _stream(stream)
+def _ws_arg(where: str, t, dev: int):
+    if t is None:
+        return None, 0
+    n = t.numel()
+    return _arg(where, t, n, t.dtype, dev), n * t.element_size()
+
+
+def _act_of(code: int):
+    return _TORCH_DT.get(code, torch.bfloat16)  # another dtype is the library's to refuse
+
+
+def _stream_on(where: str, stream, dev: int):
+    if stream is None:
+        return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+    if getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"{where}: the stream must be one of the current CUDA device")
+    return _stream(stream)
 
 
 _I32, _F32 = torch.int32, torch.float32
@@ -340,50 +341,55 @@ _I32, _F32 = torch.int32, torch.float32
 
 def moe_permute(p, x, assign_pos, topk_w, xs, stream=None):
     """x [T, H] -> xs [T*k, H]: xs[assign_pos[t*k+j]] = topk_w[t, j] * x[t] (topk_w None: x[t])."""
-    a = _Args("moe_permute", p.act_dtype)
-    n, R = p.T * p.H, p.T * p.k
-    _check(LIB.moe_permute(ctypes.byref(p), a(x, n), a(assign_pos, R, _I32), a(topk_w, R, _F32), a(xs, R * p.H),
-                           a.stream(stream)), a.where)
+    f, d, dt, H, R = "moe_permute", torch.cuda.current_device(), _act_of(p.act_dtype), p.H, p.T * p.k
+    _check(LIB.moe_permute(p, _arg(f, x, p.T * H, dt, d), _arg(f, assign_pos, R, _I32, d),
+                           _arg(f, topk_w, R, _F32, d), _arg(f, xs, R * H, dt, d), _stream_on(f, stream, d)), f)
 
 
 def moe_permute_backward(p, dxs, assign_pos, topk_w, x, dx, dtopk_w, stream=None):
     """Gradients of moe_permute: dx [T, H], and dtopk_w [T, k] where it is not None (x is read for it alone)."""
-    a = _Args("moe_permute_backward", p.act_dtype)
-    n, R = p.T * p.H, p.T * p.k
-    _check(LIB.moe_permute_backward(ctypes.byref(p), a(dxs, R * p.H), a(assign_pos, R, _I32), a(topk_w, R, _F32),
-                                    a(x, n), a(dx, n), a(dtopk_w, R, _F32), a.stream(stream)), a.where)
+    f, d, dt, H, R = "moe_permute_backward", torch.cuda.current_device(), _act_of(p.act_dtype), p.H, p.T * p.k
+    n = p.T * H
+    _check(LIB.moe_permute_backward(p, _arg(f, dxs, R * H, dt, d), _arg(f, assign_pos, R, _I32, d),
+                                    _arg(f, topk_w, R, _F32, d), _arg(f, x, n, dt, d), _arg(f, dx, n, dt, d),
+                                    _arg(f, dtopk_w, R, _F32, d), _stream_on(f, stream, d)), f)
 
 
 def moe_combine_backward(p, dout, y, assign_pos, topk_w, y_shared, shared_logit, dy, dtopk_w, dy_shared,
                          dshared_logit, stream=None):
     """Gradients of moe_combine: dy [T*k, H], dtopk_w [T, k] (or None), dy_shared [T, H], dshared_logit [T]."""
-    a = _Args("moe_combine_backward", p.act_dtype)
-    n, R = p.T * p.H, p.T * p.k
-    _check(LIB.moe_combine_backward(ctypes.byref(p), a(dout, n), a(y, R * p.H), a(assign_pos, R, _I32),
-                                    a(topk_w, R, _F32), a(y_shared, n), a(shared_logit, p.T, _F32), a(dy, R * p.H),
-                                    a(dtopk_w, R, _F32), a(dy_shared, n), a(dshared_logit, p.T, _F32),
-                                    a.stream(stream)), a.where)
+    f, d, dt, T, H = "moe_combine_backward", torch.cuda.current_device(), _act_of(p.act_dtype), p.T, p.H
+    n, R = T * H, T * p.k
+    _check(LIB.moe_combine_backward(p, _arg(f, dout, n, dt, d), _arg(f, y, R * H, dt, d),
+                                    _arg(f, assign_pos, R, _I32, d), _arg(f, topk_w, R, _F32, d),
+                                    _arg(f, y_shared, n, dt, d), _arg(f, shared_logit, T, _F32, d),
+                                    _arg(f, dy, R * H, dt, d), _arg(f, dtopk_w, R, _F32, d),
+                                    _arg(f, dy_shared, n, dt, d), _arg(f, dshared_logit, T, _F32, d),
+                                    _stream_on(f, stream, d)), f)
 
 
-def _gate_arg(a, p, t, summed: bool):
+def _gate_arg(f, p, t, dt, dev, summed: bool):
     """A gate ([T] fp32, [H], [T, H]), or its gradient, which is fp32 where it is summed over rows or columns."""
+    if t is None:
+        return None
     if p.gate == MOE_GATE_FULL:
-        return a(t, p.T * p.H)
+        return _arg(f, t, p.T * p.H, dt, dev)
     if p.gate == MOE_GATE_CHANNEL:
-        return a(t, p.H, _F32 if summed else None)
-    return a(t, p.T, _F32)
+        return _arg(f, t, p.H, _F32 if summed else dt, dev)
+    return _arg(f, t, p.T, _F32, dev)
 
 
 def moe_block_norm(p: moe_norm_problem, f, resid, g_post, gate, g_pre, resid_out, x, stream=None):
     """resid_out = resid_scale * resid + gate * RMSNorm(f) g_post, x = RMSNorm(resid_out) g_pre (None: left out)."""
-    a = _Args("moe_block_norm", p.dtype)
-    n = p.T * p.H
-    _check(LIB.moe_block_norm(ctypes.byref(p), a(f, n), a(resid, n), a(g_post, p.H), _gate_arg(a, p, gate, False),
-                              a(g_pre, p.H), a(resid_out, n), a(x, n), a.stream(stream)), a.where)
+    w, d, dt, H = "moe_block_norm", torch.cuda.current_device(), _act_of(p.dtype), p.H
+    n = p.T * H
+    _check(LIB.moe_block_norm(p, _arg(w, f, n, dt, d), _arg(w, resid, n, dt, d), _arg(w, g_post, H, dt, d),
+                              _gate_arg(w, p, gate, dt, d, False), _arg(w, g_pre, H, dt, d),
+                              _arg(w, resid_out, n, dt, d), _arg(w, x, n, dt, d), _stream_on(w, stream, d)), w)
 
 
 def moe_block_norm_workspace_bytes(p: moe_norm_problem) -> int:
-    return LIB.moe_block_norm_workspace_bytes(ctypes.byref(p))
+    return LIB.moe_block_norm_workspace_bytes(p)
 
 
 def norm_workspace(p: moe_norm_problem, device="cuda") -> torch.Tensor:
@@ -397,38 +403,40 @@ def norm_workspace(p: moe_norm_problem, device="cuda") -> torch.Tensor:
 def moe_block_norm_backward(p: moe_norm_problem, dresid_out, dx, f, resid_out, g_post, gate, g_pre, dresid, df,
                             dg_post, dgate, dg_pre, ws, stream=None):
     """Gradients of moe_block_norm; dg_post, dg_pre [H] fp32, dgate [T] or [H] fp32 or [T, H]; ws: norm_workspace(p)."""
-    a = _Args("moe_block_norm_backward", p.dtype)
-    n = p.T * p.H
-    _check(LIB.moe_block_norm_backward(ctypes.byref(p), a(dresid_out, n), a(dx, n), a(f, n), a(resid_out, n),
-                                       a(g_post, p.H), _gate_arg(a, p, gate, False), a(g_pre, p.H), a(dresid, n),
-                                       a(df, n), a(dg_post, p.H, _F32), _gate_arg(a, p, dgate, True),
-                                       a(dg_pre, p.H, _F32), *a.ws(ws), a.stream(stream)), a.where)
+    w, d, dt, H = "moe_block_norm_backward", torch.cuda.current_device(), _act_of(p.dtype), p.H
+    n = p.T * H
+    _check(LIB.moe_block_norm_backward(p, _arg(w, dresid_out, n, dt, d), _arg(w, dx, n, dt, d), _arg(w, f, n, dt, d),
+                                       _arg(w, resid_out, n, dt, d), _arg(w, g_post, H, dt, d),
+                                       _gate_arg(w, p, gate, dt, d, False), _arg(w, g_pre, H, dt, d),
+                                       _arg(w, dresid, n, dt, d), _arg(w, df, n, dt, d), _arg(w, dg_post, H, _F32, d),
+                                       _gate_arg(w, p, dgate, dt, d, True), _arg(w, dg_pre, H, _F32, d),
+                                       *_ws_arg(w, ws, d), _stream_on(w, stream, d)), w)
 
 
-def _weights_arg(a, p, w):
+def _weights_arg(f, p, w, dt, dev):
     """[groups, N, K] contiguous, or at p.w_stride from one contiguous matrix to the next (a slice of a fused
     [groups, 2 N, K] tensor)."""
     if w is None or p.w_stride in (0, p.N * p.K):
-        return a(w, p.groups * p.N * p.K)
+        return _arg(f, w, p.groups * p.N * p.K, dt, dev)
     want = (p.groups, p.N, p.K)
-    if tuple(w.shape) != want or (p.groups > 1 and w.stride(0) != p.w_stride) or not w[0].is_contiguous():
-        raise ValueError(f"{a.where}: weights must be {want} with {p.w_stride} values from one matrix to the next")
-    a(w[0], p.N * p.K)
-    return w.data_ptr()
+    if tuple(w.shape) != want or (p.groups > 1 and w.stride(0) != p.w_stride):
+        raise ValueError(f"{f}: weights must be {want} with {p.w_stride} values from one matrix to the next")
+    return _arg(f, w[0], p.N * p.K, dt, dev)  # the first matrix's
 
 
 def moe_linear(p: moe_linear_problem, x, w, bias, offsets, mul, resid, y, z, stream=None):
     """y[r] = resid[r] + act(x[r] W_g^T + bias_g) * mul[r] for the rows r of each group g (bias, mul, resid, z may be
     None; offsets [groups + 1] int32, None for one group); z receives the activation's argument."""
-    a = _Args("moe_linear", p.dtype)
-    n = p.rows * p.N
-    _check(LIB.moe_linear(ctypes.byref(p), a(x, p.rows * p.K), _weights_arg(a, p, w), a(bias, p.groups * p.N),
-                          a(offsets, p.groups + 1, _I32), a(mul, n), a(resid, n), a(y, n), a(z, n),
-                          a.stream(stream)), a.where)
+    f, d, dt, rows, G = "moe_linear", torch.cuda.current_device(), _act_of(p.dtype), p.rows, p.groups
+    n = rows * p.N
+    _check(LIB.moe_linear(p, _arg(f, x, rows * p.K, dt, d), _weights_arg(f, p, w, dt, d),
+                          _arg(f, bias, G * p.N, dt, d), _arg(f, offsets, G + 1, _I32, d), _arg(f, mul, n, dt, d),
+                          _arg(f, resid, n, dt, d), _arg(f, y, n, dt, d), _arg(f, z, n, dt, d),
+                          _stream_on(f, stream, d)), f)
 
 
 def moe_linear_workspace_bytes(p: moe_linear_problem) -> int:
-    return LIB.moe_linear_workspace_bytes(ctypes.byref(p))
+    return LIB.moe_linear_workspace_bytes(p)
 
 
 def linear_workspace(p: moe_linear_problem, device="cuda") -> torch.Tensor:
@@ -441,12 +449,13 @@ def linear_workspace(p: moe_linear_problem, device="cuda") -> torch.Tensor:
 
 def moe_linear_backward(p: moe_linear_problem, dy, x, w, offsets, mul, z, dx, dw, dbias, dmul, ws, stream=None):
     """Gradients of moe_linear (each output may be None; dbias [groups, N] fp32); ws: linear_workspace(p)."""
-    a = _Args("moe_linear_backward", p.dtype)
-    n, m = p.rows * p.N, p.rows * p.K
-    _check(LIB.moe_linear_backward(ctypes.byref(p), a(dy, n), a(x, m), _weights_arg(a, p, w),
-                                   a(offsets, p.groups + 1, _I32), a(mul, n), a(z, n), a(dx, m),
-                                   _weights_arg(a, p, dw), a(dbias, p.groups * p.N, _F32), a(dmul, n), *a.ws(ws),
-                                   a.stream(stream)), a.where)
+    f, d, dt, rows, G = "moe_linear_backward", torch.cuda.current_device(), _act_of(p.dtype), p.rows, p.groups
+    n, m = rows * p.N, rows * p.K
+    _check(LIB.moe_linear_backward(p, _arg(f, dy, n, dt, d), _arg(f, x, m, dt, d), _weights_arg(f, p, w, dt, d),
+                                   _arg(f, offsets, G + 1, _I32, d), _arg(f, mul, n, dt, d), _arg(f, z, n, dt, d),
+                                   _arg(f, dx, m, dt, d), _weights_arg(f, p, dw, dt, d),
+                                   _arg(f, dbias, G * p.N, _F32, d), _arg(f, dmul, n, dt, d), *_ws_arg(f, ws, d),
+                                   _stream_on(f, stream, d)), f)
 
 
 _DT_OF_TORCH = {torch.float32: "f32", torch.bfloat16: "bf16", torch.uint8: "fp8"}

@@ -450,11 +450,12 @@ struct Tiles {
   using MidOnce = Tile<F32, 128, 128, 2, 2, 2, 128, 2, true>;
   using Deep = Tile<F32, 128, 128, 2, 2, 4, 128, 1>;
   using Short = Tile<F32, 128, 128, 2, 2, 2, 64, 4>;
+  using Short3 = Tile<F32, 128, 128, 2, 2, 3, 64, 3>;
   using Small = Tile<F32, 64, 64, 2, 2, 4, 128, 2>;
   using SmallOnce = Tile<F32, 64, 64, 2, 2, 4, 128, 2, true>;
   using Tiny = Tile<F32, 32, 32, 1, 1, 4, 128, 4, false, 4>;
 };
-enum Choice { kBig, kMid, kMidOnce, kDeep, kShort, kSmall, kSmallOnce, kTiny };
+enum Choice { kBig, kMid, kMidOnce, kDeep, kShort, kShort3, kSmall, kSmallOnce, kTiny };
 
 // Rows of a group on average, and the tiles of edge b that a product takes about.
 int64_t group_mean(const LinearArgs& a) { return a.rows / a.G; }
@@ -502,8 +503,9 @@ Choice choose(LinearMode mode, const LinearArgs& a, bool f32) {
   // a round of 128-row tiles with four stages (2000 x 2048 x 2048: 19.6; two workgroups of two stages 26.3);
   if (t128 <= 256) return kDeep;
   // dw of short groups, which is loads, a few steps and stores: four workgroups a compute
-  // unit overlap them (512 groups of 80 rows 497; two 554);
-  if (mode == kLinDw && r <= 256) return kShort;
+  // unit overlap them (512 groups of 80 rows with their dz 542; two 599), for more than a
+  // step or two three of one more stage (80 rows 502, 39 rows 332; four 542 and 305);
+  if (mode == kLinDw && r <= 256) return r <= 44 ? kShort : kShort3;
   // groups of one tile read their weights once (512 groups of 80 rows 393; 404), others share them.
   return mode != kLinDw && r <= 128 ? kMidOnce : kMid;
 }
@@ -534,6 +536,13 @@ hipError_t launch(LinearMode mode, Job j, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <class C>
+hipError_t launch_dw(Job j, hipStream_t s) {  // tiles that dw alone takes
+  const dim3 grid((uint32_t)(j.sums + grid_of<C>(kLinDw, j.a, j.super[0])));
+  linear_tiles_kernel<kLinDw, -1, C><<<grid, C::NT, 0, s>>>(j);
+  return hipGetLastError();
+}
+
 // dx and dw of a small product side by side, `first` first.
 template <class C>
 hipError_t launch_both(LinearMode first, Job j, hipStream_t s) {
@@ -553,7 +562,8 @@ hipError_t launch_one(LinearMode mode, const Job& j, hipStream_t s) {
   if constexpr (!F32) {  // fp32 takes the others alone
     if (c == kMidOnce) return launch<typename X::MidOnce>(mode, j, s);
     if (c == kDeep) return launch<typename X::Deep>(mode, j, s);
-    if (c == kShort) return launch<typename X::Short>(mode, j, s);
+    if (c == kShort) return launch_dw<typename X::Short>(j, s);
+    if (c == kShort3) return launch_dw<typename X::Short3>(j, s);
     if (c == kSmallOnce) return launch<typename X::SmallOnce>(mode, j, s);
   }
   if (c == kBig) return launch<typename X::Big>(mode, j, s);
