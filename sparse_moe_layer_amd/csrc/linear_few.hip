@@ -95,6 +95,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void linear_few_kernel(LinearArgs a
     step(r2 + mine, p + (kAhead + 2) * kWaves);
     step(r3 + mine, p + (kAhead + 3) * kWaves);
   }
+  __builtin_amdgcn_s_waitcnt(0xF70);  // the loads past the end have landed too
   // rows 4 (lane / 16) .. + 4 of W, row lane % 16 of x
 #pragma unroll
   for (int v = 0; v < 4; ++v) red[wave][lane & 15][4 * (lane >> 4) + v] = acc[v];

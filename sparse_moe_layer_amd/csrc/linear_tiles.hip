@@ -471,14 +471,15 @@ Choice choose(LinearMode mode, const LinearArgs& a, bool f32) {
   if (f32) {
     // The matrix rate bounds every size of tile, so the least work of the busiest compute
     // unit decides, the smaller tiles' overhead counted in (forward, us, tiles of 32, 64 and
-    // 128 rows: 300 x 1024 x 1024 12.2, 18.9, 45; 2000 x 2048 x 1024 76.7, 65.5, 118;
-    // 8000 x 512 x 1024 85.2, 71.7, 68.6; the library's product 20.5, 64.2, 66.6).
+    // 128 rows: 300 x 1024 x 1024 11.9, 19.2, 63; 2000 x 2048 x 1024 76.9, 69.6, 123;
+    // 8000 x 512 x 1024 84.9, 71.5, 69.0; the library's product 20.5, 64.2, 66.6.  256 rows
+    // give nothing: 4096 x 4096 x 4096 923, 128 rows 918).
     struct Size {
       int b;
       double cost;
       Choice c;
     };
-    const Size sizes[] = {{32, 1.2, kTiny}, {64, 1.05, kSmall}, {128, 1.0, kMid}, {256, 1.0, kBig}};
+    const Size sizes[] = {{32, 1.2, kTiny}, {64, 1.05, kSmall}, {128, 1.0, kMid}};
     Choice best = kTiny;
     double least = 1e30;
     for (const Size& z : sizes) {
@@ -488,9 +489,13 @@ Choice choose(LinearMode mode, const LinearArgs& a, bool f32) {
     return best;
   }
   // us, forward unless named, of one side and the other:
-  // 256-row tiles once they fill three quarters of the chip (8192 x 2560 x 8192: 283; 128-row 391), dw
-  // also with a contraction long enough for their pipeline (512 experts of 80 rows: 645, short 497);
-  if (r >= (mode == kLinDw ? 1024 : 192) && tiles_about(mode, a, 256) >= 192) return kBig;
+  // 256-row tiles, one a compute unit at a time, where they take fewer rounds than the four times
+  // as many 128-row ones, two at a time: in one round if those need two (2304 x 4096 x 4096: 78; 97,
+  // but 2048 x 4096 x 4096: 87; 70), in more if the last round leaves at most a quarter of them out
+  // (6656 x 4096 x 4096: 188; 210, 8192 x 4096 x 2560: 177; 159); not for groups of less than a tile
+  // nor dw of contractions too short for their pipeline (512 groups of 80 rows: 514; 363);
+  const int64_t t256 = tiles_about(mode, a, 256), rounds = (t256 + 255) / 256;
+  if (r >= (mode == kLinDw ? 1024 : 192) && (rounds == 1 ? t128 > 512 : 4 * t256 >= 3 * 256 * rounds)) return kBig;
   // 32-row tiles with K over the waves where even 64-row ones are few (100 x 8192 x 512: 11.9; 19.7);
   // 64-row tiles where 128-row ones would leave most of the chip idle (256 x 4096 x 4096: 21.6; 25.7),
   // or groups of a few rows, whose weights they stream in more and smaller pieces (512 groups of 4:
@@ -503,8 +508,8 @@ Choice choose(LinearMode mode, const LinearArgs& a, bool f32) {
   // a round of 128-row tiles with four stages (2000 x 2048 x 2048: 19.6; two workgroups of two stages 26.3);
   if (t128 <= 256) return kDeep;
   // dw of short groups, which is loads, a few steps and stores: four workgroups a compute
-  // unit overlap them (512 groups of 80 rows with their dz 542; two 599), for more than a
-  // step or two three of one more stage (80 rows 502, 39 rows 332; four 542 and 305);
+  // unit overlap them, for more than a step or two three of one more stage (512 groups of
+  // 80 rows with their dz 502, of 39 rows 332; four workgroups 542 and 305; two 553 of 80);
   if (mode == kLinDw && r <= 256) return r <= 44 ? kShort : kShort3;
   // groups of one tile read their weights once (512 groups of 80 rows 393; 404), others share them.
   return mode != kLinDw && r <= 128 ? kMidOnce : kMid;
@@ -527,20 +532,18 @@ int64_t grid_of(LinearMode mode, const LinearArgs& a, int& super) {
   return tm * tn;
 }
 
-template <class C>
-hipError_t launch(LinearMode mode, Job j, hipStream_t s) {
-  const dim3 grid((uint32_t)(j.sums + grid_of<C>(mode, j.a, j.super[0])));
-  if (mode == kLinForward) linear_tiles_kernel<kLinForward, -1, C><<<grid, C::NT, 0, s>>>(j);
-  else if (mode == kLinDx) linear_tiles_kernel<kLinDx, -1, C><<<grid, C::NT, 0, s>>>(j);
-  else linear_tiles_kernel<kLinDw, -1, C><<<grid, C::NT, 0, s>>>(j);
+template <int MODE, class C>
+hipError_t launch_as(Job j, hipStream_t s) {
+  const dim3 grid((uint32_t)(j.sums + grid_of<C>((LinearMode)MODE, j.a, j.super[0])));
+  linear_tiles_kernel<MODE, -1, C><<<grid, C::NT, 0, s>>>(j);
   return hipGetLastError();
 }
 
 template <class C>
-hipError_t launch_dw(Job j, hipStream_t s) {  // tiles that dw alone takes
-  const dim3 grid((uint32_t)(j.sums + grid_of<C>(kLinDw, j.a, j.super[0])));
-  linear_tiles_kernel<kLinDw, -1, C><<<grid, C::NT, 0, s>>>(j);
-  return hipGetLastError();
+hipError_t launch(LinearMode mode, const Job& j, hipStream_t s) {
+  return mode == kLinForward ? launch_as<kLinForward, C>(j, s)
+         : mode == kLinDx    ? launch_as<kLinDx, C>(j, s)
+                             : launch_as<kLinDw, C>(j, s);
 }
 
 // dx and dw of a small product side by side, `first` first.
@@ -560,13 +563,14 @@ hipError_t launch_one(LinearMode mode, const Job& j, hipStream_t s) {
   using X = Tiles<F32>;
   const Choice c = choose(mode, j.a, F32);
   if constexpr (!F32) {  // fp32 takes the others alone
-    if (c == kMidOnce) return launch<typename X::MidOnce>(mode, j, s);
+    if (c == kMidOnce)
+      return mode == kLinDx ? launch_as<kLinDx, typename X::MidOnce>(j, s) : launch_as<kLinForward, typename X::MidOnce>(j, s);
     if (c == kDeep) return launch<typename X::Deep>(mode, j, s);
-    if (c == kShort) return launch_dw<typename X::Short>(j, s);
-    if (c == kShort3) return launch_dw<typename X::Short3>(j, s);
-    if (c == kSmallOnce) return launch<typename X::SmallOnce>(mode, j, s);
+    if (c == kShort) return launch_as<kLinDw, typename X::Short>(j, s);
+    if (c == kShort3) return launch_as<kLinDw, typename X::Short3>(j, s);
+    if (c == kSmallOnce) return launch_as<kLinForward, typename X::SmallOnce>(j, s);
+    if (c == kBig) return launch<typename X::Big>(mode, j, s);
   }
-  if (c == kBig) return launch<typename X::Big>(mode, j, s);
   if (c == kMid) return launch<typename X::Mid>(mode, j, s);
   if (c == kSmall) return launch<typename X::Small>(mode, j, s);
   return launch<typename X::Tiny>(mode, j, s);

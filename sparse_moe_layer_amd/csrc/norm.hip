@@ -41,10 +41,12 @@ __device__ __forceinline__ void block_sums(float (&a)[P], float* red, int lane, 
 }
 
 template <bool F32, int NCH>
-__global__ __launch_bounds__(1024) void norm_kernel(NormArgs a) {
+__global__ __launch_bounds__(1024) void norm_kernel(NormArgs a, int T) {
   using V = Vec<F32>;
   __shared__ float red[2][kMaxWaves];
-  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nw = blockDim.x >> 6;
+  const int64_t row = blockIdx.y * (int64_t)gridDim.x + blockIdx.x;
+  if (row >= T) return;
+  const int t = (int)row, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nw = blockDim.x >> 6;
   const int64_t base = (int64_t)t * a.nch;
   const u32x4* f = static_cast<const u32x4*>(a.f);
   const u32x4* resid = static_cast<const u32x4*>(a.resid);
@@ -362,10 +364,11 @@ size_t norm_partial_floats(int64_t T, int64_t H) {
 }
 
 hipError_t launch_norm(const NormArgs& a, int T, bool f32, hipStream_t s) {
+  const dim3 grid = row_grid(T);
 #define MOE_NORM(NCH)                                                                     \
   do {                                                                                    \
-    if (f32) norm_kernel<true, NCH><<<T, threads_of(a.nch, NCH), 0, s>>>(a);              \
-    else norm_kernel<false, NCH><<<T, threads_of(a.nch, NCH), 0, s>>>(a);                 \
+    if (f32) norm_kernel<true, NCH><<<grid, threads_of(a.nch, NCH), 0, s>>>(a, T);        \
+    else norm_kernel<false, NCH><<<grid, threads_of(a.nch, NCH), 0, s>>>(a, T);           \
   } while (0)
   if (a.nch <= 512) MOE_NORM(1);
   else if (a.nch <= 1024) MOE_NORM(2);

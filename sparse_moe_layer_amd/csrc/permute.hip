@@ -106,7 +106,8 @@ __global__ __launch_bounds__(256) void rows_kernel(RowArgs a) {
   using V = Vec<F32>;
   constexpr int U = 4 / ROWS;  // 16-byte pieces of a row that a lane has in flight, each with a sum of its own
   const int lane = threadIdx.x & 63;
-  const int64_t i0 = ((int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * ROWS;
+  const int64_t wg = blockIdx.y * (int64_t)gridDim.x + blockIdx.x;
+  const int64_t i0 = (wg * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * ROWS;
   const int64_t row = (int64_t)a.nch * 16;
   const char *d[ROWS], *in[ROWS];
   char* out[ROWS];
@@ -168,7 +169,7 @@ hipError_t launch_rows(RowArgs a, int T, int per, bool f32, hipStream_t s) {
   a.per = per;
   const bool many = a.nch <= 64;  // rows of one piece a lane
   const int64_t waves = many ? (a.n + 3) / 4 : a.n;
-  const dim3 grid((uint32_t)((waves + 3) / 4));
+  const dim3 grid = row_grid((waves + 3) / 4);
   if (f32 && many) rows_kernel<true, 4><<<grid, 256, 0, s>>>(a);
   else if (f32) rows_kernel<true, 1><<<grid, 256, 0, s>>>(a);
   else if (many) rows_kernel<false, 4><<<grid, 256, 0, s>>>(a);

@@ -60,4 +60,11 @@ __device__ __forceinline__ float wave_sums(float (&a)[P], int lane) {
 // log2 of a power of two
 constexpr int log2_of(int p) { return p <= 1 ? 0 : 1 + log2_of(p / 2); }
 
+// A grid of at least n workgroups of up to 1024 threads, in rows: a dimension holds less
+// than 2^32 threads.
+inline dim3 row_grid(int64_t n) {
+  const int64_t x = n < (1 << 21) ? n : 1 << 21;
+  return dim3((uint32_t)x, (uint32_t)((n + x - 1) / x));
+}
+
 }  // namespace moe
