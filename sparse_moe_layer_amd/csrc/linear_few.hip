@@ -62,6 +62,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void linear_few_kernel(LinearArgs a
       dma16<false>(x, xb, off, l + kPiece + h * 1024);
     }
   };
+  // the epilogue's reads go out first (thread: row tid / 16, column tid % 16)
+  const int er = (tid >> 4) & 15, ec = tid & 15;
+  const int64_t at_y = (int64_t)(t.row + min(er, rows - 1)) * a.N + n0 + min(ec, cols - 1);
+  T e_bias{}, e_mul{}, e_resid{};
+  if (a.bias) e_bias = static_cast<const T*>(a.bias)[(int64_t)t.g * a.N + n0 + min(ec, cols - 1)];
+  if (a.mul) e_mul = static_cast<const T*>(a.mul)[at_y];
+  if (a.resid) e_resid = static_cast<const T*>(a.resid)[at_y];
   const int fr = lane & 15;
   const int o0 = fr * 128 + (((lane >> 4) ^ ((fr >> 1) & 7)) << 4), o1 = fr * 128 + (((4 + (lane >> 4)) ^ ((fr >> 1) & 7)) << 4);
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -100,20 +107,17 @@ __global__ __launch_bounds__(kWaves * 64, 2) void linear_few_kernel(LinearArgs a
 #pragma unroll
   for (int v = 0; v < 4; ++v) red[wave][lane & 15][4 * (lane >> 4) + v] = acc[v];
   __syncthreads();
-  if (tid >= 256) return;
-  const int r = tid >> 4, c = tid & 15;
-  if (r >= rows || c >= cols) return;
+  if (tid >= 256 || er >= rows || ec >= cols) return;
   float z = 0.f;
 #pragma unroll
-  for (int i = 0; i < kWaves; ++i) z += red[i][r][c];
-  const int64_t i = (int64_t)(t.row + r) * a.N + n0 + c;
-  if (a.bias) z += (float)static_cast<const T*>(a.bias)[(int64_t)t.g * a.N + n0 + c];
-  if (a.z) static_cast<T*>(a.z)[i] = (T)z;
+  for (int i = 0; i < kWaves; ++i) z += red[i][er][ec];
+  if (a.bias) z += (float)e_bias;
+  if (a.z) static_cast<T*>(a.z)[at_y] = (T)z;
   float y[1] = {z};
   activate<!F32>(a.act, y);
-  if (a.mul) y[0] *= (float)static_cast<const T*>(a.mul)[i];
-  if (a.resid) y[0] += (float)static_cast<const T*>(a.resid)[i];
-  static_cast<T*>(a.y)[i] = (T)y[0];
+  if (a.mul) y[0] *= (float)e_mul;
+  if (a.resid) y[0] += (float)e_resid;
+  static_cast<T*>(a.y)[at_y] = (T)y[0];
 }
 
 }  // namespace

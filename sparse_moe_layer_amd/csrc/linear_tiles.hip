@@ -201,6 +201,42 @@ __device__ __forceinline__ void spread() {
   }
 }
 
+// What the forward epilogue reads beside the products: bias, factors and residual of a
+// thread's chunks (of W columns, H side by side) in a block of 32 rows.  Places past the
+// tile's rows or columns give values that nothing uses.
+template <class C>
+struct Epilogue {
+  static constexpr int CPR = C::BN / 8, IT = (32 * CPR + C::NT - 1) / C::NT;  // threads a row, a thread's rows of a block
+  static constexpr int H = C::F32 ? 2 : 1, W = 8 / H;
+  struct Block {
+    u32x4 mul[IT][H], resid[IT][H];
+  };
+  using T = typename C::T;
+  const T *mul, *resid;
+  u32x4 bias[H];
+  int row0, last, nn, col[H];
+  __device__ __forceinline__ Epilogue(const LinearArgs& a, int g, int m0, int m1, int n0, int tid)
+      : mul(static_cast<const T*>(a.mul)), resid(static_cast<const T*>(a.resid)), row0(m0 + tid / CPR), last(m1 - 1), nn(a.N) {
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      col[h] = min(n0 + tid % CPR * 8 + h * W, nn - W);  // the same in every row: CPR divides the threads
+      if (a.bias) bias[h] = ld16(static_cast<const T*>(a.bias) + (int64_t)g * nn + col[h]);
+    }
+  }
+  __device__ __forceinline__ void load(Block& b, int block) const {
+    if (mul) get(mul, b.mul, block);
+    if (resid) get(resid, b.resid, block);
+  }
+  __device__ __forceinline__ void get(const T* p, u32x4 (&v)[IT][H], int block) const {
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const int64_t at = (int64_t)min(row0 + block * 32 + it * (C::NT / CPR), last) * nn;
+#pragma unroll
+      for (int h = 0; h < H; ++h) v[it][h] = ld16(p + at + col[h]);
+    }
+  }
+};
+
 // One tile, the bid-th: stg the stages.
 template <int MODE, class C>
 __device__ __forceinline__ void run_tile(const LinearArgs& a, const typename C::T* p, const typename C::T* q,
@@ -268,6 +304,16 @@ __device__ __forceinline__ void run_tile(const LinearArgs& a, const typename C::
     ob.issue(st + C::BM * C::KB, step * C::BK, kn, wave, C::W_ONCE);
   };
 
+  // The epilogue's reads go out a block ahead of their use, small tiles' first block ahead
+  // of everything (8192 x 8192 x 2048 with bias and residual 244 -> 227, 40960 rows of 512 groups of 640 x 2560 520 -> 474).
+  using EX = Epilogue<C>;
+  constexpr bool EARLY = C::BM <= 64;
+  typename EX::Block extra[2];
+  LinearArgs ea = a;
+  if constexpr (MODE != kLinForward) ea.bias = ea.mul = ea.resid = nullptr;
+  const EX ex(ea, g, m0, m1, n0, tid);
+  if constexpr (EARLY) ex.load(extra[0], 0);
+
   f32x16 acc[C::MI][C::NJ];
 #pragma unroll
   for (int i = 0; i < C::MI; ++i)
@@ -321,9 +367,9 @@ __device__ __forceinline__ void run_tile(const LinearArgs& a, const typename C::
   constexpr int ROW = C::BN * (WIDE ? 4 : 2), PER = C::STAGE / (32 * ROW);  // bytes of a row, blocks a stage holds
   constexpr int BPP = C::BM / 32 < C::S * PER ? C::BM / 32 : C::S * PER;    // blocks of a pass
   static_assert(C::BM / 32 % BPP == 0 && BPP % C::WM == 0 && C::WK <= 2 * PER, "whole passes");
-  constexpr int CPR = C::BN / 8;  // threads a row
   constexpr int SWZ = ROW >= 256 ? 15 : 7;
   auto block = [&](int b) { return stg[b / PER] + b % PER * 32 * ROW; };
+  if constexpr (!EARLY) ex.load(extra[0], 0);
 #pragma unroll
   for (int pass = 0; pass < C::BM / 32 / BPP; ++pass) {
     if (pass) lds_sync();
@@ -350,10 +396,13 @@ __device__ __forceinline__ void run_tile(const LinearArgs& a, const typename C::
 #pragma unroll
     for (int b = 0; b < BPP; ++b) {
       const char* f = block(b);
-      for (int e = tid; e < 32 * CPR; e += C::NT) {
-        const int r = e / CPR, c = e % CPR * 8;
-        const int row = m0 + (pass * BPP + b) * 32 + r, col = n0 + c;
-        if (row >= m1 || col >= nn) continue;
+      const int bb = pass * BPP + b;
+      if (bb + 1 < C::BM / 32) ex.load(extra[(bb + 1) & 1], bb + 1);
+#pragma unroll
+      for (int it = 0; it < EX::IT; ++it) {
+        const int e = it * C::NT + tid, r = e / EX::CPR, c = e % EX::CPR * 8;
+        const int row = m0 + bb * 32 + r, col = n0 + c;
+        if (e >= 32 * EX::CPR || row >= m1 || col >= nn) continue;
         const char* fr = f + r * ROW;
         T* o = out + (MODE == kLinDw ? g * a.w_stride : 0) + (int64_t)row * nn + col;
         if constexpr (!WIDE) {
@@ -362,7 +411,7 @@ __device__ __forceinline__ void run_tile(const LinearArgs& a, const typename C::
           else st16(o, v);
         } else {
           // fp32: the last four of the eight columns may be past the end
-          constexpr int H = C::F32 ? 2 : 1, W = 8 / H;
+          constexpr int H = EX::H, W = EX::W;
           using V = Vec<C::F32>;
 #pragma unroll
           for (int h = 0; h < H; ++h) {
@@ -378,22 +427,21 @@ __device__ __forceinline__ void run_tile(const LinearArgs& a, const typename C::
               for (int l = 0; l < 4; ++l) z[k + l] = v[l];
             }
             if constexpr (MODE == kLinForward) {
-              const int64_t at = (int64_t)row * nn + col + h * W;
               float x[W];
               if (a.bias) {
-                V::unpack(ld16(static_cast<const T*>(a.bias) + (int64_t)g * nn + col + h * W), x);
+                V::unpack(ex.bias[h], x);
 #pragma unroll
                 for (int k = 0; k < W; ++k) z[k] += x[k];
               }
-              if (a.z) st16(static_cast<T*>(a.z) + at, V::pack(z));
+              if (a.z) st16(static_cast<T*>(a.z) + (int64_t)row * nn + col + h * W, V::pack(z));
               activate<!C::F32>(a.act, z);
               if (a.mul) {
-                V::unpack(ld16(static_cast<const T*>(a.mul) + at), x);
+                V::unpack(extra[bb & 1].mul[it][h], x);
 #pragma unroll
                 for (int k = 0; k < W; ++k) z[k] *= x[k];
               }
               if (a.resid) {
-                V::unpack(ld16(static_cast<const T*>(a.resid) + at), x);
+                V::unpack(extra[bb & 1].resid[it][h], x);
 #pragma unroll
                 for (int k = 0; k < W; ++k) z[k] += x[k];
               }
