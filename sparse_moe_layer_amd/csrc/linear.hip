@@ -93,11 +93,14 @@ size_t linear_partial_floats(int64_t rows, int64_t N, int64_t G) {
 }
 
 hipError_t launch_linear(const LinearArgs& a, bool f32, hipStream_t s) {
-  // Groups of at most 16 rows with few columns: 16 rows of W a workgroup and K over its waves
-  // (a row of 8192 x 2048: 7.9 us, 64-row tiles 20.1); more of them keep the chip busy in
-  // tiles, which read whole 64-row pieces (ten groups of 2560 x 640: 10.2; 13.5).
-  const int64_t few = (int64_t)(a.G < a.rows ? a.G : a.rows) * ((a.N + 15) / 16);
-  if (a.rows <= 16 * (int64_t)a.G && few <= 256) return launch_linear_few(a, f32, s);
+  // Groups of at most 16 rows with few columns: 16 rows of W a workgroup and K over its 8
+  // waves (a row of 8192 x 2048: 7.9 us, 64-row tiles 20.1).  Twice as many workgroups still
+  // run at once with 4 waves each, better than tiles where those waves are done in a few
+  // pieces and need little of x (ten groups of a row of 2560 x 640: 9.8; 10.3, fp32 14.4;
+  // 17.2, but 8 groups of 4096 x 1024 14.2; 13.4 and with 16 rows each 17.0; 13.4).
+  const int64_t touched = a.G < a.rows ? a.G : a.rows, few = touched * ((a.N + 15) / 16);
+  if (a.rows <= 16 * (int64_t)a.G && few <= 256) return launch_linear_few(a, 8, f32, s);
+  if (a.rows <= 2 * touched && few <= 512 && a.K <= 2560) return launch_linear_few(a, 4, f32, s);
   return launch_linear_tiles(a, f32, s);
 }
 

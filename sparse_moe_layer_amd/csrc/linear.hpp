@@ -154,7 +154,7 @@ struct TileMap {
 inline int max_tiles(int rows, int G, int bm) { return rows / bm + (G < rows ? G : rows); }
 
 // Forward for groups of at most 16 rows.
-hipError_t launch_linear_few(const LinearArgs& a, bool f32, hipStream_t s);
+hipError_t launch_linear_few(const LinearArgs& a, int waves, bool f32, hipStream_t s);
 
 // Sums of the dbias partials: n columns, `splits` each; n == 0: none.
 struct LinearSums {

@@ -1,7 +1,7 @@
 // The forward product for groups of at most 16 rows (single tokens, decode batches):
 //   z[r][n] = sum_k x[r][k] W_g[n][k]
 // bound by reading W_g once.  A workgroup has 16 rows of W (columns of y) and up to
-// 16 rows of x; its waves take every kWaves-th 128 bytes of K, so that all of them
+// 16 rows of x; its waves take every WAVES-th 128 bytes of K, so that all of them
 // stream, and add their sums through LDS.  Both operands come by direct loads (8 rows
 // x 128 bytes each: whole lines, where fragments loaded straight into registers take
 // 16 half lines a load) into LDS that only the wave itself uses, kAhead pieces in flight.
@@ -12,7 +12,7 @@
 namespace moe {
 namespace {
 
-constexpr int kWaves = 8, kAhead = 4;
+constexpr int kAhead = 4;
 constexpr int kFlags = 0x00020000;          // raw 32-bit buffer access
 constexpr uint32_t kNowhere = 0xFFFFFFF0u;  // past every buffer: a load writes zeros
 constexpr int kPiece = 16 * 128;            // bytes of an operand's piece
@@ -23,17 +23,17 @@ __device__ __forceinline__ void dma16(const void* base, uint32_t records, uint32
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)l, 16, off, 0, 0, ONCE ? 2 : 0);
 }
 
-template <bool F32>
-__global__ __launch_bounds__(kWaves * 64, 2) void linear_few_kernel(LinearArgs a) {
+template <bool F32, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, 2) void linear_few_kernel(LinearArgs a) {
   using T = typename std::conditional<F32, float, bf16>::type;
   constexpr int ESZ = sizeof(T), CE = 16 / ESZ, BK = 128 / ESZ;  // values of a chunk, of a row's piece
   // separate arrays: a read of one does not wait for loads into another
-  __shared__ __attribute__((aligned(1024))) char r0[kWaves * 2 * kPiece];
-  __shared__ __attribute__((aligned(1024))) char r1[kWaves * 2 * kPiece];
-  __shared__ __attribute__((aligned(1024))) char r2[kWaves * 2 * kPiece];
-  __shared__ __attribute__((aligned(1024))) char r3[kWaves * 2 * kPiece];
+  __shared__ __attribute__((aligned(1024))) char r0[WAVES * 2 * kPiece];
+  __shared__ __attribute__((aligned(1024))) char r1[WAVES * 2 * kPiece];
+  __shared__ __attribute__((aligned(1024))) char r2[WAVES * 2 * kPiece];
+  __shared__ __attribute__((aligned(1024))) char r3[WAVES * 2 * kPiece];
   static_assert(kAhead == 4, "four arrays");
-  __shared__ float red[kWaves][16][17];
+  __shared__ float red[WAVES][16][17];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tn = (a.N + 15) / 16;
   const TileMap map(a.offsets, a.G, a.rows, 16);
@@ -74,9 +74,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void linear_few_kernel(LinearArgs a
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   const int mine = wave * 2 * kPiece, pieces = (a.K + BK - 1) / BK;
   load(r0 + mine, wave);
-  load(r1 + mine, wave + kWaves);
-  load(r2 + mine, wave + 2 * kWaves);
-  load(r3 + mine, wave + 3 * kWaves);
+  load(r1 + mine, wave + WAVES);
+  load(r2 + mine, wave + 2 * WAVES);
+  load(r3 + mine, wave + 3 * WAVES);
   auto step = [&](char* l, int next) {
     __builtin_amdgcn_s_waitcnt(0xF70 | 4 * (kAhead - 1));  // this piece's four loads have landed
     asm volatile("" ::: "memory");
@@ -96,11 +96,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void linear_few_kernel(LinearArgs a
       acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f1, g1, acc, 0, 0, 0);
     }
   };
-  for (int p = wave; p < pieces; p += kAhead * kWaves) {
-    step(r0 + mine, p + kAhead * kWaves);
-    step(r1 + mine, p + (kAhead + 1) * kWaves);
-    step(r2 + mine, p + (kAhead + 2) * kWaves);
-    step(r3 + mine, p + (kAhead + 3) * kWaves);
+  for (int p = wave; p < pieces; p += kAhead * WAVES) {
+    step(r0 + mine, p + kAhead * WAVES);
+    step(r1 + mine, p + (kAhead + 1) * WAVES);
+    step(r2 + mine, p + (kAhead + 2) * WAVES);
+    step(r3 + mine, p + (kAhead + 3) * WAVES);
   }
   __builtin_amdgcn_s_waitcnt(0xF70);  // the loads past the end have landed too
   // rows 4 (lane / 16) .. + 4 of W, row lane % 16 of x
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void linear_few_kernel(LinearArgs a
   if (tid >= 256 || er >= rows || ec >= cols) return;
   float z = 0.f;
 #pragma unroll
-  for (int i = 0; i < kWaves; ++i) z += red[i][er][ec];
+  for (int i = 0; i < WAVES; ++i) z += red[i][er][ec];
   if (a.bias) z += (float)e_bias;
   if (a.z) static_cast<T*>(a.z)[at_y] = (T)z;
   float y[1] = {z};
@@ -122,10 +122,15 @@ __global__ __launch_bounds__(kWaves * 64, 2) void linear_few_kernel(LinearArgs a
 
 }  // namespace
 
-hipError_t launch_linear_few(const LinearArgs& a, bool f32, hipStream_t s) {
-  const int64_t grid = (int64_t)max_tiles(a.rows, a.G, 16) * ((a.N + 15) / 16);
-  if (f32) linear_few_kernel<true><<<dim3((uint32_t)grid), kWaves * 64, 0, s>>>(a);
-  else linear_few_kernel<false><<<dim3((uint32_t)grid), kWaves * 64, 0, s>>>(a);
+hipError_t launch_linear_few(const LinearArgs& a, int waves, bool f32, hipStream_t s) {
+  const dim3 grid((uint32_t)((int64_t)max_tiles(a.rows, a.G, 16) * ((a.N + 15) / 16)));
+  if (waves == 4) {
+    if (f32) linear_few_kernel<true, 4><<<grid, 256, 0, s>>>(a);
+    else linear_few_kernel<false, 4><<<grid, 256, 0, s>>>(a);
+  } else {
+    if (f32) linear_few_kernel<true, 8><<<grid, 512, 0, s>>>(a);
+    else linear_few_kernel<false, 8><<<grid, 512, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 

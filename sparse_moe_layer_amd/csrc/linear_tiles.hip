@@ -305,7 +305,8 @@ __device__ __forceinline__ void run_tile(const LinearArgs& a, const typename C::
   };
 
   // The epilogue's reads go out a block ahead of their use, small tiles' first block ahead
-  // of everything (8192 x 8192 x 2048 with bias and residual 244 -> 227, 40960 rows of 512 groups of 640 x 2560 520 -> 474).
+  // of everything (8192 x 8192 x 2048 with bias and residual 244 -> 227 us, 512 groups of 80
+  // rows of 640 x 2560 520 -> 474).
   using EX = Epilogue<C>;
   constexpr bool EARLY = C::BM <= 64;
   typename EX::Block extra[2];
@@ -544,7 +545,9 @@ Choice choose(LinearMode mode, const LinearArgs& a, bool f32) {
   // nor dw of contractions too short for their pipeline (512 groups of 80 rows: 514; 363);
   const int64_t t256 = tiles_about(mode, a, 256), rounds = (t256 + 255) / 256;
   if (r >= (mode == kLinDw ? 1024 : 192) && (rounds == 1 ? t128 > 512 : 4 * t256 >= 3 * 256 * rounds)) return kBig;
-  // 32-row tiles with K over the waves where even 64-row ones are few (100 x 8192 x 512: 11.9; 19.7);
+  // 32-row tiles with K over the waves where even 64-row ones are few (100 x 8192 x 512: 11.9; 19.7)
+  // or, as long as caches may hold the weights, groups are of at most 16 rows (16 x 4096 x 6400:
+  // 11.9; 13.5, 30 groups of 2560 x 640: 20.1; 23.7, but ten of 640 x 2560: 10.3; 9.5);
   // 64-row tiles where 128-row ones would leave most of the chip idle (256 x 4096 x 4096: 21.6; 25.7),
   // or groups of a few rows, whose weights they stream in more and smaller pieces (512 groups of 4:
   // 278; 291.  dx, whose rows of W they read in 128-byte pieces, only as long as there are few:
@@ -552,6 +555,7 @@ Choice choose(LinearMode mode, const LinearArgs& a, bool f32) {
   // non-temporally (365 groups of a row or two 185; 202, 38 groups 25.1; 21.7);
   if (tiles_about(mode, a, 64) <= 64) return kTiny;
   if (mode == kLinForward && r <= 64 && touched * a.N * a.K > 100000000) return kSmallOnce;
+  if (mode == kLinForward && r <= 16 && a.K >= 1280) return kTiny;
   if (t128 < 96 || (mode == kLinForward && r <= 64) || (mode == kLinDx && r <= 64 && t128 <= 1024)) return kSmall;
   // a round of 128-row tiles with four stages (2000 x 2048 x 2048: 19.6; two workgroups of two stages 26.3);
   if (t128 <= 256) return kDeep;

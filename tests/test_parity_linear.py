@@ -15,6 +15,7 @@ SHAPES = [(1, 8, 8, 1, "bf16"), (1, 2560, 640, 1, "bf16"), (10, 2560, 136, 16, "
           (17, 8192, 72, 1, "bf16"), (40, 520, 264, 3, "bf16"), (100, 128, 1032, 1, "bf16"), (300, 264, 328, 1, "bf16"),
           (700, 136, 72, 5, "bf16"), (513, 1032, 520, 2, "bf16"), (1030, 320, 264, 1, "bf16"), (2500, 64, 96, 40, "bf16"),
           (30, 72, 64, 1024, "bf16"), (1300, 1416, 256, 1, "bf16"), (70, 4104, 512, 1, "bf16"),
+          (10, 520, 808, 64, "bf16"), (40, 1288, 264, 40, "bf16"), (9, 260, 660, 20, "f32"),
           (1, 4, 4, 1, "f32"), (3, 1100, 36, 1, "f32"), (33, 36, 20, 3, "f32"), (300, 132, 260, 1, "f32"),
           (400, 68, 132, 7, "f32"), (129, 516, 128, 2, "f32")]
 IDS = ["x".join(map(str, s)) for s in SHAPES]

@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 # (rows, K, N, groups, dtype), long in the product's two output sizes and short in its contraction
 FORWARD = [(4090, 136, 3320, 1, "bf16"), (4000, 72, 2568, 5, "bf16"), (2990, 200, 1608, 1, "bf16"),
            (3900, 136, 1000, 40, "bf16"), (1490, 392, 1016, 1, "bf16"), (1000, 520, 600, 1, "bf16"),
-           (600, 520, 1032, 200, "bf16"), (2500, 264, 1800, 60, "bf16"), (16300, 40, 520, 64, "bf16"),
+           (600, 520, 1032, 200, "bf16"), (300, 1288, 520, 40, "bf16"), (10, 2560, 808, 64, "bf16"), (2500, 264, 1800, 60, "bf16"), (16300, 40, 520, 64, "bf16"),
            (4090, 68, 3300, 1, "f32"), (2000, 132, 1028, 1, "f32"), (900, 260, 516, 3, "f32"), (200, 516, 324, 1, "f32"),
            (3900, 68, 516, 40, "f32")]
 DX = [(4090, 3320, 136, 1, "bf16"), (4000, 2568, 72, 5, "bf16"), (2990, 1608, 200, 1, "bf16"),
@@ -62,6 +62,35 @@ def test_forward(rows, K, N, G, dt):
             xd, wd = x[a:b].double(), w[g].double().T.contiguous()
             check(y[a:b], xd @ wd, xd.abs() @ wd.abs(), K, dt, f"group {g}")
     assert bool(torch.isnan(y[~inside]).all())
+
+
+@pytest.mark.parametrize("rows,K,N,G,dt", FORWARD, ids=ids(FORWARD))
+def test_epilogue(rows, K, N, G, dt):
+    """bias, SiLU, factor and residual at the same sizes, over the factor's own tensor too."""
+    print(f"[epilogue] {rows} {K} {N} {G} {dt}", flush=True)
+    x, w, mul, off = tensors(rows, K, N, G, dt)
+    resid, bias = mul.flip(1).contiguous(), torch.linspace(-1, 1, G * N, device="cuda").view(G, N).to(DT[dt])
+    y, z = torch.full_like(mul, float("nan")), torch.full_like(mul, float("nan"))
+    p = lib.linear_problem(rows, K, N, G, dt, "silu")
+    lib.moe_linear(p, x, w, bias, off, mul, resid, y, z)
+    inside = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    for g, (a, b) in enumerate(spans(off, rows)):
+        inside[a:b] = True
+        if b == a:
+            continue
+        xd, wd, bd = x[a:b].double(), w[g].double().T.contiguous(), bias[g].double()
+        m, r, want = mul[a:b].double(), resid[a:b].double(), xd @ wd + bd
+        size = xd.abs() @ wd.abs() + bd.abs()
+        check(z[a:b], want, size, K + 1, dt, f"z of group {g}")
+        # SiLU's slope is at most 1.1; 16 steps in fp32 for it, two more for the product and the sum
+        v = want * torch.sigmoid(want)
+        bound = m.abs() * (1.1 * (K + 3) * F * size + 18 * F * v.abs()) + 2 * F * r.abs() + half(dt) * (r + v * m).abs()
+        err = (y[a:b].double() - (r + v * m)).abs()
+        assert bool((err <= bound).all()), f"y of group {g}: {float((err / bound.clamp_min(1e-300)).max()):.2f} bounds off"
+    assert bool(torch.isnan(y[~inside]).all())
+    before = mul.clone()
+    lib.moe_linear(p, x, w, bias, off, mul, resid, mul, None)
+    assert same_bits(mul[inside], y[inside]) and same_bits(mul[~inside], before[~inside])
 
 
 @pytest.mark.parametrize("rows,K,N,G,dt", DX, ids=ids(DX))
