@@ -169,7 +169,7 @@ moe_status moe_linear(const moe_linear_problem* p, const void* x, const void* w,
 
 size_t moe_linear_workspace_bytes(const moe_linear_problem* p) {
   if (check_linear(p) != MOE_OK) return 0;
-  return dz_bytes(p) + up(moe::linear_partial_floats(p->rows, p->N, p->groups) * 4) + kAlign;
+  return dz_bytes(p) + up(moe::linear_partial_floats(p->rows, p->N, p->groups, p->dtype == MOE_F32) * 4) + kAlign;
 }
 
 moe_status moe_linear_backward(const moe_linear_problem* p, const void* dy, const void* x, const void* w,

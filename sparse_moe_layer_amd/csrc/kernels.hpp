@@ -265,7 +265,7 @@ struct LinearBackArgs {
   int64_t w_stride;
   int act;
 };
-size_t linear_partial_floats(int64_t rows, int64_t N, int64_t G);
+size_t linear_partial_floats(int64_t rows, int64_t N, int64_t G, bool f32);
 hipError_t launch_linear_backward(const LinearBackArgs& a, bool f32, hipStream_t s);
 
 // Gated residual read / write (bf16).

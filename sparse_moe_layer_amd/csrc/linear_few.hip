@@ -1,10 +1,12 @@
-// The forward product for groups of at most 16 rows (single tokens, decode batches):
+// The forward product for groups of few rows (single tokens, decode batches):
 //   z[r][n] = sum_k x[r][k] W_g[n][k]
 // bound by reading W_g once.  A workgroup has 16 rows of W (columns of y) and up to
 // 16 rows of x; its waves take every WAVES-th 128 bytes of K, so that all of them
 // stream, and add their sums through LDS.  Both operands come by direct loads (8 rows
 // x 128 bytes each: whole lines, where fragments loaded straight into registers take
 // 16 half lines a load) into LDS that only the wave itself uses, kAhead pieces in flight.
+// A row of 8192 x 2048 (34 MB): 7.9 us, 4.3 TB/s with the launch; ten groups of 2560 x 640
+// (33 MB): 9.8 us, of which 2 the launch and 1 the search for the groups.
 #include "linear.hpp"
 
 #include <type_traits>

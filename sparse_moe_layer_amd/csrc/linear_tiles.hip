@@ -4,6 +4,13 @@
 //   forward  z = x W_g^T     A = x  [r][k],  B = W [n][k]     (contracted along rows of both)
 //   dx       dz W_g          A = dz [r][n],  B = W [n][k]     (B contracted along its columns)
 //   dw       dz^T x          A = dz [r][n],  B = x [r][k]     (both contracted along their columns)
+// Stages of both operands arrive in LDS by direct loads, S - 1 of them ahead; fragments are
+// read a sub-step ahead of the matrix instructions, whose last sub-step is carried past the
+// barrier.  Bound by the matrix rate at the clock that the power limit leaves (8192 x 8192 x
+// 2048 bf16: 208 to 233 us, 1.2 to 1.3 PFLOP/s, the library's product 200 to 205; fp32
+// 4096 x 4096 x 4096 918 us, 0.150 PFLOP/s, the library 0.154 at 8192) or, for groups of few
+// rows, by reading or writing each weight once (512 groups of 80 rows of 2560 x 640, 1.94 GB:
+// forward 338 us, dx 420, dw 500).
 #include "linear.hpp"
 
 #include <type_traits>
@@ -463,10 +470,8 @@ struct Job {
   const void *p, *q[2];
   void* out[2];
   int super[2];
-  int sums, second;  // first workgroups of the first and the second product
-  const float* partial;
-  float* dbias;
-  int n, splits;
+  int first, second;  // first workgroups of the two products
+  LinearSums sums;
 };
 
 // M1, M2: the products' modes (M2 < 0: one product).
@@ -481,13 +486,15 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
   char* stg[4];
   stg[0] = s0, stg[1] = s1, stg[2] = s2, stg[3] = s3;
   const int bid = blockIdx.x;
-  if (M1 != kLinForward && bid < j.sums) {
-    add_partials(j.partial, j.dbias, j.n, j.splits, bid);
-    return;
+  if constexpr (M1 != kLinForward) {
+    if (bid < j.first) {
+      add_partials(j.sums, bid);
+      return;
+    }
   }
   const T* p = static_cast<const T*>(j.p);
   if (M2 < 0 || bid < j.second)
-    run_tile<M1, C>(j.a, p, static_cast<const T*>(j.q[0]), static_cast<T*>(j.out[0]), j.super[0], bid - j.sums, stg);
+    run_tile<M1, C>(j.a, p, static_cast<const T*>(j.q[0]), static_cast<T*>(j.out[0]), j.super[0], bid - j.first, stg);
   else if constexpr (M2 >= 0)
     run_tile<M2, C>(j.a, p, static_cast<const T*>(j.q[1]), static_cast<T*>(j.out[1]), j.super[1], bid - j.second, stg);
 }
@@ -586,7 +593,7 @@ int64_t grid_of(LinearMode mode, const LinearArgs& a, int& super) {
 
 template <int MODE, class C>
 hipError_t launch_as(Job j, hipStream_t s) {
-  const dim3 grid((uint32_t)(j.sums + grid_of<C>((LinearMode)MODE, j.a, j.super[0])));
+  const dim3 grid((uint32_t)(j.first + grid_of<C>((LinearMode)MODE, j.a, j.super[0])));
   linear_tiles_kernel<MODE, -1, C><<<grid, C::NT, 0, s>>>(j);
   return hipGetLastError();
 }
@@ -601,7 +608,7 @@ hipError_t launch(LinearMode mode, const Job& j, hipStream_t s) {
 // dx and dw of a small product side by side, `first` first.
 template <class C>
 hipError_t launch_both(LinearMode first, Job j, hipStream_t s) {
-  const int64_t n = j.sums + grid_of<C>(first, j.a, j.super[0]);
+  const int64_t n = j.first + grid_of<C>(first, j.a, j.super[0]);
   j.second = (int)((n + 7) / 8 * 8);  // its first workgroup on XCD 0 too
   const LinearMode other = first == kLinDx ? kLinDw : kLinDx;
   const dim3 grid((uint32_t)(j.second + grid_of<C>(other, j.a, j.super[1])));
@@ -634,12 +641,8 @@ hipError_t launch_back(const LinearArgs& a, const void* dz, const void* w, const
   Job j{};
   j.a = a;
   j.p = dz;
-  j.partial = sums.partial;
-  j.dbias = sums.dbias;
-  j.n = sums.n;
-  j.splits = sums.splits;
-  j.sums = (sums.n + 255) / 256;
-  j.sums = (j.sums + 7) / 8 * 8;  // the first tile on XCD 0
+  j.sums = sums;
+  j.first = sums.n ? (sums.workgroups() + 7) / 8 * 8 : 0;  // the first tile on XCD 0
   // Small products side by side in one launch (1000 x 1416 x 2056 with its dz: 54.0 -> 34.5 us).
   if (dx && dw) {
     const Choice c = choose(kLinDx, a, F32);
@@ -662,7 +665,7 @@ hipError_t launch_back(const LinearArgs& a, const void* dz, const void* w, const
     j.q[0] = w;
     j.out[0] = dx;
     e = launch_one<F32>(kLinDx, j, s);
-    j.sums = 0;
+    j.first = 0;
   }
   if (dw && e == hipSuccess) {
     j.q[0] = x;

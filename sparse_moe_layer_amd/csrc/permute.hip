@@ -12,7 +12,9 @@
 namespace moe {
 namespace {
 
-// One thread per 16 bytes of x; n = T * (chunks of a row).
+// One thread per 16 bytes of x, its k stores one after the other: bound by the writes, whole
+// lines of a row next to each other (4096 x 2560 x 10 bf16, 0.23 GB: 45 us, 5.1 TB/s; the
+// copy of a large tensor reaches 4.9).  n = T * (chunks of a row).
 template <bool F32, bool W>
 __global__ __launch_bounds__(256) void permute_kernel(const char* __restrict__ x, const int32_t* __restrict__ pos,
                                                       const float* __restrict__ w, char* __restrict__ xs, int n,
@@ -41,7 +43,8 @@ __global__ __launch_bounds__(256) void permute_kernel(const char* __restrict__ x
   }
 }
 
-// dx alone: one thread per 16 bytes of dx.
+// dx alone: one thread per 16 bytes of dx, KB rows' loads in flight and summed in order
+// (4096 x 2560 x 10, 0.23 GB read and 0.02 written: 44 us, 5.3 TB/s).
 template <bool F32, bool W, int KB>
 __global__ __launch_bounds__(256) void unpermute_kernel(const char* __restrict__ dxs, const int32_t* __restrict__ pos,
                                                         const float* __restrict__ w, char* __restrict__ dx, int n,
@@ -83,7 +86,8 @@ __device__ __forceinline__ float sigmoid_f32(float z) { return 1.f / (1.f + expf
 // token: out = w * dout[t], dot = <dout[t], in>.  A wave has ROWS rows (short ones several
 // at a time).  A token's rows follow each other, so dout comes from the caches for all
 // but the first; nothing is shared between waves (4096 x 2560 x 10: 80 us; a workgroup per
-// token with its rows in registers 146).  Without dy only the products (x and dxs of
+// token with its rows in registers 146; with the shared expert 100 us, 0.48 GB, half of it
+// writes, at 4.8 TB/s).  Without dy only the products (x and dxs of
 // permute's gradient).
 struct RowArgs {
   const char *dout, *y;
