@@ -645,8 +645,10 @@ hipError_t launch_back(const LinearArgs& a, const void* dz, const void* w, const
   j.first = sums.n ? (sums.workgroups() + 7) / 8 * 8 : 0;  // the first tile on XCD 0
   // Small products side by side in one launch (1000 x 1416 x 2056 with its dz: 54.0 -> 34.5 us).
   if (dx && dw) {
-    const Choice c = choose(kLinDx, a, F32);
-    if ((c == kTiny || c == kSmall || c == kDeep) && choose(kLinDw, a, F32) == c) {
+    Choice c = choose(kLinDx, a, F32);
+    const Choice o = choose(kLinDw, a, F32);
+    if ((c == kSmall && o == kDeep) || (c == kDeep && o == kSmall)) c = kSmall;
+    if (c == kTiny ? o == c : c == kSmall ? o == kSmall || o == kDeep : c == kDeep && o == c) {
       // the longer contraction first
       const bool x_first = a.N >= group_mean(a);
       j.q[0] = x_first ? w : x;
