@@ -208,39 +208,33 @@ __device__ __forceinline__ void spread() {
   }
 }
 
-// What the forward epilogue reads beside the products: bias, factors and residual of a
-// thread's chunks (of W columns, H side by side) in a block of 32 rows.  Places past the
-// tile's rows or columns give values that nothing uses.
+// A thread's places in the epilogue: one 16-byte chunk of IT rows of each block of 32, so that
+// a wave's accesses are whole lines (fp32 with two chunks a thread: dw of 379 groups of 464 x
+// 180 84 us; 42).  And what the forward epilogue reads there beside the products: bias,
+// factors and residual.  Places past the tile's rows or columns give values that nothing uses.
 template <class C>
 struct Epilogue {
-  static constexpr int CPR = C::BN / 8, IT = (32 * CPR + C::NT - 1) / C::NT;  // threads a row, a thread's rows of a block
-  static constexpr int H = C::F32 ? 2 : 1, W = 8 / H;
+  static constexpr int W = C::CE, CPR = C::BN / W, IT = (32 * CPR + C::NT - 1) / C::NT;  // threads a row
   struct Block {
-    u32x4 mul[IT][H], resid[IT][H];
+    u32x4 mul[IT], resid[IT];
   };
   using T = typename C::T;
   const T *mul, *resid;
-  u32x4 bias[H];
-  int row0, last, nn, col[H];
+  u32x4 bias;
+  int row0, last, nn, col;
   __device__ __forceinline__ Epilogue(const LinearArgs& a, int g, int m0, int m1, int n0, int tid)
-      : mul(static_cast<const T*>(a.mul)), resid(static_cast<const T*>(a.resid)), row0(m0 + tid / CPR), last(m1 - 1), nn(a.N) {
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      col[h] = min(n0 + tid % CPR * 8 + h * W, nn - W);  // the same in every row: CPR divides the threads
-      if (a.bias) bias[h] = ld16(static_cast<const T*>(a.bias) + (int64_t)g * nn + col[h]);
-    }
+      : mul(static_cast<const T*>(a.mul)), resid(static_cast<const T*>(a.resid)), row0(m0 + tid / CPR), last(m1 - 1),
+        nn(a.N), col(min(n0 + tid % CPR * W, a.N - W)) {  // the same column in every row: CPR divides the threads
+    if (a.bias) bias = ld16(static_cast<const T*>(a.bias) + (int64_t)g * nn + col);
   }
   __device__ __forceinline__ void load(Block& b, int block) const {
     if (mul) get(mul, b.mul, block);
     if (resid) get(resid, b.resid, block);
   }
-  __device__ __forceinline__ void get(const T* p, u32x4 (&v)[IT][H], int block) const {
+  __device__ __forceinline__ void get(const T* p, u32x4 (&v)[IT], int block) const {
 #pragma unroll
-    for (int it = 0; it < IT; ++it) {
-      const int64_t at = (int64_t)min(row0 + block * 32 + it * (C::NT / CPR), last) * nn;
-#pragma unroll
-      for (int h = 0; h < H; ++h) v[it][h] = ld16(p + at + col[h]);
-    }
+    for (int it = 0; it < IT; ++it)
+      v[it] = ld16(p + (int64_t)min(row0 + block * 32 + it * (C::NT / CPR), last) * nn + col);
   }
 };
 
@@ -368,7 +362,7 @@ __device__ __forceinline__ void run_tile(const LinearArgs& a, const typename C::
   block_sync();
 
   // ---- epilogue: blocks of 32 rows go through LDS (bf16 gradients as bf16, the rest as
-  // fp32, so that z is rounded once), so that a thread has 8 values side by side.  A lane
+  // fp32, so that z is rounded once), so that a thread has 16 bytes of a row side by side.  A lane
   // holds row lane % 32 of a block and columns 8 q + 4 (lane / 32) .. + 4; 16-byte chunk c
   // of row r sits at c ^ (r & 15) (& 7 in a row of 8), so 16 rows' writes cover the banks. ----
   constexpr bool WIDE = MODE == kLinForward || C::F32 || C::WK > 1;
@@ -408,56 +402,50 @@ __device__ __forceinline__ void run_tile(const LinearArgs& a, const typename C::
       if (bb + 1 < C::BM / 32) ex.load(extra[(bb + 1) & 1], bb + 1);
 #pragma unroll
       for (int it = 0; it < EX::IT; ++it) {
-        const int e = it * C::NT + tid, r = e / EX::CPR, c = e % EX::CPR * 8;
+        const int e = it * C::NT + tid, r = e / EX::CPR, c = e % EX::CPR * EX::W;
         const int row = m0 + bb * 32 + r, col = n0 + c;
         if (e >= 32 * EX::CPR || row >= m1 || col >= nn) continue;
         const char* fr = f + r * ROW;
         T* o = out + (MODE == kLinDw ? g * a.w_stride : 0) + (int64_t)row * nn + col;
+        u32x4 v;
         if constexpr (!WIDE) {
-          const u32x4 v = ld16(fr + (((c >> 3) ^ (r & SWZ)) << 4));
-          if constexpr (MODE == kLinDw) st16_nt(o, v);
-          else st16(o, v);
+          v = ld16(fr + (((c >> 3) ^ (r & SWZ)) << 4));
         } else {
-          // fp32: the last four of the eight columns may be past the end
-          constexpr int H = EX::H, W = EX::W;
           using V = Vec<C::F32>;
+          float z[EX::W];
 #pragma unroll
-          for (int h = 0; h < H; ++h) {
-            if (h && col + W >= nn) continue;
-            float z[W];
+          for (int k = 0; k < EX::W; k += 4) {
+            const int at = (((c + k) >> 2) ^ (r & SWZ)) << 4;
+            f32x4 q = *reinterpret_cast<const f32x4*>(fr + at);
 #pragma unroll
-            for (int k = 0; k < W; k += 4) {
-              f32x4 v = *reinterpret_cast<const f32x4*>(fr + ((((c >> 2) + h + k / 4) ^ (r & SWZ)) << 4));
+            for (int w = 1; w < C::WK; ++w) q += *reinterpret_cast<const f32x4*>(block(w) + r * ROW + at);
 #pragma unroll
-              for (int w = 1; w < C::WK; ++w)
-                v += *reinterpret_cast<const f32x4*>(block(w) + r * ROW + ((((c >> 2) + h + k / 4) ^ (r & SWZ)) << 4));
-#pragma unroll
-              for (int l = 0; l < 4; ++l) z[k + l] = v[l];
-            }
-            if constexpr (MODE == kLinForward) {
-              float x[W];
-              if (a.bias) {
-                V::unpack(ex.bias[h], x);
-#pragma unroll
-                for (int k = 0; k < W; ++k) z[k] += x[k];
-              }
-              if (a.z) st16(static_cast<T*>(a.z) + (int64_t)row * nn + col + h * W, V::pack(z));
-              activate<!C::F32>(a.act, z);
-              if (a.mul) {
-                V::unpack(extra[bb & 1].mul[it][h], x);
-#pragma unroll
-                for (int k = 0; k < W; ++k) z[k] *= x[k];
-              }
-              if (a.resid) {
-                V::unpack(extra[bb & 1].resid[it][h], x);
-#pragma unroll
-                for (int k = 0; k < W; ++k) z[k] += x[k];
-              }
-            }
-            if constexpr (MODE == kLinDw) st16_nt(o + h * W, V::pack(z));
-            else st16(o + h * W, V::pack(z));
+            for (int l = 0; l < 4; ++l) z[k + l] = q[l];
           }
+          if constexpr (MODE == kLinForward) {
+            float x[EX::W];
+            if (a.bias) {
+              V::unpack(ex.bias, x);
+#pragma unroll
+              for (int k = 0; k < EX::W; ++k) z[k] += x[k];
+            }
+            if (a.z) st16(static_cast<T*>(a.z) + (int64_t)row * nn + col, V::pack(z));
+            activate<!C::F32>(a.act, z);
+            if (a.mul) {
+              V::unpack(extra[bb & 1].mul[it], x);
+#pragma unroll
+              for (int k = 0; k < EX::W; ++k) z[k] *= x[k];
+            }
+            if (a.resid) {
+              V::unpack(extra[bb & 1].resid[it], x);
+#pragma unroll
+              for (int k = 0; k < EX::W; ++k) z[k] += x[k];
+            }
+          }
+          v = V::pack(z);
         }
+        if constexpr (MODE == kLinDw) st16_nt(o, v);
+        else st16(o, v);
       }
     }
   }
@@ -474,15 +462,17 @@ struct Job {
   LinearSums sums;
 };
 
-// M1, M2: the products' modes (M2 < 0: one product).
-template <int M1, int M2, class C>
-__global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_kernel(Job j) {
-  using T = typename C::T;
+// M1, M2: the products' modes (M2 < 0: one product), C1, C2 their tiles.
+template <int M1, int M2, class C1, class C2 = C1>
+__global__ __launch_bounds__(C1::NT, C1::NW * (C1::WG_PER_CU < C2::WG_PER_CU ? C1::WG_PER_CU : C2::WG_PER_CU) / 4)
+void linear_tiles_kernel(Job j) {
+  using T = typename C1::T;
+  constexpr int STAGE = C1::STAGE > C2::STAGE ? C1::STAGE : C2::STAGE, S = C1::S > C2::S ? C1::S : C2::S;
   // separate arrays: a read of one stage does not wait for loads into another
-  __shared__ __attribute__((aligned(1024))) char s0[C::STAGE];
-  __shared__ __attribute__((aligned(1024))) char s1[C::STAGE];
-  __shared__ __attribute__((aligned(1024))) char s2[C::S > 2 ? C::STAGE : 16];
-  __shared__ __attribute__((aligned(1024))) char s3[C::S > 3 ? C::STAGE : 16];
+  __shared__ __attribute__((aligned(1024))) char s0[STAGE];
+  __shared__ __attribute__((aligned(1024))) char s1[STAGE];
+  __shared__ __attribute__((aligned(1024))) char s2[S > 2 ? STAGE : 16];
+  __shared__ __attribute__((aligned(1024))) char s3[S > 3 ? STAGE : 16];
   char* stg[4];
   stg[0] = s0, stg[1] = s1, stg[2] = s2, stg[3] = s3;
   const int bid = blockIdx.x;
@@ -494,9 +484,9 @@ __global__ __launch_bounds__(C::NT, C::NW * C::WG_PER_CU / 4) void linear_tiles_
   }
   const T* p = static_cast<const T*>(j.p);
   if (M2 < 0 || bid < j.second)
-    run_tile<M1, C>(j.a, p, static_cast<const T*>(j.q[0]), static_cast<T*>(j.out[0]), j.super[0], bid - j.first, stg);
+    run_tile<M1, C1>(j.a, p, static_cast<const T*>(j.q[0]), static_cast<T*>(j.out[0]), j.super[0], bid - j.first, stg);
   else if constexpr (M2 >= 0)
-    run_tile<M2, C>(j.a, p, static_cast<const T*>(j.q[1]), static_cast<T*>(j.out[1]), j.super[1], bid - j.second, stg);
+    run_tile<M2, C2>(j.a, p, static_cast<const T*>(j.q[1]), static_cast<T*>(j.out[1]), j.super[1], bid - j.second, stg);
 }
 
 template <bool F32>
@@ -536,9 +526,15 @@ Choice choose(LinearMode mode, const LinearArgs& a, bool f32) {
       Choice c;
     };
     const Size sizes[] = {{32, 1.2, kTiny}, {64, 1.05, kSmall}, {128, 1.0, kMid}};
+    // But dw of short groups is mostly stores, of the longest rows in 128-row tiles (17 groups of
+    // three rows of 968 x 2400: 47.7; 64 rows 59.0, 30 groups of 33 rows of 512 x 1024: 25.8; 30.4),
+    // or of a few tiles that run beside dx (16 x 2048 x 2048 with dx: 16.9; 22.8).
+    const bool stores = mode == kLinDw && r <= 64;
+    if (stores && t128 > 256) return kMid;
     Choice best = kTiny;
     double least = 1e30;
     for (const Size& z : sizes) {
+      if (stores && z.c == kMid) continue;
       const double work = (double)((tiles_about(mode, a, z.b) + 255) / 256) * z.b * z.b * z.cost;
       if (work < least) least = work, best = z.c;
     }
@@ -605,15 +601,14 @@ hipError_t launch(LinearMode mode, const Job& j, hipStream_t s) {
                              : launch_as<kLinDw, C>(j, s);
 }
 
-// dx and dw of a small product side by side, `first` first.
-template <class C>
-hipError_t launch_both(LinearMode first, Job j, hipStream_t s) {
-  const int64_t n = j.first + grid_of<C>(first, j.a, j.super[0]);
-  j.second = (int)((n + 7) / 8 * 8);  // its first workgroup on XCD 0 too
-  const LinearMode other = first == kLinDx ? kLinDw : kLinDx;
-  const dim3 grid((uint32_t)(j.second + grid_of<C>(other, j.a, j.super[1])));
-  if (first == kLinDx) linear_tiles_kernel<kLinDx, kLinDw, C><<<grid, C::NT, 0, s>>>(j);
-  else linear_tiles_kernel<kLinDw, kLinDx, C><<<grid, C::NT, 0, s>>>(j);
+// dx and dw of a small product side by side, in tiles X and W, dx first or dw.
+template <class X, class W>
+hipError_t launch_both(bool x_first, Job j, hipStream_t s) {
+  const int64_t x = grid_of<X>(kLinDx, j.a, j.super[!x_first]), w = grid_of<W>(kLinDw, j.a, j.super[x_first]);
+  j.second = (int)((j.first + (x_first ? x : w) + 7) / 8 * 8);  // its first workgroup on XCD 0 too
+  const dim3 grid((uint32_t)(j.second + (x_first ? w : x)));
+  if (x_first) linear_tiles_kernel<kLinDx, kLinDw, X, W><<<grid, X::NT, 0, s>>>(j);
+  else linear_tiles_kernel<kLinDw, kLinDx, W, X><<<grid, X::NT, 0, s>>>(j);
   return hipGetLastError();
 }
 
@@ -644,25 +639,25 @@ hipError_t launch_back(const LinearArgs& a, const void* dz, const void* w, const
   j.sums = sums;
   j.first = sums.n ? (sums.workgroups() + 7) / 8 * 8 : 0;  // the first tile on XCD 0
   // Small products side by side in one launch (1000 x 1416 x 2056 with its dz: 54.0 -> 34.5
-  // us), where one would take 64-row tiles and the other 128-row ones both with 64 (8192 x 512
-  // x 1024: 57.2 -> 48.0).  The sums are the same: K in the same steps.
+  // us, 9 x 200 x 2480 12.1 -> 8.5), where only one would take 128-row tiles both with smaller
+  // ones (8192 x 512 x 1024: 57.2 -> 48.0).  The results are those of each alone:
+  // 64 and 128 rows take K in the same steps.
   if (dx && dw) {
-    const Choice cx = choose(kLinDx, a, F32), cw = choose(kLinDw, a, F32);
-    const bool mixed = (cx == kSmall && cw == kDeep) || (cx == kDeep && cw == kSmall);
-    const Choice c = mixed ? kSmall : cx;
-    if (mixed || (cx == cw && (c == kTiny || c == kSmall || c == kDeep))) {
-      // the longer contraction first
-      const bool x_first = a.N >= group_mean(a);
-      j.q[0] = x_first ? w : x;
-      j.q[1] = x_first ? x : w;
-      j.out[0] = x_first ? dx : dw;
-      j.out[1] = x_first ? dw : dx;
-      const LinearMode first = x_first ? kLinDx : kLinDw;
-      if (c == kTiny) return launch_both<typename Tiles<F32>::Tiny>(first, j, s);
-      if constexpr (!F32)
-        if (c == kDeep) return launch_both<typename Tiles<F32>::Deep>(first, j, s);
-      return launch_both<typename Tiles<F32>::Small>(first, j, s);
-    }
+    using X = Tiles<F32>;
+    Choice cx = choose(kLinDx, a, F32), cw = choose(kLinDw, a, F32);
+    if (cx != kDeep && cw == kDeep) cw = kSmall;
+    if (cx == kDeep && cw != kDeep) cx = kSmall;
+    const bool x_first = a.N >= group_mean(a);  // the longer contraction first
+    j.q[0] = x_first ? w : x;
+    j.q[1] = x_first ? x : w;
+    j.out[0] = x_first ? dx : dw;
+    j.out[1] = x_first ? dw : dx;
+    if (cx == kTiny && cw == kTiny) return launch_both<typename X::Tiny, typename X::Tiny>(x_first, j, s);
+    if (cx == kTiny && cw == kSmall) return launch_both<typename X::Tiny, typename X::Small>(x_first, j, s);
+    if (cx == kSmall && cw == kTiny) return launch_both<typename X::Small, typename X::Tiny>(x_first, j, s);
+    if (cx == kSmall && cw == kSmall) return launch_both<typename X::Small, typename X::Small>(x_first, j, s);
+    if constexpr (!F32)
+      if (cx == kDeep && cw == kDeep) return launch_both<typename X::Deep, typename X::Deep>(x_first, j, s);
   }
   hipError_t e = hipSuccess;
   if (dx) {
