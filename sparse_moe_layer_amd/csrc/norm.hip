@@ -301,7 +301,7 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormBackArgs a, int t
   const int H = a.nch * V::N;
   float* p = a.partial + (int64_t)blockIdx.x * a.sums * H;
   __shared__ __attribute__((aligned(16))) float other[NCH == 1 ? NT * V::N : 4];
-  auto put = [&](float (&s)[NCH][V::N]) {
+  auto put = [&](float (&s)[NCH][V::N], float* alone) {
     if constexpr (NCH == 1) {
       if (groups > 1) {
         __syncthreads();
@@ -319,6 +319,11 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormBackArgs a, int t
       for (int i = 0; i < NCH; ++i) {
         const int c = me + i * tpr;
         if (c >= a.nch) continue;
+        if (gridDim.x == 1) {  // the sums themselves, at any 4 bytes
+#pragma unroll
+          for (int e = 0; e < V::N; ++e) alone[c * V::N + e] = s[i][e];
+          continue;
+        }
 #pragma unroll
         for (int e = 0; e < V::N; e += 4)
           *reinterpret_cast<f32x4*>(p + c * V::N + e) = f32x4{s[i][e], s[i][e + 1], s[i][e + 2], s[i][e + 3]};
@@ -327,11 +332,11 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormBackArgs a, int t
     p += H;
   };
   if constexpr (POST) {
-    if (a.dg_post) put(s_post);
+    if (a.dg_post) put(s_post, a.dg_post);
   }
-  if (a.dg_pre) put(s_pre);
+  if (a.dg_pre) put(s_pre, a.dg_pre);
   if constexpr (GATE == MOE_GATE_CHANNEL) {
-    if (a.dgate) put(s_gate);
+    if (a.dgate) put(s_gate, static_cast<float*>(a.dgate));
   }
 }
 
@@ -396,6 +401,7 @@ static void back_kernel(const NormBackArgs& a, int& grid, hipStream_t s) {
   const int tpr = threads_of(a.nch, NCH), groups = NCH == 1 && tpr < NT ? NT / tpr : 1;
   grid = (a.T + groups - 1) / groups;
   grid = grid < kNormMaxPartials ? grid : kNormMaxPartials;
+  if (grid == 2) grid = 1;  // a second round of rows takes less than a launch for the sums (6 x 2560 11.3 -> 9.7 us)
   if (a.g_post) back_kernel<F32, NCH, NT, true>(a, grid, groups * tpr, tpr, s);
   else back_kernel<F32, NCH, NT, false>(a, grid, groups * tpr, tpr, s);
 }
@@ -405,19 +411,22 @@ hipError_t launch_norm_backward(NormBackArgs a, bool f32, hipStream_t s) {
   a.sums = (a.dg_post != nullptr) + (a.dg_pre != nullptr) + (a.gate_kind == MOE_GATE_CHANNEL && a.dgate);
   int grid = 0;
   if (f32) {
-    if (a.nch <= 448) back_kernel<true, 1, 1024>(a, grid, s);
+    if (a.nch <= 448) back_kernel<true, 1, 1024>(a, grid, s);  // rows that leave no wave idle
     else if (a.nch <= 512) back_kernel<true, 1, 512>(a, grid, s);
     else if (a.nch <= 1024) back_kernel<true, 2, 512>(a, grid, s);
     else if (a.nch <= 2048) back_kernel<true, 4, 512>(a, grid, s);
     else back_kernel<true, 4, 1024>(a, grid, s);
   } else {
-    if (a.nch <= 448) back_kernel<false, 1, 1024>(a, grid, s);
+    // 1024 threads where their 128 registers hold the sums (4096 x 2560, token's gate: 31.5 us,
+    // 512 threads 33.8; full gate behind a post norm: 51.4, 40.9; channel's 46.1, 38.5)
+    const bool few = !a.g_post || a.gate_kind < MOE_GATE_CHANNEL;
+    if (a.nch <= 448 && few) back_kernel<false, 1, 1024>(a, grid, s);
     else if (a.nch <= 512) back_kernel<false, 1, 512>(a, grid, s);
     else if (a.nch <= 1024) back_kernel<false, 2, 512>(a, grid, s);
     else back_kernel<false, 4, 512>(a, grid, s);
   }
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.sums == 0) return e;
+  if (e != hipSuccess || a.sums == 0 || grid == 1) return e;
   float* out[3] = {};
   int n = 0;
   if (a.dg_post) out[n++] = a.dg_post;
