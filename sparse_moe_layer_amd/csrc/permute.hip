@@ -150,7 +150,7 @@ __global__ __launch_bounds__(256) void rows_kernel(RowArgs a) {
       V::unpack(vi[u], y);
 #pragma unroll
       for (int e = 0; e < V::N; ++e) {
-        dot[u & 3] = fmaf(x[e], y[e], dot[u & 3]);
+        dot[u & 3] = fmaf(x[e], y[e], dot[u & 3]);  // a row's are next to each other
         x[e] *= w[q];
       }
       if (a.dy) st16(out[q] + (int64_t)c * 16, V::pack(x));
@@ -159,11 +159,9 @@ __global__ __launch_bounds__(256) void rows_kernel(RowArgs a) {
   const float s = wave_sums<4>(dot, lane);
 #pragma unroll
   for (int q = 0; q < ROWS; ++q) {
-    float v = __shfl(s, q * 16, kWave);
-    if constexpr (ROWS == 1) {
+    float v = __shfl(s, q * (64 / ROWS), kWave);
 #pragma unroll
-      for (int u = 1; u < 4; ++u) v += __shfl(s, u * 16, kWave);
-    }
+    for (int u = 1; u < 4 / ROWS; ++u) v += __shfl(s, q * (64 / ROWS) + u * 16, kWave);
     if (lane || i0 + q >= a.n) continue;
     if (shared[q]) a.dsl[at[q]] = w[q] * sigmoid_f32(-a.sl[at[q]]) * v;
     else a.dw[at[q]] = ok[q] ? v : 0.f;
@@ -173,8 +171,8 @@ __global__ __launch_bounds__(256) void rows_kernel(RowArgs a) {
 hipError_t launch_rows(RowArgs a, int T, int per, bool f32, hipStream_t s) {
   a.n = (int64_t)T * per;
   a.per = per;
-  const bool many = a.nch <= 64;  // rows of one piece a lane
-  const int64_t waves = many ? (a.n + 3) / 4 : a.n;
+  const int rows = a.nch <= 64 ? 4 : a.nch <= 128 ? 2 : 1;  // a wave: rows of one piece a lane, of two
+  const int64_t waves = (a.n + rows - 1) / rows;
   const dim3 grid = row_grid((waves + 3) / 4);
 #define MOE_ROWS(ROWS, U)                                              \
   do {                                                                 \
@@ -183,7 +181,9 @@ hipError_t launch_rows(RowArgs a, int T, int per, bool f32, hipStream_t s) {
   } while (0)
   // a row that takes little more than one round of 4 pieces a lane in one of 5 (1500 x 1280 x 4
   // fp32 15.2 -> 13.9 us, 4096 x 2560 x 10 102.9 -> 100.9; longer ones in one of 8: the same)
-  if (many) MOE_ROWS(4, 1);
+  // (6550 x 552 x 18, one row a wave: 84 us; two 64)
+  if (rows == 4) MOE_ROWS(4, 1);
+  else if (rows == 2) MOE_ROWS(2, 2);
   else if (a.nch > 256 && a.nch <= 320) MOE_ROWS(1, 5);
   else MOE_ROWS(1, 4);
 #undef MOE_ROWS

@@ -19,8 +19,9 @@ DX = [(4090, 3320, 136, 1, "bf16"), (4000, 2568, 72, 5, "bf16"), (2990, 1608, 20
       (4090, 3300, 68, 1, "f32"), (2000, 1028, 132, 1, "f32"), (900, 516, 260, 3, "f32"), (200, 324, 516, 1, "f32")]
 DW = [(1100, 3320, 4088, 1, "bf16"), (300, 2184, 2056, 1, "bf16"), (380, 776, 648, 10, "bf16"), (1000, 776, 648, 10, "bf16"),
       (200, 1016, 1504, 1, "bf16"), (200, 600, 520, 1, "bf16"), (200, 200, 520, 1, "bf16"),
-      (300, 2052, 2180, 1, "f32"), (400, 1028, 1028, 4, "f32"), (150, 516, 520, 3, "f32"), (150, 132, 260, 1, "f32")]
-BOTH = [(600, 1024, 2560, 1, "bf16"), (1490, 1016, 1504, 1, "bf16"), (1000, 600, 520, 1, "bf16"), (90, 200, 264, 1, "bf16"), (500, 264, 520, 1, "f32"),
+      (300, 2052, 2180, 1, "f32"), (400, 1028, 1028, 4, "f32"), (200, 1028, 1028, 5, "f32"), (150, 516, 520, 3, "f32"), (150, 132, 260, 1, "f32")]
+BOTH = [(9, 200, 2480, 1, "bf16"), (2000, 512, 128, 1, "bf16"), (16, 1028, 2052, 1, "f32"), (2000, 516, 132, 1, "f32"),
+        (600, 1024, 2560, 1, "bf16"), (1490, 1016, 1504, 1, "bf16"), (1000, 600, 520, 1, "bf16"), (90, 200, 264, 1, "bf16"), (500, 264, 520, 1, "f32"),
         (100, 132, 260, 1, "f32")]
 
 
