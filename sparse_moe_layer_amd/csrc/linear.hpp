@@ -39,7 +39,8 @@ template <bool FAST>
 __device__ __forceinline__ float normal_cdf(float z, float& density) {
   density = exp_of<FAST>(-0.5f * z * z);
   if constexpr (FAST) {
-    const float x = fabsf(z) * 0.70710678f, r = __builtin_amdgcn_rcpf(x + 3.f);
+    // past x = 16 the density is 0 in fp32; an infinite x would make the fit's argument inf * 0
+    const float x = fminf(fabsf(z) * 0.70710678f, 16.f), r = __builtin_amdgcn_rcpf(x + 3.f);
     const float h = 0.5f * density * r * erfcx_poly((x - 3.f) * r);
     return z < 0.f ? h : 1.f - h;
   } else {
