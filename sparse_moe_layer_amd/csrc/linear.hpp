@@ -7,7 +7,8 @@
 namespace moe {
 
 // (x + 3) erfcx(x) for x >= 0, erfcx(x) = e^(x^2) erfc(x), as a polynomial in
-// t = (x - 3) / (x + 3): a least-maximum fit over x in [0, 12], off by 4e-9.
+// t = (x - 3) / (x + 3): a least-maximum fit over x in [0, 12], off by at most 4.7e-8 (near
+// x = 0.1; 2e-8 relative).
 __device__ __forceinline__ float erfcx_poly(float t) {
   float p = -3.14715813e-4f;
   p = fmaf(p, t, -4.63499426e-4f);
