@@ -45,7 +45,9 @@
  *    (hipGetLastError); faults during execution surface at the caller's next
  *    synchronisation.  NaN/Inf inputs give unspecified outputs.
  *  - T == 0 is a valid no-op returning MOE_OK once the problem itself is
- *    valid; no pointer is read or written (they may be NULL).
+ *    valid; no pointer is read or written (they may be NULL).  Gradients that
+ *    are sums over tokens are the exception: they are written, as zeros
+ *    (moe_block_norm_backward, moe_linear_backward with rows == 0).
  *  - Routing ties: experts are ordered by descending fp32 logit, equal logits
  *    by ascending expert id.  Results are deterministic run to run.
  *  - Expert ids, the dispatch permutation and all integer outputs are exact;
@@ -499,8 +501,10 @@ size_t moe_block_norm_workspace_bytes(const moe_norm_problem* p);
  *   is NULL; dg_post, dg_pre [H] fp32, or NULL; dgate: [T] fp32, [H] fp32 or
  *   [T,H] dtype by p->gate, or NULL.
  * dg_post needs g_post, dg_pre needs dx, dgate needs a gate (MOE_ERR_NULL).
- * T == 0 launches nothing, so the sums are not written.  ws: 256-byte aligned,
- * moe_block_norm_workspace_bytes(p) bytes; concurrent calls need distinct ones. */
+ * T == 0: dg_post, dg_pre and a channel gate's dgate are zeros where they are
+ * given, and no other pointer is looked at (all of them may be NULL).  ws:
+ * 256-byte aligned, moe_block_norm_workspace_bytes(p) bytes; concurrent calls
+ * need distinct ones.                                                       */
 moe_status moe_block_norm_backward(const moe_norm_problem* p, const void* dresid_out, const void* dx, const void* f,
                                    const void* resid_out, const void* g_post, const void* gate, const void* g_pre,
                                    void* dresid, void* df, float* dg_post, void* dgate, float* dg_pre, void* ws,

@@ -120,7 +120,13 @@ moe_status moe_block_norm_backward(const moe_norm_problem* p, const void* dresid
                                    void* dresid, void* df, float* dg_post, void* dgate, float* dg_pre, void* ws,
                                    size_t ws_bytes, void* stream) {
   moe_status st = check_norm(p);
-  if (st != MOE_OK || p->T == 0) return st;
+  if (st != MOE_OK) return st;
+  if (p->T == 0) {  // the sums over no tokens; the gradients with a row a token are empty
+    float* sum = p->gate == MOE_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr;
+    if (!al4(dg_post) || !al4(dg_pre) || !al4(sum)) return MOE_ERR_ALIGN;
+    if (!dg_post && !dg_pre && !sum) return MOE_OK;
+    return hip_status(moe::launch_norm_no_rows(dg_post, dg_pre, sum, (int)p->H, (hipStream_t)stream));
+  }
   if (!dresid_out && !dx) return MOE_ERR_NULL;
   if (dx && (!resid_out || !g_pre)) return MOE_ERR_NULL;
   if ((f == nullptr) != (df == nullptr) || (!f && !dresid)) return MOE_ERR_NULL;

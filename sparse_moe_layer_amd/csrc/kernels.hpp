@@ -240,6 +240,7 @@ struct NormBackArgs {
 size_t norm_partial_floats(int64_t T, int64_t H);
 hipError_t launch_norm(const NormArgs& a, int T, bool f32, hipStream_t s);
 hipError_t launch_norm_backward(NormBackArgs a, bool f32, hipStream_t s);
+hipError_t launch_norm_no_rows(float* dg_post, float* dg_pre, float* dgate, int H, hipStream_t s);
 
 // Products over groups of rows: pointers as in the C ABI.
 struct LinearArgs {

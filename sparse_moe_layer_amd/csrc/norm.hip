@@ -363,6 +363,15 @@ __global__ __launch_bounds__(1024) void norm_sums_kernel(const float* __restrict
   }
 }
 
+// The sums over no tokens.
+__global__ __launch_bounds__(256) void norm_no_rows_kernel(float* o0, float* o1, float* o2, int H) {
+  const int col = blockIdx.x * 256 + threadIdx.x;
+  if (col >= H) return;
+  if (o0) o0[col] = 0.f;
+  if (o1) o1[col] = 0.f;
+  if (o2) o2[col] = 0.f;
+}
+
 // Threads of a workgroup for nch chunks, NCH a thread.
 int threads_of(int nch, int per) { return ((nch + per - 1) / per + 63) / 64 * 64; }
 
@@ -404,6 +413,11 @@ static void back_kernel(const NormBackArgs& a, int& grid, hipStream_t s) {
   if (grid == 2) grid = 1;  // a second round of rows takes less than a launch for the sums (6 x 2560 11.3 -> 9.7 us)
   if (a.g_post) back_kernel<F32, NCH, NT, true>(a, grid, groups * tpr, tpr, s);
   else back_kernel<F32, NCH, NT, false>(a, grid, groups * tpr, tpr, s);
+}
+
+hipError_t launch_norm_no_rows(float* dg_post, float* dg_pre, float* dgate, int H, hipStream_t s) {
+  norm_no_rows_kernel<<<(H + 255) / 256, 256, 0, s>>>(dg_post, dg_pre, dgate, H);
+  return hipGetLastError();
 }
 
 hipError_t launch_norm_backward(NormBackArgs a, bool f32, hipStream_t s) {
