@@ -28,7 +28,7 @@ moe_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
 moe_status check_norm(const moe_norm_problem* p) {
   if (!p) return MOE_ERR_NULL;
   if (p->dtype != MOE_F32 && p->dtype != MOE_BF16) return MOE_ERR_DTYPE;
-  if (p->T < 0 || p->H < 1 || p->H > MOE_NORM_MAX_H || p->T >= ((int64_t)1 << 31) / p->H) return MOE_ERR_SHAPE;
+  if (p->T < 0 || p->H < 1 || p->H > MOE_NORM_MAX_H || p->T > INT32_MAX / p->H) return MOE_ERR_SHAPE;
   if (p->gate < MOE_GATE_NONE || p->gate > MOE_GATE_FULL) return MOE_ERR_SHAPE;
   if (!(p->eps > 0.f) || !std::isfinite(p->eps) || !std::isfinite(p->resid_scale)) return MOE_ERR_SHAPE;
   return p->H % (p->dtype == MOE_F32 ? 4 : 8) ? MOE_ERR_UNSUPPORTED : MOE_OK;
