@@ -201,7 +201,6 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormBackArgs a, int t
     float ss[8] = {};
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int c = me + i * tpr;
       float d[V::N], x[V::N], r[V::N], q[V::N], g[V::N];
       V::unpack(v.x[i], x);
       V::unpack(v.r[i], r);
@@ -243,56 +242,59 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormBackArgs a, int t
     const float sq = fmaf(rr, fmaf(-mr, ss[5], ss[4]), ss[3]);
     const float mf = gt * sq * a.inv_h * rf * rf;
     if (GATE == MOE_GATE_NONE && a.dgate && live && me == 0) static_cast<float*>(a.dgate)[t] = rf * sq;
+    // an idle group's zeros times an infinite gain or gate would be NaN in the sums over tokens
+    if (live) {
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int c = me + i * tpr;
-      const bool in = live && c < a.nch;
-      float dr[V::N], fv[V::N], g[V::N], o[V::N];
-      V::unpack(v.d[i], dr);
-      V::unpack(v.f[i], fv);
-      if (a.dx) {
-        float x[V::N], r[V::N];
-        V::unpack(v.x[i], x);
-        V::unpack(v.r[i], r);
-        V::unpack(k_pre[i], g);
+      for (int i = 0; i < NCH; ++i) {
+        const int c = me + i * tpr;
+        const bool in = c < a.nch;
+        float dr[V::N], fv[V::N], g[V::N], o[V::N];
+        V::unpack(v.d[i], dr);
+        V::unpack(v.f[i], fv);
+        if (a.dx) {
+          float x[V::N], r[V::N];
+          V::unpack(v.x[i], x);
+          V::unpack(v.r[i], r);
+          V::unpack(k_pre[i], g);
+#pragma unroll
+          for (int e = 0; e < V::N; ++e) {
+            dr[e] = fmaf(rr, fmaf(-r[e], mr, g[e] * x[e]), dr[e]);
+            s_pre[i][e] = fmaf(x[e] * rr, r[e], s_pre[i][e]);
+          }
+        }
+        if (a.dresid && in) {
+#pragma unroll
+          for (int e = 0; e < V::N; ++e) o[e] = a.scale * dr[e];
+          st16(static_cast<u32x4*>(a.dresid) + base + c, V::pack(o));
+        }
+        if (!f) continue;
+        float dn[V::N], gp[V::N];
 #pragma unroll
         for (int e = 0; e < V::N; ++e) {
-          dr[e] = fmaf(rr, fmaf(-r[e], mr, g[e] * x[e]), dr[e]);
-          s_pre[i][e] = fmaf(x[e] * rr, r[e], s_pre[i][e]);
+          dn[e] = gt * dr[e];
+          gp[e] = 1.f;
         }
-      }
-      if (a.dresid && in) {
+        if constexpr (POST) V::unpack(k_post[i], gp);
+        if constexpr (GATE != MOE_GATE_NONE) {
+          if constexpr (GATE == MOE_GATE_FULL) V::unpack(v.g[i], g);
+          else V::unpack(k_gate[i], g);
 #pragma unroll
-        for (int e = 0; e < V::N; ++e) o[e] = a.scale * dr[e];
-        st16(static_cast<u32x4*>(a.dresid) + base + c, V::pack(o));
-      }
-      if (!f) continue;
-      float dn[V::N], gp[V::N];
-#pragma unroll
-      for (int e = 0; e < V::N; ++e) {
-        dn[e] = gt * dr[e];
-        gp[e] = 1.f;
-      }
-      if constexpr (POST) V::unpack(k_post[i], gp);
-      if constexpr (GATE != MOE_GATE_NONE) {
-        if constexpr (GATE == MOE_GATE_FULL) V::unpack(v.g[i], g);
-        else V::unpack(k_gate[i], g);
-#pragma unroll
-        for (int e = 0; e < V::N; ++e) {
-          dn[e] *= g[e];
-          o[e] = fv[e] * rf * gp[e] * dr[e];  // n dr: the gate's gradient
-          if constexpr (GATE == MOE_GATE_CHANNEL) s_gate[i][e] += o[e];
+          for (int e = 0; e < V::N; ++e) {
+            dn[e] *= g[e];
+            o[e] = fv[e] * rf * gp[e] * dr[e];  // n dr: the gate's gradient
+            if constexpr (GATE == MOE_GATE_CHANNEL) s_gate[i][e] += o[e];
+          }
+          if (GATE == MOE_GATE_FULL && a.dgate && in) st16(static_cast<u32x4*>(a.dgate) + base + c, V::pack(o));
         }
-        if (GATE == MOE_GATE_FULL && a.dgate && in) st16(static_cast<u32x4*>(a.dgate) + base + c, V::pack(o));
-      }
-      if constexpr (POST) {
+        if constexpr (POST) {
 #pragma unroll
-        for (int e = 0; e < V::N; ++e) {
-          s_post[i][e] = fmaf(dn[e] * rf, fv[e], s_post[i][e]);
-          dn[e] = rf * fmaf(-fv[e], mf, dn[e] * gp[e]);
+          for (int e = 0; e < V::N; ++e) {
+            s_post[i][e] = fmaf(dn[e] * rf, fv[e], s_post[i][e]);
+            dn[e] = rf * fmaf(-fv[e], mf, dn[e] * gp[e]);
+          }
         }
+        if (in) st16(static_cast<u32x4*>(a.df) + base + c, V::pack(dn));
       }
-      if (in) st16(static_cast<u32x4*>(a.df) + base + c, V::pack(dn));
     }
     if constexpr (AHEAD) v = next;
   }
