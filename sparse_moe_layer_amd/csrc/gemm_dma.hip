@@ -22,8 +22,7 @@
 // stage's first fragments are read, so no stage starts on an LDS wait.  A stage holds a 32-wide K slice,
 // [row][4 chunks of 16 B], chunk c of row r at position c ^ ((r >> 2) & 3):
 // a half-wave's 16-byte fragment reads cover 16 rows and 64 banks span four
-// 64-byte rows, so the XOR spreads them over all banks.  (The template also
-// takes a 64-wide K step: 8 chunks per 128-byte row, XOR (r >> 1) & 7.)  Each lane's direct
+// 64-byte rows, so the XOR spreads them over all banks.  Each lane's direct
 // load fetches the global chunk that belongs at its LDS position, so global
 // reads stay whole 64-byte row segments.
 //
@@ -45,10 +44,10 @@
 namespace moe {
 namespace {
 
-
-template <int BM_, int BN_, int WM_, int WN_, int S_, int WG_PER_CU_, int BK_ = 32, bool F8_ = false>
+template <int BM_, int BN_, int WM_, int WN_, int S_, int WG_PER_CU_, bool F8_ = false>
 struct Cfg {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, BK = BK_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_;
+  static constexpr int BK = 32;         // K step: two sub-steps, the second carried
   static constexpr bool F8 = F8_;       // B holds fp8 codes (1 byte per element)
   static constexpr int RPL = 512 / BK;  // rows one 1 KB direct load fills
   static constexpr int RPL8 = 1024 / BK;  // fp8 B rows one 1 KB direct load fills
@@ -62,14 +61,13 @@ struct Cfg {
   static constexpr int LB = F8 ? BN / (RPL8 * NW) : BN / (RPL * NW);  // B direct loads per lane per stage
   static constexpr int L = LA + LB;
   static constexpr int STAGE = (BM + BN) * BK;  // elements per stage buffer
-  static_assert(BK == 32 || BK == 64, "K step");
-  static_assert(MI >= 1 && NJ >= 2 && NJ % 2 == 0 && LA >= 1 && LB >= 1, "tiling");
+  static_assert(MI >= 1 && NJ >= 2 && NJ % 2 == 0 && MI * NJ <= 8 && LA >= 1 && LB >= 1, "tiling");
   static_assert(S >= 2 && S <= 6 && L * (S - 2) < 64, "pipeline depth");
   static_assert(S * STAGE * 2 * WG_PER_CU_ <= 160 * 1024, "LDS");
-  static_assert(!F8 || (BK == 32 && S == 4 && MI * NJ <= 8 && NJ == 2 && CW == 64), "fp8 B tiling");
+  static_assert(!F8 || (S == 4 && NJ == 2 && CW == 64), "fp8 B tiling");
 };
 using BigCfg = Cfg<256, 256, 2, 4, 4, 1>;
-using BigCfg8 = Cfg<256, 256, 2, 4, 4, 1, 32, true>;
+using BigCfg8 = Cfg<256, 256, 2, 4, 4, 1, true>;
 
 constexpr int vmcnt_imm(int n) { return 0xF70 | (n & 15) | (((n >> 4) & 3) << 14); }
 // the same wait, and for every LDS operation of this wave
@@ -104,12 +102,10 @@ __device__ __forceinline__ void lds_sync() {
   block_sync();
 }
 
-// Chunk c of row r: 4 chunks per 64-byte row XOR (r >> 2) & 3, or 8 per
-// 128-byte row XOR (r >> 1) & 7 (16 rows of one chunk hit 16 bank groups).
-template <int BK>
-__device__ __forceinline__ int swz(int r) { return BK == 32 ? (r >> 2) & 3 : (r >> 1) & 7; }
-template <int BK>
-__device__ __forceinline__ int lds_pos(int r, int c) { return r * BK + ((c ^ swz<BK>(r)) << 3); }
+// Chunk c of row r: 4 chunks per 64-byte row XOR (r >> 2) & 3 (16 rows of one
+// chunk hit 16 bank groups).
+__device__ __forceinline__ int swz(int r) { return (r >> 2) & 3; }
+__device__ __forceinline__ int lds_pos(int r, int c) { return r * 32 + ((c ^ swz(r)) << 3); }
 
 // The direct loads of one K step into one stage buffer: load i of wave w
 // fills 16 rows (NW*i + w)*16 .. +16 (1 KB) of the A part, then of the B part.
@@ -133,7 +129,7 @@ __device__ __forceinline__ void issue_stage(bf16* st, const bf16* abase, const u
 // swizzled.  Block ii / jj adds a whole number of 32-row blocks, so every
 // fragment read is one of these plus a compile-time offset.
 struct FragOff {
-  int a[4], b[4];  // per 16-wide K sub-step of a stage
+  int a[2], b[2];  // per 16-wide K sub-step of a stage
   int b8;          // fp8 B: byte offset of this lane's first code (block 0, chunk 0)
 };
 
@@ -143,8 +139,8 @@ __device__ __forceinline__ FragOff frag_offsets(int wm, int wn, int lane) {
 #pragma unroll
   for (int ks = 0; ks < C::BK / 16; ++ks) {
     const int c = ks * 2 + (lane >> 5);
-    o.a[ks] = lds_pos<C::BK>(wm * 32 + (lane & 31), c);
-    o.b[ks] = lds_pos<C::BK>(C::BM + wn * C::CW + (lane & 31), c);
+    o.a[ks] = lds_pos(wm * 32 + (lane & 31), c);
+    o.b[ks] = lds_pos(C::BM + wn * C::CW + (lane & 31), c);
   }
   o.b8 = C::BM * C::BK * 2 + wn * (C::CW / 32) * 1024 + (lane & 31) * 16 + 8 * (lane >> 5);
   return o;
@@ -163,9 +159,6 @@ __device__ __forceinline__ void load_frags(const bf16* st, int ks, const FragOff
 // bf16 fragments of one K sub-step held across a barrier: the stage's second
 // sub-step, whose MFMAs run at the start of the next stage (zero at a tile's
 // first stage, so there they add nothing).
-template <class C>
-constexpr bool kCarry = C::BK == 32 && C::MI * C::NJ <= 8;
-
 template <class C, int NB>
 struct Carry {
   bf16x8 a[NB], b[C::NJ];
@@ -186,7 +179,7 @@ __device__ __forceinline__ void mfma_sub(f32x16 (&acc)[C::MI][C::NJ], const bf16
 template <class C, int NB>
 __device__ __forceinline__ void compute_stage_carry(f32x16 (&acc)[C::MI][C::NJ], const bf16* st, const FragOff& o,
                                                     Carry<C, NB>& cy) {
-  static_assert(C::BK == 32 && !C::F8, "two bf16 K sub-steps per stage");
+  static_assert(!C::F8, "bf16 weights");
   bf16x8 af[NB], bfr[C::NJ];
   load_frags<C, NB>(st, 0, o, af, bfr);
   mfma_sub<C, NB>(acc, cy.a, cy.b);
@@ -217,7 +210,7 @@ __device__ __forceinline__ void compute_stage_carry(f32x16 (&acc)[C::MI][C::NJ],
 template <class C, int NB>
 __device__ __forceinline__ void compute_stage_carry8(f32x16 (&acc)[C::MI][C::NJ], const bf16* st, const FragOff& o,
                                                      float sc0, float sc1, Carry<C, NB>& cy) {
-  static_assert(C::BK == 32 && C::F8, "two fp8 K sub-steps per stage");
+  static_assert(C::F8, "fp8 weights");
   const char* sb = reinterpret_cast<const char*>(st) + o.b8;
   bf16x8 af[NB], bfr[C::NJ];
   u32x2 c0[C::NJ], c1[C::NJ];
@@ -257,99 +250,6 @@ __device__ __forceinline__ void compute_stage_carry8(f32x16 (&acc)[C::MI][C::NJ]
   }
 }
 
-// MFMAs of one stage: 2 K sub-steps of 16, fragments of both loaded first.
-template <class C, int NB>
-__device__ __forceinline__ void compute_stage(f32x16 (&acc)[C::MI][C::NJ], const bf16* st, const FragOff& o,
-                                              float sc0, float sc1) {
-  if constexpr (C::F8) {
-    // B block jj: 8 codes of row (lane % 32) at K 16*ks + 8*(lane/32), in
-    // chunk ks of its 32-row block; block 0 takes scale sc0, block 1 sc1
-    // (one K sub-step at a time: the decode's temporaries leave no room for
-    // both sub-steps' fragments next to the 128 accumulators)
-    const char* sb = reinterpret_cast<const char*>(st) + o.b8;
-    constexpr int KS = C::BK / 16;
-    bf16x8 af[KS][NB], bfr[KS][C::NJ];
-    u32x2 codes[KS][C::NJ];
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-#pragma unroll
-      for (int jj = 0; jj < C::NJ; ++jj) codes[ks][jj] = *reinterpret_cast<const u32x2*>(sb + jj * 1024 + ks * 512);
-#pragma unroll
-      for (int ii = 0; ii < NB; ++ii)
-        af[ks][ii] = *reinterpret_cast<const bf16x8*>(st + o.a[ks] + ii * C::WM * 32 * C::BK);
-#pragma unroll
-      for (int jj = 0; jj < C::NJ; ++jj)
-        bfr[ks][jj] = __builtin_bit_cast(bf16x8, fp8x8_to_bf16x8(codes[ks][jj], jj == 0 ? sc0 : sc1));
-    }
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-      for (int ii = 0; ii < NB; ++ii)
-#pragma unroll
-        for (int jj = 0; jj < C::NJ; ++jj)
-          acc[ii][jj] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[ks][ii], bfr[ks][jj], acc[ii][jj], 0, 0, 0);
-    // Schedule as in the bf16 path, with each sub-step's decode (VALU) placed
-    // among the previous sub-step's MFMAs.
-    constexpr int NR = NB + C::NJ;  // fragment reads per sub-step
-    constexpr int NM = NB * C::NJ;  // MFMAs per sub-step
-    constexpr int NV = 16 * C::NJ;  // decode instructions per sub-step
-    __builtin_amdgcn_sched_group_barrier(0x100, NR, 0);
-    __builtin_amdgcn_sched_group_barrier(0x002, NV, 0);
-#pragma unroll
-    for (int ks = 0; ks + 1 < KS; ++ks) {
-#pragma unroll
-      for (int i = 0; i < NM; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        if (i < NR) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, NV / NM, 0);
-      }
-    }
-    __builtin_amdgcn_sched_group_barrier(0x008, NM, 0);
-  } else if constexpr (C::MI * C::NJ > 8) {
-    // 128 x 128 wave tiles: one K sub-step of fragments at a time
-#pragma unroll
-    for (int ks = 0; ks < C::BK / 16; ++ks) {
-      bf16x8 af[NB], bfr[C::NJ];
-      load_frags<C, NB>(st, ks, o, af, bfr);
-#pragma unroll
-      for (int ii = 0; ii < NB; ++ii)
-#pragma unroll
-        for (int jj = 0; jj < C::NJ; ++jj)
-          acc[ii][jj] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[ii], bfr[jj], acc[ii][jj], 0, 0, 0);
-    }
-  } else {
-    bf16x8 af[C::BK / 16][NB], bfr[C::BK / 16][C::NJ];
-#pragma unroll
-    for (int ks = 0; ks < C::BK / 16; ++ks) load_frags<C, NB>(st, ks, o, af[ks], bfr[ks]);
-#pragma unroll
-    for (int ks = 0; ks < C::BK / 16; ++ks)
-#pragma unroll
-      for (int ii = 0; ii < NB; ++ii)
-#pragma unroll
-        for (int jj = 0; jj < C::NJ; ++jj)
-          acc[ii][jj] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[ks][ii], bfr[ks][jj], acc[ii][jj], 0, 0, 0);
-    // Schedule: sub-step 0's fragment reads, then each sub-step's MFMAs
-    // alternating with the next sub-step's reads, so LDS latency hides under
-    // MFMAs (left alone, the compiler reuses one set of fragment registers
-    // and waits on LDS before every few MFMAs).
-    constexpr int NR = NB + C::NJ;  // fragment reads per sub-step
-    constexpr int NM = NB * C::NJ;  // MFMAs per sub-step
-    constexpr int NP = NR < NM ? NR : NM;
-    __builtin_amdgcn_sched_group_barrier(0x100, NR, 0);
-#pragma unroll
-    for (int ks = 0; ks + 1 < C::BK / 16; ++ks) {
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      }
-      if constexpr (NM > NP) __builtin_amdgcn_sched_group_barrier(0x008, NM - NP, 0);
-      if constexpr (NR > NP) __builtin_amdgcn_sched_group_barrier(0x100, NR - NP, 0);
-    }
-    __builtin_amdgcn_sched_group_barrier(0x008, NM, 0);
-  }
-}
-
 // One K step s held in buffer b: wait until this wave's loads of step s have
 // landed (the S-2 younger stages may stay in flight), one barrier (every
 // wave's loads landed, every wave done with buffer b-1), refill buffer b-1
@@ -366,23 +266,17 @@ __device__ __forceinline__ void step(f32x16 (&acc)[C::MI][C::NJ], bf16* const* s
     scl0 = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, sc0[s >> 2])));
     scl1 = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, sc1[s >> 2])));
   }
-  // carried reads of buffer b-1 must be done before any wave refills it
-  if constexpr (kCarry<C>) {
-    // nothing of the previous stage (its last MFMAs cover its last reads)
-    // moves past the wait and barrier
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm((C::S - 2) * C::L));
-    block_sync();
-    __builtin_amdgcn_sched_barrier(0);
-  } else {
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm((C::S - 2) * C::L));
-    block_sync();
-  }
+  // carried reads of buffer b-1 must be done before any wave refills it;
+  // nothing of the previous stage (its last MFMAs cover its last reads)
+  // moves past the wait and barrier
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm((C::S - 2) * C::L));
+  block_sync();
+  __builtin_amdgcn_sched_barrier(0);
   const uint32_t kn = (uint32_t)(s + C::S - 1) * C::BK;
   issue_stage<C>(stg[(B + C::S - 1) % C::S], abase, aoff, bbase, boff, kn < klast ? kn : klast, wave);
-  if constexpr (kCarry<C> && C::F8) compute_stage_carry8<C, NB>(acc, stg[B], o, scl0, scl1, cy);
-  else if constexpr (kCarry<C>) compute_stage_carry<C, NB>(acc, stg[B], o, cy);
-  else compute_stage<C, NB>(acc, stg[B], o, scl0, scl1);
+  if constexpr (C::F8) compute_stage_carry8<C, NB>(acc, stg[B], o, scl0, scl1, cy);
+  else compute_stage_carry<C, NB>(acc, stg[B], o, cy);
 }
 
 // The K loop of one tile over nk steps, nk % S == R: step s uses buffer s % S.
@@ -420,7 +314,7 @@ __device__ __forceinline__ void mainloop(f32x16 (&acc)[C::MI][C::NJ], bf16* cons
   if constexpr (R > 2) step<C, NB, 2>(acc, stg, abase, aoff, bbase, boff, nfull + 2, klast, wave, o, sc0, sc1, scl0, scl1, cy);
   if constexpr (R > 3) step<C, NB, 3>(acc, stg, abase, aoff, bbase, boff, nfull + 3, klast, wave, o, sc0, sc1, scl0, scl1, cy);
   if constexpr (R > 4) step<C, NB, 4>(acc, stg, abase, aoff, bbase, boff, nfull + 4, klast, wave, o, sc0, sc1, scl0, scl1, cy);
-  if constexpr (kCarry<C>) mfma_sub<C, NB>(acc, cy.a, cy.b);
+  mfma_sub<C, NB>(acc, cy.a, cy.b);
 }
 
 template <class C, int NB>
@@ -482,7 +376,7 @@ __device__ __forceinline__ void run_tile(const FfnArgs& f, int mt, int nt, bf16*
     // 16 bytes (one cache line request instead of sixteen; the loads stay
     // unconditional, so the compiler's wait counts stay exact)
     const bool dead = (C::NW * i + wave) * C::RPL >= nrows;
-    const int gchunk = dead ? 0 : lpos ^ swz<C::BK>(row);
+    const int gchunk = dead ? 0 : lpos ^ swz(row);
     const int rr = dead ? nrows - 1 : (row < nrows ? row : nrows - 1);
     const int gr = base + r0 + rr;
     if (MODE == 1) {
@@ -517,7 +411,7 @@ __device__ __forceinline__ void run_tile(const FfnArgs& f, int mt, int nt, bf16*
     } else {
       const int grow0 = (C::NW * i + wave) * C::RPL;  // wave-uniform first row of the load
       const int n = grow0 + lrow;                       // B tile row
-      const int gchunk = lpos ^ swz<C::BK>(n);
+      const int gchunk = lpos ^ swz(n);
       int col;
       if (MODE == 1) {
         // wave column wc (CW rows) holds CW/2 gate rows, then the up rows of
@@ -599,8 +493,10 @@ __device__ __forceinline__ void run_tile(const FfnArgs& f, int mt, int nt, bf16*
   constexpr int BPS = C::STAGE / (BAND * CCOLS);        // bands per stage buffer
   static_assert(BPS >= 1 && C::MI <= C::S * BPS && CPR >= 8, "epilogue staging");
   auto cpos = [&](int r, int col) { return r * CCOLS + ((((col >> 3) ^ (((r >> 2) & 1) << 2))) << 3) + (col & 7); };
-  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // trailing (redundant) direct loads have landed
-  block_sync();                              // every wave is done reading the stage buffers
+  // trailing (redundant) direct loads have landed, and this wave is done reading the
+  // stage buffers, before any wave writes its part of the tile there
+  __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(0));
+  block_sync();
 #pragma unroll
   for (int ii = 0; ii < C::MI; ++ii) {
     bf16* ct = stg[ii / BPS] + (ii % BPS) * BAND * CCOLS;
