@@ -416,7 +416,7 @@ def moe_block_norm_backward(p: moe_norm_problem, dresid_out, dx, f, resid_out, g
 def _weights_arg(f, p, w, dt, dev):
     """[groups, N, K] contiguous, or at p.w_stride from one contiguous matrix to the next (a slice of a fused
     [groups, 2 N, K] tensor)."""
-    if w is None or p.w_stride in (0, p.N * p.K):
+    if w is None or p.w_stride in (0, p.N * p.K) or p.groups < 1:
         return _arg(f, w, p.groups * p.N * p.K, dt, dev)
     want = (p.groups, p.N, p.K)
     if tuple(w.shape) != want or (p.groups > 1 and w.stride(0) != p.w_stride):
