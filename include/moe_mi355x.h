@@ -430,8 +430,11 @@ moe_status moe_mx_dequantize(const void* codes, const void* scales, int64_t rows
  *   x [T,H] act; assign_pos [T,k] as moe_dispatch returns it; xs [T*k, H] act.
  * The positions in [0, T*k) must differ; an assignment with a position outside
  * has no row (dropped, or another GPU's), here and in the two calls below, and
- * rows that no assignment names are left as they were.  Uses T, H, E, k and
- * act_dtype of p.                                                           */
+ * rows that no assignment names are left as they were.  p has to be a valid
+ * problem as a whole (moe_validate: I and w_dtype, and so T*k*I < 2^31, too),
+ * in this call and the two below; of it they use T, H, E, k and act_dtype.
+ * Where the experts are the caller's own, I may be as small as 8 (bf16) or 4
+ * (f32).                                                                    */
 moe_status moe_permute(const moe_problem* p, const void* x, const int32_t* assign_pos, const float* topk_w, void* xs,
                        void* stream);
 

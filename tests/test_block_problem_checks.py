@@ -1,8 +1,23 @@
 """What a problem as a whole has to be in the block calls: refused by the library, also where Python looks at tensors first."""
+import ctypes
+
 import pytest
 import torch
 
 import sparse_moe_layer_amd as lib
+from sparse_moe_layer_amd import _lib
+
+SHAPE, UNSUP, NULL = _lib.MOE_ERR_SHAPE, _lib.MOE_ERR_UNSUPPORTED, _lib.MOE_ERR_NULL
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), NULL), (dict(I=8), NULL), (dict(I=0), SHAPE), (dict(I=4), UNSUP), (dict(I=4, act="f32", wdt="f32"), NULL),
+    (dict(T=1 << 20, k=8, I=256), UNSUP), (dict(T=1 << 20, k=8, I=248), NULL), (dict(T=1 << 28, k=8, H=8, I=8), SHAPE)])
+def test_permute_problems_as_a_whole(kw, status):
+    """The expert's hidden width counts although the calls do not read it: any small one will do."""
+    p = lib.problem(**dict(dict(T=64, H=256, E=16, k=4, I=128), **kw))
+    for fn, n in ((_lib.LIB.moe_permute, 5), (_lib.LIB.moe_permute_backward, 7), (_lib.LIB.moe_combine_backward, 11)):
+        assert fn(ctypes.byref(p), *[None] * n) == status
 
 
 def test_no_groups_of_strided_weights(monkeypatch):
