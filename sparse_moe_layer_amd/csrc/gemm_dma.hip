@@ -39,6 +39,7 @@
 // persistent grid so that consecutive tiles land on one XCD (workgroup i runs
 // on XCD i mod 8), sharing A slices and weight slices in that XCD's L2.
 #include "common.hpp"
+#include "dma.hpp"
 #include "kernels.hpp"
 
 namespace moe {
@@ -69,37 +70,10 @@ struct Cfg {
 using BigCfg = Cfg<256, 256, 2, 4, 4, 1>;
 using BigCfg8 = Cfg<256, 256, 2, 4, 4, 1, true>;
 
-constexpr int vmcnt_imm(int n) { return 0xF70 | (n & 15) | (((n >> 4) & 3) << 14); }
-// the same wait, and for every LDS operation of this wave
-constexpr int vmcnt_lgkm0_imm(int n) { return vmcnt_imm(n) & ~0xF00; }
-
-// A 16-byte direct load (global memory to LDS, no registers) through a
-// buffer resource over base, at byte offset voff + soff < 2^32 (the layer
-// checks keep every element offset below 2^31); soff is wave-uniform (the K
-// step), voff the lane's row and chunk.  The compiler counts buffer loads to LDS
-// apart from LDS reads, so fragment reads keep partial LDS waits; with the
-// global_load_lds form in flight it waits for every outstanding LDS operation
-// before each MFMA that consumes a fragment.
-constexpr int kBufferFlags = 0x00020000;  // raw (untyped) 32-bit buffer access
+// Offsets of the loads are below 2^32 bytes: the layer checks keep every element offset below
+// 2^31, and nothing is read past a tensor's end.
 __device__ __forceinline__ void dma16b(const void* base, uint32_t voff, uint32_t soff, bf16* l) {
-  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, 0xFFFFFFFF,
-                                                                      kBufferFlags);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)l, 16, voff, soff, 0, 0);
-}
-
-// Compiler-level fence around the raw s_barrier (the barrier builtin itself
-// does not order memory operations for the compiler).
-__device__ __forceinline__ void block_sync() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
-// The same once this wave's LDS accesses are done: where other waves read what it
-// wrote (the barrier alone does not wait for them).
-__device__ __forceinline__ void lds_sync() {
-  __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(63));
-  block_sync();
+  dma16(base, 0xFFFFFFFF, voff, soff, l);
 }
 
 // Chunk c of row r: 4 chunks per 64-byte row XOR (r >> 2) & 3 (16 rows of one

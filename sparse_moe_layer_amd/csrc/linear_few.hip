@@ -7,6 +7,7 @@
 // 16 half lines a load) into LDS that only the wave itself uses, kAhead pieces in flight.
 // A row of 8192 x 2048 (34 MB): 7.9 us, 4.3 TB/s with the launch; ten groups of 2560 x 640
 // (33 MB): 9.8 us, of which 2 the launch and 1 the search for the groups.
+#include "dma.hpp"
 #include "linear.hpp"
 
 #include <type_traits>
@@ -15,15 +16,7 @@ namespace moe {
 namespace {
 
 constexpr int kAhead = 4;
-constexpr int kFlags = 0x00020000;          // raw 32-bit buffer access
-constexpr uint32_t kNowhere = 0xFFFFFFF0u;  // past every buffer: a load writes zeros
-constexpr int kPiece = 16 * 128;            // bytes of an operand's piece
-
-template <bool ONCE>
-__device__ __forceinline__ void dma16(const void* base, uint32_t records, uint32_t off, char* l) {
-  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, records, kFlags);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)l, 16, off, 0, 0, ONCE ? 2 : 0);
-}
+constexpr int kPiece = 16 * 128;  // bytes of an operand's piece
 
 template <bool F32, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, 2) void linear_few_kernel(LinearArgs a) {
@@ -60,8 +53,8 @@ __global__ __launch_bounds__(WAVES * 64, 2) void linear_few_kernel(LinearArgs a)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t off = p * BK + kc[h] < a.K ? at[h] + p * 128 : kNowhere;
-      dma16<true>(w, wb, off, l + h * 1024);
-      dma16<false>(x, xb, off, l + kPiece + h * 1024);
+      dma16(w, wb, off, 0, l + h * 1024, true);
+      dma16(x, xb, off, 0, l + kPiece + h * 1024);
     }
   };
   // the epilogue's reads go out first (thread: row tid / 16, column tid % 16)
@@ -80,12 +73,12 @@ __global__ __launch_bounds__(WAVES * 64, 2) void linear_few_kernel(LinearArgs a)
   load(r2 + mine, wave + 2 * WAVES);
   load(r3 + mine, wave + 3 * WAVES);
   auto step = [&](char* l, int next) {
-    __builtin_amdgcn_s_waitcnt(0xF70 | 4 * (kAhead - 1));  // this piece's four loads have landed
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(4 * (kAhead - 1)));  // this piece's four loads have landed
     asm volatile("" ::: "memory");
     using F = typename std::conditional<F32, f32x4, bf16x8>::type;
     const F f0 = *reinterpret_cast<const F*>(l + o0), g0 = *reinterpret_cast<const F*>(l + kPiece + o0);
     const F f1 = *reinterpret_cast<const F*>(l + o1), g1 = *reinterpret_cast<const F*>(l + kPiece + o1);
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // and are read, before the next ones overwrite them
+    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(63));  // and are read, before the next ones overwrite them
     asm volatile("" ::: "memory");
     load(l, next);
     if constexpr (F32) {  // K 16 j + 4 h + e over the four h of a wave, for e in 0 .. 3
@@ -104,7 +97,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void linear_few_kernel(LinearArgs a)
     step(r2 + mine, p + (kAhead + 2) * WAVES);
     step(r3 + mine, p + (kAhead + 3) * WAVES);
   }
-  __builtin_amdgcn_s_waitcnt(0xF70);  // the loads past the end have landed too
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // the loads past the end have landed too
   // rows 4 (lane / 16) .. + 4 of W, row lane % 16 of x
 #pragma unroll
   for (int v = 0; v < 4; ++v) red[wave][lane & 15][4 * (lane >> 4) + v] = acc[v];

@@ -11,6 +11,7 @@
 // 4096 x 4096 x 4096 918 us, 0.150 PFLOP/s, the library 0.154 at 8192) or, for groups of few
 // rows, by reading or writing each weight once (512 groups of 80 rows of 2560 x 640, 1.94 GB:
 // forward 338 us, dx 420, dw 500).
+#include "dma.hpp"
 #include "linear.hpp"
 
 #include <type_traits>
@@ -44,34 +45,6 @@ struct Tile {
   static_assert(MI >= 1 && NJ >= 1 && LA >= 1 && LB >= 1 && L * (S - 1) < 64, "tiling");
   static_assert(S * STAGE * WG_PER_CU <= 160 * 1024, "LDS");
 };
-
-constexpr int vmcnt_imm(int n) { return 0xF70 | (n & 15) | (((n >> 4) & 3) << 14); }
-constexpr int vmcnt_lgkm0_imm(int n) { return vmcnt_imm(n) & ~0xF00; }
-
-constexpr int kBufferFlags = 0x00020000;  // raw 32-bit buffer access
-constexpr uint32_t kNowhere = 0xFFFFFFF0u;  // past every buffer: the load writes zeros to LDS
-
-__device__ __forceinline__ void block_sync() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
-// The same after this wave's LDS accesses are done (the barrier alone does not wait for
-// them).
-__device__ __forceinline__ void lds_sync() {
-  __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(63));
-  block_sync();
-}
-
-// A 16-byte direct load from base + voff + soff to LDS (voff the lane's, soff the
-// wave's); past `records` bytes it writes zeros.  once: non-temporal.
-__device__ __forceinline__ void dma16(const char* base, uint32_t records, uint32_t voff, uint32_t soff, char* l,
-                                      bool once) {
-  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, records, kBufferFlags);
-  if (once) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)l, 16, voff, soff, 0, 2);
-  else __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)l, 16, voff, soff, 0, 0);
-}
 
 // Where 16-byte chunk c of an operand's row lies within the row of a stage: c ^ swz.
 //  Rows along K (KB bytes): 16 rows' fragment reads of one chunk cover all banks.
