@@ -13,6 +13,11 @@ namespace {
 // One pass over dy, z and mul, bound by HBM (40960 x 640 bf16 with SiLU and a factor, 0.26 GB:
 // 43 us, 6 TB/s).  Workgroup: 32 threads across 16-byte chunks, 8 rows at a time, of split
 // blockIdx.x of group blockIdx.z's rows (without sums: of all groups' rows).
+// bf16 dz is rounded once here, as the operand of both products that bf16 matrix instructions
+// take: dx and dw are then 2.35e-3 (root mean square) from the exact gradients, of which the
+// rounding of dx and dw themselves is 1.66e-3.  Kept in two bf16 parts it would double both
+// products' matrix instructions and dz's bytes; in fp32 they run at a ninth of the rate.  dbias
+// adds the unrounded values, and without activation and factor dz is dy, not rounded at all.
 template <bool F32>
 __global__ __launch_bounds__(256) void linear_dz_kernel(LinearBackArgs a, int splits, bool sums, bool store) {
   using V = Vec<F32>;
