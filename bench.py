@@ -189,7 +189,7 @@ def mfma_ceiling(lib, stream, launches=2000):
 
 def kernel_source_sha():
     h = hashlib.sha256()
-    for f in ("gemm.hip", "gemm_dma.hip", "stream.hip", "stream_item.hpp", "common.hpp", "kernels.hpp"):
+    for f in ("gemm.hip", "gemm_dma.hip", "dma.hpp", "stream.hip", "stream_item.hpp", "common.hpp", "kernels.hpp"):
         h.update(open(os.path.join(ROOT, "sparse_moe_layer_amd", "csrc", f), "rb").read())
     return h.hexdigest()[:16]
 
