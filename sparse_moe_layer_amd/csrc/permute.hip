@@ -44,7 +44,9 @@ __global__ __launch_bounds__(256) void permute_kernel(const char* __restrict__ x
 }
 
 // dx alone: one thread per 16 bytes of dx, KB rows' loads in flight and summed in order
-// (4096 x 2560 x 10, 0.23 GB read and 0.02 written: 44 us, 5.3 TB/s).
+// (4096 x 2560 x 10, 0.23 GB read and 0.02 written: 44 us, 5.3 TB/s).  A batch's places past k
+// load row 0, so KB is the least of 4, 8 and 10 that takes k at once (k = 8: 34.0 us in a batch of
+// 8, 36.6 in one of 10; k = 5 27.2 and 29.0), and 8 at a time for more.
 template <bool F32, bool W, int KB>
 __global__ __launch_bounds__(256) void unpermute_kernel(const char* __restrict__ dxs, const int32_t* __restrict__ pos,
                                                         const float* __restrict__ w, char* __restrict__ dx, int n,
@@ -313,11 +315,11 @@ hipError_t launch_permute_backward(const void* dxs, const int32_t* pos, const fl
     if (e != hipSuccess) return e;
   }
   const int n = T * chunks.d, grid = (n + 255) / 256;
-#define MOE_UNPERMUTE(F32, W)                                                                               \
-  do {                                                                                                      \
-    if (k <= 4) unpermute_kernel<F32, W, 4><<<grid, 256, 0, s>>>(d, pos, w, o, n, chunks, k, T * k);        \
-    else if (k <= 10) unpermute_kernel<F32, W, 10><<<grid, 256, 0, s>>>(d, pos, w, o, n, chunks, k, T * k); \
-    else unpermute_kernel<F32, W, 8><<<grid, 256, 0, s>>>(d, pos, w, o, n, chunks, k, T * k);               \
+#define MOE_UNPERMUTE(F32, W)                                                                                         \
+  do {                                                                                                                \
+    if (k <= 4) unpermute_kernel<F32, W, 4><<<grid, 256, 0, s>>>(d, pos, w, o, n, chunks, k, T * k);                  \
+    else if (k == 9 || k == 10) unpermute_kernel<F32, W, 10><<<grid, 256, 0, s>>>(d, pos, w, o, n, chunks, k, T * k); \
+    else unpermute_kernel<F32, W, 8><<<grid, 256, 0, s>>>(d, pos, w, o, n, chunks, k, T * k);                         \
   } while (0)
   if (f32 && w) MOE_UNPERMUTE(true, true);
   else if (f32) MOE_UNPERMUTE(true, false);
